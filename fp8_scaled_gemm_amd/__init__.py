@@ -22,6 +22,14 @@ Functions keep the C names and argument order:
     fp8g_roof_mfma(blocks, iters), fp8g_roof_stream(src, dst, write_ratio)
                                             (roof probes for the benchmark)
 
+The attention block's operators (``include/fp8g_block.h``, module ``block``):
+
+    lora_add(base, x, A, B, scale, seg_start, seg_adapter)             -> out
+    qk_norm_rope(q, k, q_weight, k_weight, positions, cos_sin)         -> (q, k)
+    kv4_cache(pages, heads, page_size, dk, dv)                         -> KV4Cache
+    kv4_append(cache, k, v, slots), kv4_gather(cache, slots)           -> (k, v)
+    kv4_attention(q, cache, page_table, q_start, kv_len)               -> out
+
 E4M3 tensors are ``torch.float8_e4m3fn`` (OCP, the gfx950 format) and E5M2
 tensors ``torch.float8_e5m2``, or either as raw ``torch.uint8`` codes; the
 FNUZ variants of gfx942 are rejected.
@@ -35,6 +43,7 @@ __all__ = ["load", "fp8_quantize_rowwise", "fp8_quantize_ex", "mxfp8_quantize", 
            "fp8_gemm_scaled_noalloc", "mxfp8_gemm",
            "fp8_gemm_scaled_ex", "mxfp8_gemm_ex", "concat_mla_k", "fp8g_roof_mfma", "fp8g_roof_stream",
            "status_string",
+           "lora_add", "qk_norm_rope", "KV4Cache", "kv4_cache", "kv4_append", "kv4_gather", "kv4_attention",
            "Fp8gError", "LIB_PATH", "HEADER_PATH", "OUT_BF16", "OUT_F32", "FMT_E4M3", "FMT_E5M2"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -61,6 +70,15 @@ _SIGNATURES = {
     "concat_mla_k": [_VOIDP, _VOIDP, _VOIDP, _I64, _I64, _I64, ctypes.c_int, _VOIDP],
     "fp8g_gemm_schedule": [_I64, _I64, _I64, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int),
                            ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)],
+    "lora_add": [_VOIDP] * 7 + [_I64] * 6 + [ctypes.c_int, _VOIDP, _VOIDP, _I64, _VOIDP],
+    "lora_add_workspace": [_I64] * 6,
+    "qk_norm_rope": [_VOIDP, _I64, _VOIDP, _I64, ctypes.c_int] + [_I64] * 4 + [_VOIDP, _VOIDP, ctypes.c_float, _VOIDP,
+                     _I64, _VOIDP, _VOIDP, _I64, _I64, ctypes.c_int, _VOIDP, _I64, _VOIDP, _I64, _VOIDP],
+    "kv4_append": [_VOIDP, _I64, _VOIDP, _I64, ctypes.c_int] + [_I64] * 4 + [_VOIDP, _I64, _I64] + [_VOIDP] * 5,
+    "kv4_gather": [_VOIDP] * 4 + [_I64] * 5 + [_VOIDP, _I64, ctypes.c_int, _VOIDP, _VOIDP, _VOIDP],
+    "kv4_attention": [_VOIDP, _I64, _I64, _I64] + [_VOIDP] * 4 + [_I64] * 5 + [_VOIDP, _I64, _I64, _VOIDP, _VOIDP,
+                      ctypes.c_float, ctypes.c_int, _I64, _VOIDP, _VOIDP, _VOIDP, _I64, _VOIDP],
+    "kv4_attention_workspace": [_I64] * 9,
     "fp8g_roof_mfma": [_I64, _I64, _VOIDP, _VOIDP],
     "fp8g_roof_stream": [_VOIDP, _I64, _VOIDP, ctypes.c_int, ctypes.c_int, _VOIDP],
 }
@@ -88,7 +106,7 @@ def load():
         for name, args in _SIGNATURES.items():
             fn = getattr(lib, name)
             fn.argtypes = args
-            fn.restype = ctypes.c_int
+            fn.restype = ctypes.c_int64 if name.endswith("_workspace") else ctypes.c_int
         lib.fp8g_status_string.argtypes = [ctypes.c_int]
         lib.fp8g_status_string.restype = ctypes.c_char_p
         _lib = lib
@@ -399,3 +417,7 @@ def fp8g_roof_stream(src, dst, write_ratio, nontemporal_stores=0):
     _check(load().fp8g_roof_stream(_ptr(src), nbytes, _ptr(dst), int(write_ratio), int(nontemporal_stores),
                                    _stream()), "fp8g_roof_stream")
     return dst
+
+
+from .block import (KV4Cache, kv4_append, kv4_attention, kv4_cache, kv4_gather, lora_add,  # noqa: E402
+                    qk_norm_rope)

@@ -1,0 +1,464 @@
+// kv4_attention: attention over the paged MXFP4 cache.
+//
+// For a query row q (one query of one head) and the keys it sees,
+//   s_j = scale q . k_j,   out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+// in one pass over the keys with the running maximum m and sum l.
+//
+// A workgroup takes 16 rows -- the group of query heads that share a key head,
+// and neighbouring queries of a sequence where that leaves room -- and a chunk
+// of the sequence's keys.  Its four waves take 64 keys at a time each, on their
+// own (no barrier inside the loop), and join their maxima, sums and outputs at
+// the end.  Chunks, cut where few rows would leave the chip idle, leave their
+// partial results in the workspace; a second kernel joins them in order.
+//
+// Both products run transposed on v_mfma_f32_16x16x32_bf16, so that the result
+// layout of the first is the operand layout of the second and softmax weights
+// never leave their lane:
+//   S^T[key, row] = K Q^T,   O^T[dim, row] = V^T P^T
+// with the row as the matrix core's N: lane l holds row l % 16, g = l / 16.
+// * Keys: lane (m, g) is row m of the first operand.  It loads the 16 bytes of
+//   dims 32 g .. 32 g + 31 (one scale) of a key; the four 8-dim pieces are its
+//   operands of four products.  The order of dims along K is free as long as
+//   the queries follow it.
+// * In a step of 64 keys, product tile i (of 4) takes keys 4 m + i: the lane's
+//   four keys are neighbours (4 scales in one load), and the result holds, in
+//   lane group g, the 16 neighbouring keys 16 g + 4 r + i.
+// * Values: lane (m, g) loads dims 8 m .. 8 m + 7 of those 16 keys (4 bytes
+//   each, 16 scales in one load) and turns 8 keys x 8 dims into eight operands
+//   with one convert and one byte permute for each pair of elements.
+// E2M1 with a power-of-two scale is exact in bf16, one convert instruction for
+// two elements; only the softmax weights are rounded (to bf16).
+
+#include "device_common.h"
+#include "launch_block.h"
+#include "segments.h"
+
+#include <type_traits>
+
+namespace fp8g {
+
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+
+constexpr int ATTN_THREADS = 256;
+constexpr int ATTN_ROWS_LOG2 = 4, ATTN_ROWS = 1 << ATTN_ROWS_LOG2;
+constexpr int ATTN_STEP = 64;                      // keys of a wave's step
+constexpr int ATTN_CHUNK = 4 * ATTN_STEP;          // keys of a workgroup's step
+
+// n / d for n < 2^31 by a multiply: q = (mulhi(n, mul) + n) >> shift
+struct FastDiv {
+    uint32_t mul, shift;
+};
+static FastDiv fast_div(uint32_t d) {
+    FastDiv f;
+    f.shift = 0;
+    while ((1ull << f.shift) < d) f.shift++;
+    f.mul = (uint32_t)((((1ull << f.shift) - d) << 32) / d + 1);
+    return f;
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, FastDiv f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
+
+struct AttnPlan {
+    int ids, chunk, splits;
+    FastDiv page;
+};
+
+// Two E2M1 elements (byte SEL of codes) times 2^(scale - 127), as bf16.
+template <int SEL>
+__device__ __forceinline__ uint32_t fp4x2(uint32_t codes, float scale) {
+    return __builtin_bit_cast(uint32_t, (bf16x2v)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, SEL));
+}
+__device__ __forceinline__ bf16x8 fp4x8(uint32_t codes, float scale) {
+    const v4u r = {fp4x2<0>(codes, scale), fp4x2<1>(codes, scale), fp4x2<2>(codes, scale), fp4x2<3>(codes, scale)};
+    return __builtin_bit_cast(bf16x8, r);
+}
+// UE8M0 code in byte i of w, as a float
+template <int I>
+__device__ __forceinline__ float scale_of(uint32_t w) {
+    uint32_t r;
+    if constexpr (I == 3) r = (w >> 1) & 0x7F800000u;
+    else if constexpr (I == 2) r = (w << 7) & 0x7F800000u;
+    else if constexpr (I == 1) r = (w << 15) & 0x7F800000u;
+    else r = (w << 23) & 0x7F800000u;
+    return __builtin_bit_cast(float, r);
+}
+__device__ __forceinline__ float over_groups_max(float v) {
+    v = __builtin_fmaxf(v, __shfl_xor(v, 16, 64));
+    return __builtin_fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float over_groups_sum(float v) {
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+
+// What a block of rows sees.
+struct AttnBlock {
+    int seq, row0, rows, q0, queries, kv;
+};
+__device__ __forceinline__ bool attn_block(const Kv4AttnArgs& a, int group, int id, AttnBlock& b) {
+    auto start = [&](int i) { return min(max(a.q_start[i], 0), a.queries); };
+    const int found = find_block(start, a.batch, group, ATTN_ROWS_LOG2, id);
+    if (found == 0) return false;
+    b.seq = found - 1;
+    b.q0 = __builtin_amdgcn_readfirstlane(start(b.seq));
+    b.queries = __builtin_amdgcn_readfirstlane(start(b.seq + 1)) - b.q0;
+    b.row0 = (id - ((int)(((int64_t)b.q0 * group) >> ATTN_ROWS_LOG2) + b.seq)) * ATTN_ROWS;
+    b.rows = b.queries * group;
+    const int64_t room = (int64_t)a.max_pages * a.page_size;
+    b.kv = (int)min((int64_t)max(__builtin_amdgcn_readfirstlane(a.kv_len[b.seq]), 0), room);
+    return b.row0 < b.rows;
+}
+
+template <int DK, int DV>
+struct AttnStep {
+    // one step's codes and scales, as loaded
+    static constexpr int KW = DK / 32;    // dwords of a lane's piece of a key
+    uint32_t k[4][KW];
+    uint32_t ks[DK == 192 ? 2 : 1];
+    uint32_t v[16];
+    v4u vs;
+};
+
+template <int DK, int DV, bool SPLIT>
+__global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnArgs a, AttnPlan p) {
+    constexpr int KW = DK / 32, DT = DV / 16;   // products along the head dim; 16-dim tiles of the output
+    __shared__ float s_o[4][ATTN_ROWS][DV + 4];
+    __shared__ float s_m[4][ATTN_ROWS], s_l[4][ATTN_ROWS];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    const int group = a.q_heads / a.kv_heads;
+    const int split = blockIdx.x % p.splits, rest = blockIdx.x / p.splits;
+    const int h = rest % a.kv_heads, id = rest / a.kv_heads;
+    AttnBlock b;
+    if (!attn_block(a, group, id, b)) return;
+
+    // the lane's row, its query and the keys [lo, hi) that it sees
+    const int row = b.row0 + n;
+    const bool real = row < b.rows;
+    const int qi = min(row, b.rows - 1) / group;
+    const int head = h * group + min(row, b.rows - 1) % group;
+    const int first = b.kv - b.queries;      // position of query 0
+    auto top_of = [&](int q) { return a.causal ? max(0, min(b.kv, first + q + 1)) : b.kv; };
+    auto low_of = [&](int q) { return a.window ? max(0, first + q + 1 - a.window) : 0; };
+    const int hi = real ? top_of(qi) : 0, lo = low_of(qi);
+    const int q_first = b.row0 / group, q_last = (min(b.row0 + ATTN_ROWS, b.rows) - 1) / group;
+    const int all_lo = min(low_of(q_first), b.kv), all_hi = top_of(q_last);   // of the union
+    const int in_lo = low_of(q_last), in_hi = top_of(q_first);                // of the intersection
+    const int64_t begin = (all_lo & ~(ATTN_STEP - 1)) + (int64_t)split * p.chunk;
+    const int end = (int)min((int64_t)all_hi, begin + p.chunk);
+    const int64_t out_row = (int64_t)(b.q0 + qi) * a.q_heads + head;
+    float* const part_o = a.workspace;
+    float* const part_ml = a.workspace + (int64_t)a.queries * a.q_heads * p.splits * DV;
+    if (SPLIT && begin >= end) {
+        if (threadIdx.x < ATTN_ROWS && real) part_ml[(out_row * p.splits + split) * 2] = -INFINITY;
+        return;
+    }
+
+    // queries: dims in the order of the keys' pieces
+    bf16x8 q[KW];
+    {
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(b.q0 + qi) * a.q_stride + (int64_t)head * DK;
+#pragma unroll
+        for (int j = 0; j < KW; j++) {
+            const int d = DK == 64 ? 16 * g + 8 * j : (j < 4 ? 32 * g + 8 * j : 128 + 16 * g + 8 * (j - 4));
+            q[j] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const v4u*>(src + d));
+        }
+    }
+
+    const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
+    auto page_of = [&](int key, int& at) {   // at: the key's row in its page
+        const int slot = min((int)divide(key, p.page), a.max_pages - 1);
+        at = key - (int)divide(key, p.page) * a.page_size;
+        return min(max(table[slot], 0), a.pages - 1);
+    };
+    typedef AttnStep<DK, DV> Step;
+    auto load = [&](Step& s, int base) {
+        int at;
+        {
+            const int64_t ph = (int64_t)page_of(base + 4 * n, at) * a.kv_heads + h;
+            const uint8_t* c = a.k_codes + (ph * a.page_size + at) * (DK / 2);
+            const uint8_t* sc = a.k_scales + ph * (DK / 32) * a.page_size + at;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint8_t* r = c + i * (DK / 2);
+                if constexpr (DK == 64) {
+                    const v2u w = *reinterpret_cast<const v2u*>(r + 8 * g);
+                    s.k[i][0] = w[0], s.k[i][1] = w[1];
+                } else {
+                    const v4u w = *reinterpret_cast<const v4u*>(r + 16 * g);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) s.k[i][j] = w[j];
+                    if constexpr (DK == 192) {
+                        const v2u x = *reinterpret_cast<const v2u*>(r + 64 + 8 * g);
+                        s.k[i][4] = x[0], s.k[i][5] = x[1];
+                    }
+                }
+            }
+            s.ks[0] = *reinterpret_cast<const uint32_t*>(sc + (DK == 64 ? g >> 1 : g) * a.page_size);
+            if constexpr (DK == 192) s.ks[1] = *reinterpret_cast<const uint32_t*>(sc + (4 + (g >> 1)) * a.page_size);
+        }
+        const int64_t ph = (int64_t)page_of(base + 16 * g, at) * a.kv_heads + h;
+        const uint8_t* c = a.v_codes + (ph * a.page_size + at) * (DV / 2);
+        const uint8_t* sc = a.v_scales + ph * (DV / 32) * a.page_size + at;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            if constexpr (DV == 64)
+                s.v[i] = *reinterpret_cast<const uint16_t*>(c + i * (DV / 2) + 2 * n);
+            else
+                s.v[i] = *reinterpret_cast<const uint32_t*>(c + i * (DV / 2) + 4 * n);
+        }
+        s.vs = *reinterpret_cast<const v4u*>(sc + (DV == 64 ? n >> 3 : n >> 2) * a.page_size);
+    };
+
+    v4f o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; d++) o[d] = v4f{0, 0, 0, 0};
+    float m = -INFINITY, l = 0.0f;
+    const float c2 = a.scale * 1.4426950408889634f;   // scores in powers of two
+
+    Step s;
+    int base = (int)begin + ATTN_STEP * wave;
+    if (base < end) load(s, base);
+    for (; base < end; base += ATTN_CHUNK) {
+        Step next;
+        if (base + ATTN_CHUNK < end) load(next, base + ATTN_CHUNK);
+        // scores
+        v4f acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) acc[i] = v4f{0, 0, 0, 0};
+        const float k0[4] = {scale_of<0>(s.ks[0]), scale_of<1>(s.ks[0]), scale_of<2>(s.ks[0]), scale_of<3>(s.ks[0])};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+#pragma unroll
+            for (int j = 0; j < (KW < 4 ? KW : 4); j++)
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4x8(s.k[i][j], k0[i]), q[j], acc[i], 0, 0, 0);
+        }
+        if constexpr (DK == 192) {
+            const float k1[4] = {scale_of<0>(s.ks[1]), scale_of<1>(s.ks[1]), scale_of<2>(s.ks[1]), scale_of<3>(s.ks[1])};
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+#pragma unroll
+                for (int j = 4; j < 6; j++)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4x8(s.k[i][j], k1[i]), q[j], acc[i], 0, 0, 0);
+            }
+        }
+        // acc[i][r]: key base + 16 g + 4 r + i of row n
+        float w[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) w[i][r] = acc[i][r] * c2;
+        if (base + ATTN_STEP > in_hi || base < in_lo || base + ATTN_STEP > end) {
+            // a step that some row sees only a part of.  Values outside the
+            // block's keys get a scale of 2^-127: whatever their bytes hold is
+            // then finite, and a weight of zero removes it.
+            const int top = min(hi, end);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    const int key = base + 16 * g + 4 * r + i;
+                    if (key >= top || key < lo) w[i][r] = -INFINITY;
+                }
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                uint32_t keep = 0;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int key = base + 16 * g + 4 * r + i;
+                    if (key < all_hi && key >= all_lo) keep |= 0xFFu << (8 * i);
+                }
+                s.vs[r] &= keep;
+            }
+        }
+        float top = w[0][0];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) top = __builtin_fmaxf(top, w[i][r]);
+        const float m_new = __builtin_fmaxf(m, over_groups_max(top));
+        const float m_use = m_new == -INFINITY ? 0.0f : m_new;   // a row that has seen nothing yet
+        const float alpha = __builtin_amdgcn_exp2f(m - m_use);
+        m = m_new;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                w[i][r] = __builtin_amdgcn_exp2f(w[i][r] - m_use);
+                sum += w[i][r];
+            }
+        l = l * alpha + sum;
+#pragma unroll
+        for (int d = 0; d < DT; d++) o[d] *= alpha;
+        // values: 8 keys (16 g + 8 u ..) at a time
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const v4u pw = {bf16x2_bits(w[0][2 * u], w[1][2 * u]), bf16x2_bits(w[2][2 * u], w[3][2 * u]),
+                            bf16x2_bits(w[0][2 * u + 1], w[1][2 * u + 1]), bf16x2_bits(w[2][2 * u + 1], w[3][2 * u + 1])};
+            const bf16x8 pf = __builtin_bit_cast(bf16x8, pw);
+            float sc[8];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const uint32_t q4 = s.vs[2 * u + e];
+                sc[4 * e + 0] = scale_of<0>(q4), sc[4 * e + 1] = scale_of<1>(q4);
+                sc[4 * e + 2] = scale_of<2>(q4), sc[4 * e + 3] = scale_of<3>(q4);
+            }
+            auto pair = [&](auto sel) {
+                constexpr int SEL = decltype(sel)::value;
+                uint32_t x[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) x[j] = fp4x2<SEL>(s.v[8 * u + j], sc[j]);
+                v4u even, odd;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    even[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x05040100u);
+                    odd[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x07060302u);
+                }
+                o[2 * SEL] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), pf, o[2 * SEL], 0, 0, 0);
+                o[2 * SEL + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), pf, o[2 * SEL + 1], 0, 0, 0);
+            };
+            pair(std::integral_constant<int, 0>{});
+            pair(std::integral_constant<int, 1>{});
+            if constexpr (DV == 128) {
+                pair(std::integral_constant<int, 2>{});
+                pair(std::integral_constant<int, 3>{});
+            }
+        }
+        s = next;
+    }
+    // join the waves: o[d][r] is dim DT (4 g + r) + d of row n
+    l = over_groups_sum(l);
+#pragma unroll
+    for (int r = 0; r < 4; r++)
+#pragma unroll
+        for (int d = 0; d < DT; d++) s_o[wave][n][DT * (4 * g + r) + d] = o[d][r];
+    if (g == 0) s_m[wave][n] = m, s_l[wave][n] = l;
+    __syncthreads();
+    const int tr = threadIdx.x >> 4, tl = threadIdx.x & 15;     // 16 threads a row
+    const int orow = b.row0 + tr;
+    if (orow >= b.rows) return;
+    float mm = s_m[0][tr];
+#pragma unroll
+    for (int w = 1; w < 4; w++) mm = __builtin_fmaxf(mm, s_m[w][tr]);
+    const float mu = mm == -INFINITY ? 0.0f : mm;
+    float fac[4], ll = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; w++) {
+        fac[w] = __builtin_amdgcn_exp2f(s_m[w][tr] - mu);
+        ll += s_l[w][tr] * fac[w];
+    }
+    const int64_t target = (int64_t)(b.q0 + orow / group) * a.q_heads + h * group + orow % group;
+    float r[DT];
+#pragma unroll
+    for (int d = 0; d < DT; d++) {
+        float x = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; w++) x += s_o[w][tr][DT * tl + d] * fac[w];
+        r[d] = x;
+    }
+    if constexpr (SPLIT) {
+        float* dst = part_o + (target * p.splits + split) * DV + DT * tl;
+#pragma unroll
+        for (int d = 0; d < DT; d += 4) *reinterpret_cast<v4f*>(dst + d) = v4f{r[d], r[d + 1], r[d + 2], r[d + 3]};
+        if (tl == 0) {
+            part_ml[(target * p.splits + split) * 2] = mm;
+            part_ml[(target * p.splits + split) * 2 + 1] = ll;
+        }
+    } else {
+        const float inv = ll > 0.0f ? 1.0f / ll : (mm == -INFINITY ? 0.0f : 1.0f / ll);
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + target * DV + DT * tl;
+#pragma unroll
+        for (int d = 0; d < DT; d += 4)
+            *reinterpret_cast<v2u*>(dst + d) = v2u{bf16x2_bits(r[d] * inv, r[d + 1] * inv), bf16x2_bits(r[d + 2] * inv, r[d + 3] * inv)};
+        if (a.lse && tl == 0) a.lse[target] = mm == -INFINITY ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f;
+    }
+}
+
+// Joins the chunks of every row, in order: DV / 4 lanes a row.
+template <int DV>
+__global__ __launch_bounds__(ATTN_THREADS) void kv4_attention_join_kernel(Kv4AttnArgs a, AttnPlan p) {
+    constexpr int LANES = DV / 4, ROWS = ATTN_THREADS / LANES;
+    const int64_t rows = (int64_t)a.queries * a.q_heads;
+    const int64_t row = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
+    const int lane = threadIdx.x % LANES;
+    if (row >= rows) return;
+    const int query = (int)(row / a.q_heads);
+    if (query < a.q_start[0] || query >= a.q_start[a.batch]) return;   // of no sequence
+    const float* part_o = a.workspace + row * p.splits * DV + 4 * lane;
+    const float* part_ml = a.workspace + rows * p.splits * DV + row * p.splits * 2;
+    float m = -INFINITY;
+    for (int s = 0; s < p.splits; s++) m = __builtin_fmaxf(m, part_ml[2 * s]);
+    const float mu = m == -INFINITY ? 0.0f : m;
+    v4f o = {0, 0, 0, 0};
+    float l = 0.0f;
+    for (int s = 0; s < p.splits; s++) {
+        const float ms = part_ml[2 * s];
+        if (ms == -INFINITY) continue;      // an empty chunk has written no more than this
+        const float f = __builtin_amdgcn_exp2f(ms - mu);
+        l += part_ml[2 * s + 1] * f;
+        o += *reinterpret_cast<const v4f*>(part_o + (int64_t)s * DV) * f;
+    }
+    const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+    *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.out) + row * DV + 4 * lane) =
+        v2u{bf16x2_bits(o[0] * inv, o[1] * inv), bf16x2_bits(o[2] * inv, o[3] * inv)};
+    if (a.lse && lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+}
+
+static AttnPlan attn_plan(const Kv4AttnArgs& a) {
+    AttnPlan p;
+    const int group = a.q_heads / a.kv_heads;
+    p.ids = (int)((int64_t)a.queries * group / ATTN_ROWS) + a.batch;
+    p.page = fast_div((uint32_t)a.page_size);
+    int64_t keys = (int64_t)a.max_pages * a.page_size;
+    if (a.window && keys > (int64_t)a.window + ATTN_ROWS + ATTN_STEP) keys = (int64_t)a.window + ATTN_ROWS + ATTN_STEP;
+    // blocks that certainly have rows
+    int64_t blocks = ((int64_t)a.queries * group + ATTN_ROWS - 1) / ATTN_ROWS;
+    const int some = a.batch < a.queries ? a.batch : a.queries;
+    if (blocks < some) blocks = some;
+    blocks *= a.kv_heads;
+    int64_t want = blocks >= 2048 ? 1 : 2048 / blocks;
+    const int64_t most = ((int64_t)1 << 30) / ((int64_t)p.ids * a.kv_heads);   // keeps the grid's size an int
+    if (want > most) want = most < 1 ? 1 : most;
+    int64_t chunk = ((keys + want - 1) / want + ATTN_CHUNK - 1) / ATTN_CHUNK * ATTN_CHUNK;
+    if (chunk < ATTN_CHUNK) chunk = ATTN_CHUNK;
+    p.chunk = (int)chunk;
+    p.splits = (int)((keys + chunk - 1) / chunk);
+    if (p.splits < 1) p.splits = 1;
+    return p;
+}
+
+int64_t kv4_attention_bytes(const Kv4AttnArgs& a) {
+    if (a.queries == 0 || a.batch == 0 || a.q_heads == 0) return 0;
+    const AttnPlan p = attn_plan(a);
+    return p.splits > 1 ? (int64_t)a.queries * a.q_heads * p.splits * (a.dv + 2) * 4 : 0;
+}
+
+template <int DK, int DV>
+static hipError_t launch_dims(const Kv4AttnArgs& a, hipStream_t stream) {
+    const AttnPlan p = attn_plan(a);
+    const dim3 grid((unsigned)((int64_t)p.ids * a.kv_heads * p.splits)), block(ATTN_THREADS);
+    if (p.splits == 1) {
+        kv4_attention_kernel<DK, DV, false><<<grid, block, 0, stream>>>(a, p);
+        return hipGetLastError();
+    }
+    kv4_attention_kernel<DK, DV, true><<<grid, block, 0, stream>>>(a, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    constexpr int ROWS = ATTN_THREADS / (DV / 4);
+    const int64_t rows = (int64_t)a.queries * a.q_heads;
+    kv4_attention_join_kernel<DV><<<dim3((unsigned)((rows + ROWS - 1) / ROWS)), block, 0, stream>>>(a, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_kv4_attention(const Kv4AttnArgs& in, hipStream_t stream) {
+    Kv4AttnArgs a = in;
+    if (a.pages == 0) a.max_pages = 0;   // no page to read: no sequence has keys
+    if (a.dk == 64) return launch_dims<64, 64>(a, stream);
+    if (a.dk == 128) return launch_dims<128, 128>(a, stream);
+    return launch_dims<192, 128>(a, stream);
+}
+
+}  // namespace fp8g
