@@ -3,17 +3,21 @@
 //
 //   y = x * rsqrt(mean x^2 + eps) * w;   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s)
 //
-// HBM-bound: every element is read and written once.  One head row is held by
-// L lanes (a power of two, 16 bytes a lane), so the sum of squares needs only
-// log2(L) lane exchanges and no shared memory.  A slot of L lanes stays with
-// one token and walks over its heads: the token's cosines and sines (per axis
-// gathered, 2 loads a pair) then stay in registers for all of them.
+// With r = 1 / sqrt(mean x^2 + eps) and p(e) the other element of e's pair,
+//   out_e = r * (x_e C_e + x_p(e) S_e),   C_e = w_e c,  S_e = -/+ w_p(e) s
+// (C_e = w_e, S_e = 0 behind rotary_dim), so a row needs two products an
+// element once its token's C and S are there.  A workgroup works them out once
+// for its tokens, for queries and for keys, in LDS, one element a thread: the
+// look-ups (axis -> position -> cosine, sine) are a chain of three loads that
+// would otherwise stand in front of every row.
 //
-// Where a pair is (i, i + rotary_dim / 2) the lane that holds i needs its
-// partner's 16 bytes too; it loads them a second time (they hit the cache that
-// the row just passed through) instead of exchanging them over the lanes.
-// Both loads of a row come before its store in the same wave, so a row may be
-// written in place.
+// HBM-bound: every element is read and written once.  A row is held by L lanes
+// (a power of two, 16 bytes a lane), so its sum of squares takes log2(L) lane
+// exchanges.  Where a pair is (i, i + rotary_dim / 2), a lane loads its
+// partner's 16 bytes a second time (they are in the cache that the row just
+// passed through) instead of exchanging them over the lanes.  The loads of a
+// row come before its store in the same wave, and a wave holds whole rows, so
+// a row may be written in place.
 
 #include "device_common.h"
 #include "launch_block.h"
@@ -24,6 +28,8 @@ typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
 constexpr int QK_THREADS = 256;
+constexpr int QK_AHEAD = 4;          // rows of a slot in flight
+constexpr int QK_LDS = 16384;        // C and S of a workgroup's tokens: 16 bytes an element of head_dim
 
 template <bool F32>
 struct QkRow {
@@ -61,94 +67,114 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-template <bool F32, int L>
-__global__ __launch_bounds__(QK_THREADS) void qk_norm_rope_kernel(QkArgs a, int tokens_per_wg, int row_blocks) {
+// How a launch is cut: `tokens` of a workgroup, all of their rows or, with row
+// blocks, `part` rows of its one token.
+struct QkPlan {
+    int tokens, row_blocks, part;
+};
+
+template <bool F32, int L, bool INTERLEAVED>
+__global__ __launch_bounds__(QK_THREADS) void qk_norm_rope_kernel(QkArgs a, QkPlan p) {
     using Row = QkRow<F32>;
     constexpr int VEC = Row::VEC, SLOTS = QK_THREADS / L;
+    constexpr int64_t ESZ = F32 ? 4 : 2;
+    extern __shared__ float coef[];            // [token][q: C, S; k: C, S][head_dim]
+    const int D = a.head_dim, half = a.rotary_dim >> 1;
+    const int tile = blockIdx.x / p.row_blocks, block = blockIdx.x - tile * p.row_blocks;
+    const int64_t t0 = (int64_t)tile * p.tokens;
+    const int tokens = (int)min((int64_t)p.tokens, a.tokens - t0);
     const int rows = a.q_heads + a.k_heads;
+    const int first = block * p.part, last = min(rows, first + p.part);   // rows of each token
     const int slot = threadIdx.x / L, lane = threadIdx.x % L;
-    // a slot's token and first row; with several row blocks a token's rows are
-    // dealt out over them
-    const int tile = blockIdx.x / row_blocks, part = blockIdx.x - tile * row_blocks;
-    int64_t t = tile;
-    int row = part * SLOTS + slot, step = row_blocks * SLOTS;
-    if (tokens_per_wg > 1) {
-        const int sub = slot / rows;
-        t = (int64_t)tile * tokens_per_wg + sub;
-        row = sub < tokens_per_wg ? slot - sub * rows : rows;
-        step = rows;
-    }
-    if (t >= a.tokens) row = rows;
+    const int total = tokens * (last - first);
     // the lane's 16 bytes of a row; lanes past the row's end repeat the last
     // ones and count for nothing
-    const int chunks = a.head_dim / VEC;
+    const int chunks = D / VEC;
     const bool live = lane < chunks;
     const int e0 = (live ? lane : chunks - 1) * VEC;
-    const int half = a.rotary_dim >> 1;
-    const bool turns = e0 < a.rotary_dim;
-    const bool second = turns && !a.interleaved && e0 >= half;
-    const int partner = a.interleaved || !turns ? e0 : (second ? e0 - half : e0 + half);
-    // cosines and sines of the lane's pairs; sines with the sign of the term
-    // that the partner adds.  Interleaved: VEC / 2 pairs, each twice.
-    float c[VEC], s[VEC];
+    const int partner = INTERLEAVED || e0 >= a.rotary_dim ? e0 : (e0 >= half ? e0 - half : e0 + half);
+
+    // a row's place, and the next one of the slot
+    const int span = last - first, step_token = SLOTS / span, step_row = SLOTS % span;
+    int token = slot / span, row = first + slot % span;
+    auto next = [&] {
+        row += step_row, token += step_token;
+        if (row >= last) row -= span, token++;
+    };
+    v4u x[QK_AHEAD], y[QK_AHEAD];
+    char* dst[QK_AHEAD];
+    const float* cs[QK_AHEAD];
+    int f = slot;
+    auto load = [&] {
+        int g = f;
 #pragma unroll
-    for (int j = 0; j < VEC; j++) c[j] = 1.0f, s[j] = 0.0f;
-    if (turns && row < rows) {
-        const int i0 = a.interleaved ? e0 >> 1 : (second ? e0 - half : e0);
-        if (a.axes == 1) {
-            const int p = min(max(a.positions[t], 0), a.max_position - 1);
-            const float* table = a.cos_sin + (int64_t)p * a.rotary_dim;
-#pragma unroll
-            for (int j = 0; j < VEC; j++) {
-                const int i = i0 + (a.interleaved ? j >> 1 : j);
-                c[j] = table[i];
-                s[j] = table[half + i];
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < VEC; j++) {
-                const int i = i0 + (a.interleaved ? j >> 1 : j);
-                const int ax = min(max(a.axis[i], 0), a.axes - 1);
-                const int p = min(max(a.positions[(int64_t)ax * a.tokens + t], 0), a.max_position - 1);
-                const float* table = a.cos_sin + (int64_t)p * a.rotary_dim;
-                c[j] = table[i];
-                s[j] = table[half + i];
+        for (int u = 0; u < QK_AHEAD; u++, g += SLOTS) {
+            if (g < total) {
+                const bool is_k = row >= a.q_heads;
+                const int h = is_k ? row - a.q_heads : row;
+                const int64_t t = t0 + token;
+                const char* src = static_cast<const char*>(is_k ? a.k : a.q) +
+                                  (t * (is_k ? a.k_stride : a.q_stride) + (int64_t)h * D) * ESZ;
+                dst[u] = static_cast<char*>(is_k ? a.k_out : a.q_out) +
+                         (t * (is_k ? a.k_out_stride : a.q_out_stride) + (int64_t)h * D) * ESZ + e0 * ESZ;
+                cs[u] = coef + (token * 4 + (is_k ? 2 : 0)) * D + e0;
+                x[u] = *reinterpret_cast<const v4u*>(src + e0 * ESZ);
+                if constexpr (!INTERLEAVED) y[u] = *reinterpret_cast<const v4u*>(src + partner * ESZ);
+                next();
             }
         }
-#pragma unroll
-        for (int j = 0; j < VEC; j++)
-            if (a.interleaved ? !(j & 1) : !second) s[j] = -s[j];
+    };
+    load();      // the first rows travel while C and S are worked out
+
+    for (int i = threadIdx.x; i < tokens * D; i += QK_THREADS) {
+        const int tok = i / D, e = i - tok * D;
+        float c = 1.0f, s = 0.0f;
+        int other = e;
+        if (e < a.rotary_dim) {
+            const bool second = INTERLEAVED ? (e & 1) : e >= half;
+            const int pair = INTERLEAVED ? e >> 1 : (second ? e - half : e);
+            other = INTERLEAVED ? e ^ 1 : (second ? e - half : e + half);
+            const int ax = a.axes > 1 ? min(max(a.axis[pair], 0), a.axes - 1) : 0;
+            const int pos = min(max(a.positions[(int64_t)ax * a.tokens + t0 + tok], 0), a.max_position - 1);
+            const float* table = a.cos_sin + (int64_t)pos * a.rotary_dim + pair;
+            c = table[0];
+            s = second ? table[half] : -table[half];
+        }
+        float* dc = coef + tok * 4 * D + e;
+        dc[0] = (a.q_weight ? a.q_weight[e] : 1.0f) * c;
+        dc[D] = (a.q_weight ? a.q_weight[other] : 1.0f) * s;
+        dc[2 * D] = (a.k_weight ? a.k_weight[e] : 1.0f) * c;
+        dc[3 * D] = (a.k_weight ? a.k_weight[other] : 1.0f) * s;
     }
-    const float inv_dim = 1.0f / (float)a.head_dim;
-    for (; row < rows; row += step) {
-        const bool is_k = row >= a.q_heads;
-        const int h = is_k ? row - a.q_heads : row;
-        const int64_t esz = F32 ? 4 : 2;
-        const char* src = static_cast<const char*>(is_k ? a.k : a.q) +
-                          (t * (is_k ? a.k_stride : a.q_stride) + (int64_t)h * a.head_dim) * esz;
-        char* dst = static_cast<char*>(is_k ? a.k_out : a.q_out) +
-                    (t * (is_k ? a.k_out_stride : a.q_out_stride) + (int64_t)h * a.head_dim) * esz;
-        const float* w = is_k ? a.k_weight : a.q_weight;
-        float x[VEC], y[VEC], wx[VEC], wy[VEC];
-        Row::unpack(*reinterpret_cast<const v4u*>(src + e0 * esz), x);
-        Row::unpack(*reinterpret_cast<const v4u*>(src + partner * esz), y);
+    __syncthreads();
+
+    const float inv_dim = 1.0f / (float)D;
+    for (; f < total; f += QK_AHEAD * SLOTS) {
+        v4u xs[QK_AHEAD], ys[QK_AHEAD];
+        char* ds[QK_AHEAD];
+        const float* cc[QK_AHEAD];
 #pragma unroll
-        for (int j = 0; j < VEC; j++) {
-            wx[j] = w ? w[e0 + j] : 1.0f;
-            wy[j] = w ? w[partner + j] : 1.0f;
+        for (int u = 0; u < QK_AHEAD; u++) xs[u] = x[u], ys[u] = y[u], ds[u] = dst[u], cc[u] = cs[u];
+        const int now = f;
+        f += QK_AHEAD * SLOTS;
+        load();
+        f = now;
+#pragma unroll
+        for (int u = 0; u < QK_AHEAD; u++) {
+            if (now + u * SLOTS >= total) continue;     // a slot's lanes stay together
+            float v[VEC], w[VEC], o[VEC];
+            Row::unpack(xs[u], v);
+            if constexpr (!INTERLEAVED) Row::unpack(ys[u], w);
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < VEC; j++) sum += v[j] * v[j];
+            sum = group_sum<L>(live ? sum : 0.0f);
+            const float r = 1.0f / __builtin_sqrtf(sum * inv_dim + a.eps);
+#pragma unroll
+            for (int j = 0; j < VEC; j++)
+                o[j] = r * (v[j] * cc[u][j] + (INTERLEAVED ? v[j ^ 1] : w[j]) * cc[u][D + j]);
+            if (live) *reinterpret_cast<v4u*>(ds[u]) = Row::pack(o);
         }
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VEC; j++) sum += x[j] * x[j];
-        sum = group_sum<L>(live ? sum : 0.0f);
-        const float r = 1.0f / __builtin_sqrtf(sum * inv_dim + a.eps);
-        float o[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; j++) {
-            const int jp = a.interleaved ? j ^ 1 : j;
-            o[j] = x[j] * r * wx[j] * c[j] + (a.interleaved ? x[jp] * r * wx[jp] : y[j] * r * wy[j]) * s[j];
-        }
-        if (live) *reinterpret_cast<v4u*>(dst + e0 * esz) = Row::pack(o);
     }
 }
 
@@ -156,17 +182,28 @@ template <bool F32, int L>
 static hipError_t launch_l(const QkArgs& a, hipStream_t stream) {
     constexpr int SLOTS = QK_THREADS / L;
     const int rows = a.q_heads + a.k_heads;
-    int tokens_per_wg = 1, row_blocks = 1;
-    if (rows <= SLOTS) {
-        tokens_per_wg = SLOTS / rows;
+    QkPlan p;
+    p.part = rows, p.row_blocks = 1;
+    const int64_t passes = ((int64_t)a.tokens * rows + SLOTS - 1) / SLOTS;
+    if (passes <= 2048) {
+        // few rows: one pass of them a workgroup, over the whole chip
+        p.tokens = rows < SLOTS ? SLOTS / rows : 1;
+        p.row_blocks = (rows + SLOTS - 1) / SLOTS;
+        p.part = (rows + p.row_blocks - 1) / p.row_blocks;
     } else {
-        // few tokens: a row for every slot; many: up to 4 rows a slot, so that
-        // the token's cosines and sines serve them all
-        const int most = (rows + SLOTS - 1) / SLOTS;
-        row_blocks = a.tokens >= 2048 ? (most + 3) / 4 : most;
+        // many: about 16 passes a workgroup, at least 2048 workgroups
+        int64_t each = passes / 2048;
+        each = each > 16 ? 16 : each;
+        p.tokens = (int)((each * SLOTS + rows - 1) / rows);
     }
-    const int64_t grid = ((int64_t)a.tokens + tokens_per_wg - 1) / tokens_per_wg * row_blocks;
-    qk_norm_rope_kernel<F32, L><<<dim3((unsigned)grid), dim3(QK_THREADS), 0, stream>>>(a, tokens_per_wg, row_blocks);
+    const int most = QK_LDS / (a.head_dim * 16);
+    if (p.tokens > most) p.tokens = most;
+    const int64_t grid = ((int64_t)a.tokens + p.tokens - 1) / p.tokens * p.row_blocks;
+    const unsigned lds = p.tokens * a.head_dim * 16;
+    if (a.interleaved)
+        qk_norm_rope_kernel<F32, L, true><<<dim3((unsigned)grid), dim3(QK_THREADS), lds, stream>>>(a, p);
+    else
+        qk_norm_rope_kernel<F32, L, false><<<dim3((unsigned)grid), dim3(QK_THREADS), lds, stream>>>(a, p);
     return hipGetLastError();
 }
 
