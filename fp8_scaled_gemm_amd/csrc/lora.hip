@@ -29,199 +29,303 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int LORA_THREADS = 256;
-constexpr int LORA_BLOCK_LOG2 = 4, LORA_BLOCK = 1 << LORA_BLOCK_LOG2;   // tokens a block
 constexpr int LORA_MAX_SPLITS = 16;
 
-// The block's tokens [t0, t1) and its adapter (-1: none).  Tokens in front of
-// the first segment and behind the last are segments without an adapter.
+// The block's tokens [t0, t1), at most 16 TT, and its adapter (-1: none).
+// Tokens in front of the first segment and behind the last are segments
+// without an adapter.
 struct LoraBlock {
     int t0, t1, adapter;
 };
+template <int TT>
 __device__ __forceinline__ LoraBlock lora_block(const LoraArgs& a, int id) {
+    constexpr int LOG2 = TT == 4 ? 6 : TT == 2 ? 5 : 4;
     const int S = a.segments;
     auto start = [&](int v) {   // starts of the S + 2 segments, and the end
         if (v <= 0) return 0;
         if (v > S + 1) return a.tokens;
         return min(max(a.seg_start[v - 1], 0), a.tokens);
     };
-    const int v = find_block(start, S + 2, 1, LORA_BLOCK_LOG2, id) - 1;
+    const int v = find_block(start, S + 2, 1, LOG2, id) - 1;
     const int begin = __builtin_amdgcn_readfirstlane(start(v)), end = __builtin_amdgcn_readfirstlane(start(v + 1));
     LoraBlock b;
-    b.t0 = begin + (id - ((begin >> LORA_BLOCK_LOG2) + v)) * LORA_BLOCK;
-    b.t1 = min(end, b.t0 + LORA_BLOCK);
+    b.t0 = begin + (id - ((begin >> LOG2) + v)) * (16 * TT);
+    b.t1 = min(end, b.t0 + 16 * TT);
     b.adapter = v >= 1 && v <= S ? __builtin_amdgcn_readfirstlane(a.seg_adapter[v - 1]) : -1;
     if (b.adapter >= a.adapters) b.adapter = -1;
     return b;
 }
 
-__device__ __forceinline__ bf16x8 load8(const uint16_t* p, bool live) {
-    const v4u zero = {0, 0, 0, 0};
-    return __builtin_bit_cast(bf16x8, live ? *reinterpret_cast<const v4u*>(p) : zero);
-}
-
-template <int RT>   // 16-row tiles of the rank
+template <int RT, int TT>   // 16-row tiles of the rank, 16-token tiles of a block
 __global__ __launch_bounds__(LORA_THREADS) void lora_shrink_kernel(LoraArgs a, int splits, int k_split) {
-    __shared__ float part[4][RT][16 * 16];
+    __shared__ v4f part[2][RT * TT][64];
     const int id = blockIdx.x / splits, split = blockIdx.x - id * splits;
-    const LoraBlock b = lora_block(a, id);
+    const LoraBlock b = lora_block<TT>(a, id);
     if (b.t0 >= b.t1 || b.adapter < 0) return;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
     const int k0 = split * k_split, k1 = min(a.k, k0 + k_split);
-    const uint16_t* x = static_cast<const uint16_t*>(a.x) + (int64_t)min(b.t0 + m, b.t1 - 1) * a.k;
     const uint16_t* A = static_cast<const uint16_t*>(a.A) + (int64_t)b.adapter * a.rank * a.k;
-    const uint16_t* rows[RT];
-    v4f acc[RT];
+    const uint16_t *rows[RT], *xs[TT];
+    v4f acc[RT][TT];
+#pragma unroll
+    for (int t = 0; t < TT; t++)
+        xs[t] = static_cast<const uint16_t*>(a.x) + (int64_t)min(b.t0 + 16 * t + m, b.t1 - 1) * a.k + k0 + 8 * g;
 #pragma unroll
     for (int r = 0; r < RT; r++) {
-        rows[r] = A + (int64_t)min(16 * r + m, a.rank - 1) * a.k;
-        acc[r] = v4f{0, 0, 0, 0};
+        rows[r] = A + (int64_t)min(16 * r + m, a.rank - 1) * a.k + k0 + 8 * g;
+#pragma unroll
+        for (int t = 0; t < TT; t++) acc[r][t] = v4f{0, 0, 0, 0};
     }
-#pragma unroll 4
-    for (int k = k0 + 32 * wave; k < k1; k += 128) {
-        const int at = k + 8 * g;
-        const bool live = at < k1;
-        const bf16x8 xf = load8(x + at, live);
+    // The waves take turns over blocks of 32 of k, AHEAD of them at a time and
+    // the next ones already on their way.
+    constexpr int AHEAD = RT + TT <= 2 ? 8 : RT + TT <= 6 ? 3 : RT + TT <= 8 ? 2 : 1;
+    struct Batch {
+        v4u w[AHEAD][RT], x[AHEAD][TT];
+    };
+    const int full = (k1 - k0) >> 5;
+    auto load = [&](Batch& s, int i) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++)
+            if (i + 4 * u < full) {
+                const int at = 32 * (i + 4 * u);
+#pragma unroll
+                for (int t = 0; t < TT; t++) s.x[u][t] = *reinterpret_cast<const v4u*>(xs[t] + at);
+#pragma unroll
+                for (int r = 0; r < RT; r++) s.w[u][r] = *reinterpret_cast<const v4u*>(rows[r] + at);
+            }
+    };
+    auto multiply = [&](const v4u* w, const v4u* x) {
 #pragma unroll
         for (int r = 0; r < RT; r++)
-            acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(load8(rows[r] + at, live), xf, acc[r], 0, 0, 0);
-    }
-    // lane: token m, ranks 16 r + 4 g + i; the four waves' sums meet in LDS
 #pragma unroll
-    for (int r = 0; r < RT; r++) *reinterpret_cast<v4f*>(&part[wave][r][m * 16 + 4 * g]) = acc[r];
+            for (int t = 0; t < TT; t++)
+                acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[r]),
+                                                                    __builtin_bit_cast(bf16x8, x[t]), acc[r][t], 0, 0, 0);
+    };
+    Batch now;
+    load(now, wave);
+    for (int i = wave; i < full; i += 4 * AHEAD) {
+        Batch next;
+        load(next, i + 4 * AHEAD);
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++)
+            if (i + 4 * u < full) multiply(now.w[u], now.x[u]);
+        now = next;
+    }
+    if (wave == (full & 3) && ((k1 - k0) & 31)) {       // what is left of k, a multiple of 8
+        const int at = 32 * full;
+        const bool live = at + 8 * g < k1 - k0;
+        v4u w[RT], x[TT];
+#pragma unroll
+        for (int t = 0; t < TT; t++) x[t] = live ? *reinterpret_cast<const v4u*>(xs[t] + at) : v4u{0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < RT; r++) w[r] = live ? *reinterpret_cast<const v4u*>(rows[r] + at) : v4u{0, 0, 0, 0};
+        multiply(w, x);
+    }
+    // lane: token m, ranks 16 r + 4 g + i.  The waves' sums meet in LDS: 0 + 2
+    // and 1 + 3, then both.
+    auto put = [&](int at) {
+#pragma unroll
+        for (int r = 0; r < RT; r++)
+#pragma unroll
+            for (int t = 0; t < TT; t++) part[at][r * TT + t][lane] = acc[r][t];
+    };
+    auto add = [&](int at) {
+#pragma unroll
+        for (int r = 0; r < RT; r++)
+#pragma unroll
+            for (int t = 0; t < TT; t++) acc[r][t] += part[at][r * TT + t][lane];
+    };
+    if (wave >= 2) put(wave - 2);
     __syncthreads();
-    for (int i = threadIdx.x; i < RT * 256; i += LORA_THREADS) {
-        const int r = i >> 8, tok = (i >> 4) & 15, rank = 16 * r + (i & 15);
-        const float sum = (part[0][r][i & 255] + part[1][r][i & 255]) + (part[2][r][i & 255] + part[3][r][i & 255]);
-        if (rank < a.rank && b.t0 + tok < b.t1)
-            a.workspace[((int64_t)split * a.tokens + b.t0 + tok) * a.rank + rank] = sum;
+    if (wave < 2) add(wave);
+    if (wave == 1) put(1);      // its own slice, read before
+    __syncthreads();
+    if (wave != 0) return;
+    add(1);
+#pragma unroll
+    for (int t = 0; t < TT; t++) {
+        const int tok = b.t0 + 16 * t + m;
+        if (tok >= b.t1) continue;
+        float* dst = a.workspace + ((int64_t)split * a.tokens + tok) * a.rank + 4 * g;
+#pragma unroll
+        for (int r = 0; r < RT; r++)    // the rank is a multiple of 8: 4 of it are inside or outside
+            if (16 * r + 4 * g < a.rank) *reinterpret_cast<v4f*>(dst + 16 * r) = acc[r][t];
     }
 }
 
+// 16 bytes of a row of base or out: UNIT consecutive elements, aligned to
+// their own size only (a row of odd length starts anywhere).
 template <bool F32>
 struct LoraOut {
-    // 4 consecutive elements, aligned to their own size only: a row of odd
-    // length starts anywhere
-    typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
-    typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
-    static __device__ __forceinline__ v4f load(const char* p) {
+    static constexpr int UNIT = F32 ? 4 : 8, ESZ = F32 ? 4 : 2;
+    typedef uint32_t u4 __attribute__((ext_vector_type(4), aligned(2)));
+    static __device__ __forceinline__ v4u load(const char* p) {
+        const u4 v = *reinterpret_cast<const u4*>(p);
+        return v4u{v[0], v[1], v[2], v[3]};
+    }
+    static __device__ __forceinline__ void store(char* p, v4u v) { *reinterpret_cast<u4*>(p) = u4{v[0], v[1], v[2], v[3]}; }
+    static __device__ __forceinline__ v4u add(v4u v, const v4f* d) {
         if constexpr (F32) {
-            const f4 v = *reinterpret_cast<const f4*>(p);
-            return v4f{v[0], v[1], v[2], v[3]};
+            return __builtin_bit_cast(v4u, __builtin_bit_cast(v4f, v) + d[0]);
         } else {
-            const u2 v = *reinterpret_cast<const u2*>(p);
-            return v4f{__builtin_bit_cast(float, v[0] << 16), __builtin_bit_cast(float, v[0] & 0xFFFF0000u),
-                       __builtin_bit_cast(float, v[1] << 16), __builtin_bit_cast(float, v[1] & 0xFFFF0000u)};
+            v4u r;
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                r[i] = bf16x2_bits(__builtin_bit_cast(float, v[i] << 16) + d[i >> 1][(2 * i) & 3],
+                                   __builtin_bit_cast(float, v[i] & 0xFFFF0000u) + d[i >> 1][(2 * i + 1) & 3]);
+            return r;
         }
     }
-    static __device__ __forceinline__ void store(char* p, v4f v) {
+    static __device__ __forceinline__ void add1(char* dst, const char* src, float d) {
         if constexpr (F32)
-            *reinterpret_cast<f4*>(p) = f4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<float*>(dst) = *reinterpret_cast<const float*>(src) + d;
         else
-            *reinterpret_cast<u2*>(p) = u2{bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
-    }
-    static __device__ __forceinline__ float load1(const char* p) {
-        if constexpr (F32)
-            return *reinterpret_cast<const float*>(p);
-        else
-            return __builtin_bit_cast(float, (uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
-    }
-    static __device__ __forceinline__ void store1(char* p, float v) {
-        if constexpr (F32)
-            *reinterpret_cast<float*>(p) = v;
-        else
-            *reinterpret_cast<uint16_t*>(p) = (uint16_t)(bf16x2_bits(v, 0.0f) & 0xFFFFu);
+            *reinterpret_cast<uint16_t*>(dst) =
+                (uint16_t)bf16x2_bits(__builtin_bit_cast(float, (uint32_t)*reinterpret_cast<const uint16_t*>(src) << 16) + d, 0.0f);
     }
 };
 
-template <bool F32>
+template <bool F32, int TT>
 __global__ __launch_bounds__(LORA_THREADS) void lora_expand_kernel(LoraArgs a, int splits, int col_blocks, int cols) {
     constexpr int PIECES = F32 ? 3 : 2, ESZ = F32 ? 4 : 2;
     using Out = LoraOut<F32>;
-    extern __shared__ uint16_t pieces[];   // [16 tokens][kk], kk = PIECES * rank up to a multiple of 32, + 8
+    constexpr int UNITS = 16 / Out::UNIT;
+    extern __shared__ uint16_t pieces[];   // [16 TT tokens][kk], kk = PIECES * rank up to a multiple of 32, + 8
     const int id = blockIdx.x / col_blocks, part = blockIdx.x - id * col_blocks;
-    const LoraBlock b = lora_block(a, id);
+    const LoraBlock b = lora_block<TT>(a, id);
     if (b.t0 >= b.t1) return;
     const int n0 = part * cols, n1 = min(a.n, n0 + cols);
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
-    const int t = b.t0 + m;
-    const char* base = static_cast<const char*>(a.base) + (int64_t)t * a.n * ESZ;
-    char* out = static_cast<char*>(a.out) + (int64_t)t * a.n * ESZ;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
+    const char* base = static_cast<const char*>(a.base);
+    char* out = static_cast<char*>(a.out);
     if (b.adapter < 0) {
-        if (a.out == a.base || t >= b.t1) return;
-        for (int n = n0 + 64 * wave + 16 * g; n < n1; n += 256)
-            for (int q = 0; q < 16 && n + q < n1; q += 4) {
-                if (n + q + 4 <= n1)
-                    Out::store(out + (int64_t)(n + q) * ESZ, Out::load(base + (int64_t)(n + q) * ESZ));
-                else
-                    for (int i = n + q; i < n1; i++) Out::store1(out + (int64_t)i * ESZ, Out::load1(base + (int64_t)i * ESZ));
+        if (a.out == a.base) return;
+        for (int t = b.t0 + wave; t < b.t1; t += 4)
+            for (int c = n0 + lane * Out::UNIT; c < n1; c += 64 * Out::UNIT) {
+                const int64_t at = ((int64_t)t * a.n + c) * ESZ;
+                if (c + Out::UNIT <= n1) {
+                    Out::store(out + at, Out::load(base + at));
+                } else {
+                    for (int i = 0; c + i < n1; i++) Out::add1(out + at + i * ESZ, base + at + i * ESZ, -0.0f);
+                }
             }
         return;
     }
     const int steps = (PIECES * a.rank + 31) >> 5, row = steps * 32 + 8;
+    const uint16_t* B = static_cast<const uint16_t*>(a.B) + (int64_t)b.adapter * a.n * a.rank;
+    // Tile q, row m of the product is column n + 16 (m / 4) + 4 q + m % 4, so
+    // that a lane ends up with 16 consecutive columns of its token.
+    v4u w[4], old[TT][UNITS];
+    const uint16_t* src[4];
+    auto load_w = [&](int f) {       // step f: ranks 32 f + 8 g .. of the pieces, which repeat B's
+        int r = 32 * f + 8 * g;
+        while (r >= a.rank) r -= a.rank;
+#pragma unroll
+        for (int q = 0; q < 4; q++) w[q] = *reinterpret_cast<const v4u*>(src[q] + r);
+    };
+    auto load = [&](int n) {
+        const int col = n + 16 * (m >> 2) + (m & 3), c0 = n + 16 * g;
+#pragma unroll
+        for (int q = 0; q < 4; q++) src[q] = B + (int64_t)min(col + 4 * q, a.n - 1) * a.rank;
+        load_w(0);
+#pragma unroll
+        for (int t = 0; t < TT; t++) {
+            const int tok = b.t0 + 16 * t + m;
+#pragma unroll
+            for (int u = 0; u < UNITS; u++)
+                if (tok < b.t1 && c0 + (u + 1) * Out::UNIT <= n1)
+                    old[t][u] = Out::load(base + ((int64_t)tok * a.n + c0) * ESZ + 16 * u);
+        }
+    };
+    int n = n0 + 64 * wave;
+    if (n < n1) load(n);             // on their way while h is put together
+
     const float scale = a.scale[b.adapter];
-    for (int i = threadIdx.x; i < LORA_BLOCK * a.rank; i += LORA_THREADS) {
-        const int tok = i / a.rank, r = i - tok * a.rank;
-        float h = 0.0f;
+    const int quads = a.rank >> 2;
+    for (int i = threadIdx.x; i < 16 * TT * quads; i += LORA_THREADS) {
+        const int tok = i / quads, r = 4 * (i - tok * quads);
+        v4f h = {0, 0, 0, 0};
         if (b.t0 + tok < b.t1)
-            for (int s = 0; s < splits; s++) h += a.workspace[((int64_t)s * a.tokens + b.t0 + tok) * a.rank + r];
+#pragma unroll 4
+            for (int s = 0; s < splits; s++)
+                h += *reinterpret_cast<const v4f*>(a.workspace + ((int64_t)s * a.tokens + b.t0 + tok) * a.rank + r);
         h *= scale;
 #pragma unroll
         for (int p = 0; p < PIECES; p++) {
-            const uint32_t bits = bf16x2_bits(h, 0.0f) & 0xFFFFu;
-            pieces[tok * row + p * a.rank + r] = (uint16_t)bits;
-            h -= __builtin_bit_cast(float, bits << 16);
+            const uint32_t lo = bf16x2_bits(h[0], h[1]), hi = bf16x2_bits(h[2], h[3]);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(&pieces[tok * row + p * a.rank + r]);
+            dst[0] = lo, dst[1] = hi;
+            h -= v4f{__builtin_bit_cast(float, lo << 16), __builtin_bit_cast(float, lo & 0xFFFF0000u),
+                     __builtin_bit_cast(float, hi << 16), __builtin_bit_cast(float, hi & 0xFFFF0000u)};
         }
     }
     const int tail = steps * 32 - PIECES * a.rank;
-    for (int i = threadIdx.x; i < LORA_BLOCK * tail; i += LORA_THREADS)
+    for (int i = threadIdx.x; i < 16 * TT * tail; i += LORA_THREADS)
         pieces[(i / tail) * row + PIECES * a.rank + i % tail] = 0;
     __syncthreads();
-    const uint16_t* B = static_cast<const uint16_t*>(a.B) + (int64_t)b.adapter * a.n * a.rank;
-    for (int n = n0 + 64 * wave; n < n1; n += 256) {
-        // tile q, row m of the product: column n + 16 (m / 4) + 4 q + m % 4, so
-        // that a lane ends up with 16 consecutive columns of its token
-        v4f acc[4];
+    for (; n < n1; n += 256) {
+        v4f acc[TT][4];
 #pragma unroll
-        for (int q = 0; q < 4; q++) acc[q] = v4f{0, 0, 0, 0};
-        const int col = n + 16 * (m >> 2) + (m & 3);
+        for (int t = 0; t < TT; t++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) acc[t][q] = v4f{0, 0, 0, 0};
         for (int f = 0; f < steps; f++) {
-            const int at = 32 * f + 8 * g;
-            const bool live = at < PIECES * a.rank;
-            int r = at;
-            while (r >= a.rank && live) r -= a.rank;
-            const bf16x8 h = *reinterpret_cast<const bf16x8*>(&pieces[m * row + at]);
+            v4u now[4];
+            const bool live = 32 * f + 8 * g < PIECES * a.rank;    // behind the pieces: nothing, whatever B holds
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const bf16x8 w = load8(B + (int64_t)min(col + 4 * q, a.n - 1) * a.rank + r, live);
-                acc[q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, h, acc[q], 0, 0, 0);
+            for (int q = 0; q < 4; q++) now[q] = live ? w[q] : v4u{0, 0, 0, 0};
+            if (f + 1 < steps) load_w(f + 1);
+#pragma unroll
+            for (int t = 0; t < TT; t++) {
+                const bf16x8 h = *reinterpret_cast<const bf16x8*>(&pieces[(16 * t + m) * row + 32 * f + 8 * g]);
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, now[q]), h, acc[t][q], 0, 0, 0);
             }
         }
-        if (t < b.t1) {
+        const int c0 = n + 16 * g;
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const int c = n + 16 * g + 4 * q;
-                const int64_t off = (int64_t)c * ESZ;
-                if (c + 4 <= n1) {
-                    Out::store(out + off, Out::load(base + off) + acc[q]);
+        for (int t = 0; t < TT; t++) {
+            const int tok = b.t0 + 16 * t + m;
+            if (tok >= b.t1) continue;
+            const int64_t at = ((int64_t)tok * a.n + c0) * ESZ;
+#pragma unroll
+            for (int u = 0; u < UNITS; u++) {
+                const int c = c0 + u * Out::UNIT;
+                if (c + Out::UNIT <= n1) {
+                    Out::store(out + at + 16 * u, Out::add(old[t][u], &acc[t][u * (Out::UNIT / 4)]));
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        if (c + i < n1) Out::store1(out + off + i * ESZ, Out::load1(base + off + i * ESZ) + acc[q][i]);
+                    for (int i = 0; i < Out::UNIT; i++)
+                        if (c + i < n1)
+                            Out::add1(out + at + (u * Out::UNIT + i) * ESZ, base + at + (u * Out::UNIT + i) * ESZ,
+                                      acc[t][u * (Out::UNIT / 4) + i / 4][i & 3]);
                 }
             }
         }
+        if (n + 256 < n1) load(n + 256);
     }
 }
 
 struct LoraPlan {
-    int ids, splits, k_split, col_blocks, cols;
+    int tiles, ids, splits, k_split;                 // shrink: 16-token tiles of a block
+    int out_tiles, out_ids, col_blocks, cols;        // expand
 };
+// Blocks of 16 * tiles tokens: their numbers, and how many certainly have tokens.
+static int lora_ids(const LoraArgs& a, int tiles) { return a.tokens / (16 * tiles) + a.segments + 2; }
+static int lora_blocks(const LoraArgs& a, int tiles) {
+    const int full = (a.tokens + 16 * tiles - 1) / (16 * tiles), some = a.segments < a.tokens ? a.segments : a.tokens;
+    return full > some ? full : some;
+}
 static LoraPlan lora_plan(const LoraArgs& a) {
     LoraPlan p;
-    p.ids = a.tokens / LORA_BLOCK + a.segments + 2;
-    // blocks that certainly have tokens
-    const int full = (a.tokens + LORA_BLOCK - 1) / LORA_BLOCK;
-    const int blocks = full > a.segments ? full : (a.segments < a.tokens ? a.segments : a.tokens);
+    // Long segments: blocks of up to 64 tokens read the adapter less often; a
+    // wave's sums (rank tiles times token tiles) stay at 16 tiles or fewer.
+    const bool wide = a.tokens / (a.segments > 0 ? a.segments : 1) >= 32;
+    p.tiles = !wide || a.rank > 128 ? 1 : a.rank > 64 ? 2 : 4;
+    p.ids = lora_ids(a, p.tiles);
+    int blocks = lora_blocks(a, p.tiles);
     // about two workgroups a CU, of at least 256 of k each
     int splits = (512 + blocks - 1) / blocks;
     const int most = (a.k + 255) / 256;
@@ -229,6 +333,9 @@ static LoraPlan lora_plan(const LoraArgs& a) {
     splits = splits > LORA_MAX_SPLITS ? LORA_MAX_SPLITS : splits < 1 ? 1 : splits;
     p.k_split = ((a.k + splits - 1) / splits + 127) / 128 * 128;
     p.splits = a.k > 0 ? (a.k + p.k_split - 1) / p.k_split : 0;
+    p.out_tiles = wide ? 4 : 1;
+    p.out_ids = lora_ids(a, p.out_tiles);
+    blocks = lora_blocks(a, p.out_tiles);
     int col_blocks = (1024 + blocks - 1) / blocks;
     const int most_cols = (a.n + 255) / 256;
     col_blocks = col_blocks > most_cols ? most_cols : col_blocks;
@@ -242,9 +349,21 @@ int64_t lora_add_bytes(const LoraArgs& a) {
     return (int64_t)lora_plan(a).splits * a.tokens * a.rank * 4;
 }
 
-template <int RT>
+template <int RT, int TT>
 static hipError_t shrink(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
-    lora_shrink_kernel<RT><<<dim3((unsigned)(p.ids * p.splits)), dim3(LORA_THREADS), 0, stream>>>(a, p.splits, p.k_split);
+    lora_shrink_kernel<RT, TT><<<dim3((unsigned)(p.ids * p.splits)), dim3(LORA_THREADS), 0, stream>>>(a, p.splits, p.k_split);
+    return hipGetLastError();
+}
+
+template <bool F32>
+static hipError_t expand(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
+    const int steps = ((F32 ? 3 : 2) * a.rank + 31) / 32;
+    const unsigned lds = 16 * p.out_tiles * (steps * 32 + 8) * 2;
+    const dim3 grid((unsigned)(p.out_ids * p.col_blocks)), block(LORA_THREADS);
+    if (p.out_tiles == 4)
+        lora_expand_kernel<F32, 4><<<grid, block, lds, stream>>>(a, p.splits, p.col_blocks, p.cols);
+    else
+        lora_expand_kernel<F32, 1><<<grid, block, lds, stream>>>(a, p.splits, p.col_blocks, p.cols);
     return hipGetLastError();
 }
 
@@ -254,23 +373,17 @@ hipError_t launch_lora_add(const LoraArgs& in, int f32, hipStream_t stream) {
     const LoraPlan p = lora_plan(a);
     if (a.adapters > 0 && a.segments > 0) {
         hipError_t e;
-        if (a.rank <= 16) e = shrink<1>(a, p, stream);
-        else if (a.rank <= 32) e = shrink<2>(a, p, stream);
-        else if (a.rank <= 64) e = shrink<4>(a, p, stream);
-        else if (a.rank <= 128) e = shrink<8>(a, p, stream);
-        else e = shrink<16>(a, p, stream);
+        // the rank's tiles times the block's are what a wave accumulates
+        if (a.rank <= 16) e = p.tiles == 4 ? shrink<1, 4>(a, p, stream) : shrink<1, 1>(a, p, stream);
+        else if (a.rank <= 32) e = p.tiles == 4 ? shrink<2, 4>(a, p, stream) : shrink<2, 1>(a, p, stream);
+        else if (a.rank <= 64) e = p.tiles == 4 ? shrink<4, 4>(a, p, stream) : shrink<4, 1>(a, p, stream);
+        else if (a.rank <= 128) e = p.tiles == 2 ? shrink<8, 2>(a, p, stream) : shrink<8, 1>(a, p, stream);
+        else e = shrink<16, 1>(a, p, stream);
         if (e != hipSuccess) return e;
     } else if (a.out == a.base) {
         return hipSuccess;
     }
-    const int steps = ((f32 ? 3 : 2) * a.rank + 31) / 32;
-    const unsigned lds = LORA_BLOCK * (steps * 32 + 8) * 2;
-    const dim3 grid((unsigned)(p.ids * p.col_blocks)), block(LORA_THREADS);
-    if (f32)
-        lora_expand_kernel<true><<<grid, block, lds, stream>>>(a, p.splits, p.col_blocks, p.cols);
-    else
-        lora_expand_kernel<false><<<grid, block, lds, stream>>>(a, p.splits, p.col_blocks, p.cols);
-    return hipGetLastError();
+    return f32 ? expand<true>(a, p, stream) : expand<false>(a, p, stream);
 }
 
 }  // namespace fp8g
