@@ -100,15 +100,15 @@ struct AttnBlock {
 };
 __device__ __forceinline__ bool attn_block(const Kv4AttnArgs& a, int group, int id, AttnBlock& b) {
     auto start = [&](int i) { return min(max(a.q_start[i], 0), a.queries); };
-    const int found = find_block(start, a.batch, group, ATTN_ROWS_LOG2, id);
-    if (found == 0) return false;
-    b.seq = found - 1;
-    b.q0 = __builtin_amdgcn_readfirstlane(start(b.seq));
-    b.queries = __builtin_amdgcn_readfirstlane(start(b.seq + 1)) - b.q0;
+    const Sequence s = find_sequence(start, [&](int i) { return a.kv_len[i]; }, a.batch, group, ATTN_ROWS_LOG2, id);
+    if (s.index < 0) return false;
+    b.seq = s.index;
+    b.q0 = s.start;
+    b.queries = s.end - s.start;
     b.row0 = (id - ((int)(((int64_t)b.q0 * group) >> ATTN_ROWS_LOG2) + b.seq)) * ATTN_ROWS;
     b.rows = b.queries * group;
     const int64_t room = (int64_t)a.max_pages * a.page_size;
-    b.kv = (int)min((int64_t)max(__builtin_amdgcn_readfirstlane(a.kv_len[b.seq]), 0), room);
+    b.kv = (int)min((int64_t)max(s.word, 0), room);
     return b.row0 < b.rows;
 }
 

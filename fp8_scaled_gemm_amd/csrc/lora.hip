@@ -46,81 +46,88 @@ __device__ __forceinline__ LoraBlock lora_block(const LoraArgs& a, int id) {
         if (v > S + 1) return a.tokens;
         return min(max(a.seg_start[v - 1], 0), a.tokens);
     };
-    const int v = find_block(start, S + 2, 1, LOG2, id) - 1;
-    const int begin = __builtin_amdgcn_readfirstlane(start(v)), end = __builtin_amdgcn_readfirstlane(start(v + 1));
+    const Sequence q = find_sequence(
+        start, [&](int v) { return v >= 1 && v <= S ? a.seg_adapter[v - 1] : -1; }, S + 2, 1, LOG2, id);
     LoraBlock b;
-    b.t0 = begin + (id - ((begin >> LOG2) + v)) * (16 * TT);
-    b.t1 = min(end, b.t0 + 16 * TT);
-    b.adapter = v >= 1 && v <= S ? __builtin_amdgcn_readfirstlane(a.seg_adapter[v - 1]) : -1;
+    b.t0 = q.start + (id - ((q.start >> LOG2) + q.index)) * (16 * TT);
+    b.t1 = min(q.end, b.t0 + 16 * TT);
+    b.adapter = q.word;
     if (b.adapter >= a.adapters) b.adapter = -1;
     return b;
 }
 
 template <int RT, int TT>   // 16-row tiles of the rank, 16-token tiles of a block
-__global__ __launch_bounds__(LORA_THREADS) void lora_shrink_kernel(LoraArgs a, int splits, int k_split) {
+__global__ __launch_bounds__(LORA_THREADS, 2) void lora_shrink_kernel(LoraArgs a, int splits, int k_split, int rank_blocks) {
     __shared__ v4f part[2][RT * TT][64];
-    const int id = blockIdx.x / splits, split = blockIdx.x - id * splits;
+    const int id = blockIdx.x / (splits * rank_blocks), rest = blockIdx.x - id * splits * rank_blocks;
+    const int split = rest / rank_blocks, rank0 = (rest - split * rank_blocks) * (16 * RT);
     const LoraBlock b = lora_block<TT>(a, id);
     if (b.t0 >= b.t1 || b.adapter < 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
     const int k0 = split * k_split, k1 = min(a.k, k0 + k_split);
-    const uint16_t* A = static_cast<const uint16_t*>(a.A) + (int64_t)b.adapter * a.rank * a.k;
-    const uint16_t *rows[RT], *xs[TT];
+    // Row 16 r + m of the adapter; the last 8 rows of a rank that is an odd
+    // multiple of 8 are read twice instead of rows that are not there.
+    const int ranks = min(a.rank - rank0, 16 * RT);
+    const uint16_t* A = static_cast<const uint16_t*>(a.A) + ((int64_t)b.adapter * a.rank + rank0) * a.k + k0 + 8 * g;
+    const uint16_t *whole = A + (int64_t)m * a.k, *half = A + (int64_t)(m & 7) * a.k;
+    const uint16_t* xs[TT];
     v4f acc[RT][TT];
 #pragma unroll
     for (int t = 0; t < TT; t++)
         xs[t] = static_cast<const uint16_t*>(a.x) + (int64_t)min(b.t0 + 16 * t + m, b.t1 - 1) * a.k + k0 + 8 * g;
 #pragma unroll
-    for (int r = 0; r < RT; r++) {
-        rows[r] = A + (int64_t)min(16 * r + m, a.rank - 1) * a.k + k0 + 8 * g;
+    for (int r = 0; r < RT; r++)
 #pragma unroll
         for (int t = 0; t < TT; t++) acc[r][t] = v4f{0, 0, 0, 0};
-    }
-    // The waves take turns over blocks of 32 of k, AHEAD of them at a time and
-    // the next ones already on their way.
-    constexpr int AHEAD = RT + TT <= 2 ? 8 : RT + TT <= 6 ? 3 : RT + TT <= 8 ? 2 : 1;
-    struct Batch {
-        v4u w[AHEAD][RT], x[AHEAD][TT];
+    // The waves take turns over units of 64 of k (a row's 128-byte line), AHEAD
+    // of them at a time and the next ones already on their way.
+    constexpr int AHEAD = RT + TT <= 2 ? 4 : RT + TT <= 5 ? 2 : 1;
+    struct Unit {
+        v4u w[2][RT], x[2][TT];
     };
-    const int full = (k1 - k0) >> 5;
-    auto load = [&](Batch& s, int i) {
+    auto row = [&](int r) { return (16 * r + 16 <= ranks ? whole : half) + (int64_t)min(16 * r, ranks - 8) * a.k; };
+    auto load = [&](Unit& s, int at, bool live0, bool live1) {
 #pragma unroll
-        for (int u = 0; u < AHEAD; u++)
-            if (i + 4 * u < full) {
-                const int at = 32 * (i + 4 * u);
+        for (int t = 0; t < TT; t++) {
+            s.x[0][t] = live0 ? *reinterpret_cast<const v4u*>(xs[t] + at) : v4u{0, 0, 0, 0};
+            s.x[1][t] = live1 ? *reinterpret_cast<const v4u*>(xs[t] + at + 32) : v4u{0, 0, 0, 0};
+        }
 #pragma unroll
-                for (int t = 0; t < TT; t++) s.x[u][t] = *reinterpret_cast<const v4u*>(xs[t] + at);
-#pragma unroll
-                for (int r = 0; r < RT; r++) s.w[u][r] = *reinterpret_cast<const v4u*>(rows[r] + at);
-            }
+        for (int r = 0; r < RT; r++) {
+            s.w[0][r] = live0 ? *reinterpret_cast<const v4u*>(row(r) + at) : v4u{0, 0, 0, 0};
+            s.w[1][r] = live1 ? *reinterpret_cast<const v4u*>(row(r) + at + 32) : v4u{0, 0, 0, 0};
+        }
     };
-    auto multiply = [&](const v4u* w, const v4u* x) {
+    auto multiply = [&](const Unit& s) {
 #pragma unroll
-        for (int r = 0; r < RT; r++)
+        for (int j = 0; j < 2; j++)
 #pragma unroll
-            for (int t = 0; t < TT; t++)
-                acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[r]),
-                                                                    __builtin_bit_cast(bf16x8, x[t]), acc[r][t], 0, 0, 0);
+            for (int r = 0; r < RT; r++)
+#pragma unroll
+                for (int t = 0; t < TT; t++)
+                    acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8, s.w[j][r]), __builtin_bit_cast(bf16x8, s.x[j][t]), acc[r][t], 0, 0, 0);
     };
-    Batch now;
-    load(now, wave);
+    const int full = (k1 - k0) >> 6;
+    Unit now[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; u++)
+        if (wave + 4 * u < full) load(now[u], 64 * (wave + 4 * u), true, true);
     for (int i = wave; i < full; i += 4 * AHEAD) {
-        Batch next;
-        load(next, i + 4 * AHEAD);
+        Unit next[AHEAD];
 #pragma unroll
         for (int u = 0; u < AHEAD; u++)
-            if (i + 4 * u < full) multiply(now.w[u], now.x[u]);
-        now = next;
+            if (i + 4 * (AHEAD + u) < full) load(next[u], 64 * (i + 4 * (AHEAD + u)), true, true);
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++) {
+            if (i + 4 * u < full) multiply(now[u]);
+            now[u] = next[u];
+        }
     }
-    if (wave == (full & 3) && ((k1 - k0) & 31)) {       // what is left of k, a multiple of 8
-        const int at = 32 * full;
-        const bool live = at + 8 * g < k1 - k0;
-        v4u w[RT], x[TT];
-#pragma unroll
-        for (int t = 0; t < TT; t++) x[t] = live ? *reinterpret_cast<const v4u*>(xs[t] + at) : v4u{0, 0, 0, 0};
-#pragma unroll
-        for (int r = 0; r < RT; r++) w[r] = live ? *reinterpret_cast<const v4u*>(rows[r] + at) : v4u{0, 0, 0, 0};
-        multiply(w, x);
+    if (wave == (full & 3) && ((k1 - k0) & 63)) {       // what is left of k, a multiple of 8
+        const int at = 64 * full + 8 * g;
+        load(now[0], 64 * full, at < k1 - k0, at + 32 < k1 - k0);
+        multiply(now[0]);
     }
     // lane: token m, ranks 16 r + 4 g + i.  The waves' sums meet in LDS: 0 + 2
     // and 1 + 3, then both.
@@ -147,10 +154,10 @@ __global__ __launch_bounds__(LORA_THREADS) void lora_shrink_kernel(LoraArgs a, i
     for (int t = 0; t < TT; t++) {
         const int tok = b.t0 + 16 * t + m;
         if (tok >= b.t1) continue;
-        float* dst = a.workspace + ((int64_t)split * a.tokens + tok) * a.rank + 4 * g;
+        float* dst = a.workspace + ((int64_t)split * a.tokens + tok) * a.rank + rank0 + 4 * g;
 #pragma unroll
         for (int r = 0; r < RT; r++)    // the rank is a multiple of 8: 4 of it are inside or outside
-            if (16 * r + 4 * g < a.rank) *reinterpret_cast<v4f*>(dst + 16 * r) = acc[r][t];
+            if (16 * r + 4 * g < ranks) *reinterpret_cast<v4f*>(dst + 16 * r) = acc[r][t];
     }
 }
 
@@ -309,7 +316,7 @@ __global__ __launch_bounds__(LORA_THREADS) void lora_expand_kernel(LoraArgs a, i
 }
 
 struct LoraPlan {
-    int tiles, ids, splits, k_split;                 // shrink: 16-token tiles of a block
+    int tiles, ids, splits, k_split, rank_blocks;    // shrink: 16-token tiles of a block
     int out_tiles, out_ids, col_blocks, cols;        // expand
 };
 // Blocks of 16 * tiles tokens: their numbers, and how many certainly have tokens.
@@ -321,19 +328,20 @@ static int lora_blocks(const LoraArgs& a, int tiles) {
 static LoraPlan lora_plan(const LoraArgs& a) {
     LoraPlan p;
     // Long segments: blocks of up to 64 tokens read the adapter less often; a
-    // wave's sums (rank tiles times token tiles) stay at 16 tiles or fewer.
+    // wave's sums (rank tiles, 8 at most, times token tiles) stay at 16 tiles.
     const bool wide = a.tokens / (a.segments > 0 ? a.segments : 1) >= 32;
-    p.tiles = !wide || a.rank > 128 ? 1 : a.rank > 64 ? 2 : 4;
+    p.rank_blocks = a.rank > 128 ? 2 : 1;
+    p.tiles = !wide ? 1 : a.rank > 64 ? 2 : 4;
     p.ids = lora_ids(a, p.tiles);
     int blocks = lora_blocks(a, p.tiles);
     // about two workgroups a CU, of at least 256 of k each
-    int splits = (512 + blocks - 1) / blocks;
+    int splits = (512 + blocks * p.rank_blocks - 1) / (blocks * p.rank_blocks);
     const int most = (a.k + 255) / 256;
     splits = splits > most ? most : splits;
     splits = splits > LORA_MAX_SPLITS ? LORA_MAX_SPLITS : splits < 1 ? 1 : splits;
     p.k_split = ((a.k + splits - 1) / splits + 127) / 128 * 128;
     p.splits = a.k > 0 ? (a.k + p.k_split - 1) / p.k_split : 0;
-    p.out_tiles = wide ? 4 : 1;
+    p.out_tiles = wide ? 2 : 1;
     p.out_ids = lora_ids(a, p.out_tiles);
     blocks = lora_blocks(a, p.out_tiles);
     int col_blocks = (1024 + blocks - 1) / blocks;
@@ -351,7 +359,8 @@ int64_t lora_add_bytes(const LoraArgs& a) {
 
 template <int RT, int TT>
 static hipError_t shrink(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
-    lora_shrink_kernel<RT, TT><<<dim3((unsigned)(p.ids * p.splits)), dim3(LORA_THREADS), 0, stream>>>(a, p.splits, p.k_split);
+    lora_shrink_kernel<RT, TT><<<dim3((unsigned)(p.ids * p.splits * p.rank_blocks)), dim3(LORA_THREADS), 0, stream>>>(
+        a, p.splits, p.k_split, p.rank_blocks);
     return hipGetLastError();
 }
 
@@ -360,8 +369,8 @@ static hipError_t expand(const LoraArgs& a, const LoraPlan& p, hipStream_t strea
     const int steps = ((F32 ? 3 : 2) * a.rank + 31) / 32;
     const unsigned lds = 16 * p.out_tiles * (steps * 32 + 8) * 2;
     const dim3 grid((unsigned)(p.out_ids * p.col_blocks)), block(LORA_THREADS);
-    if (p.out_tiles == 4)
-        lora_expand_kernel<F32, 4><<<grid, block, lds, stream>>>(a, p.splits, p.col_blocks, p.cols);
+    if (p.out_tiles == 2)
+        lora_expand_kernel<F32, 2><<<grid, block, lds, stream>>>(a, p.splits, p.col_blocks, p.cols);
     else
         lora_expand_kernel<F32, 1><<<grid, block, lds, stream>>>(a, p.splits, p.col_blocks, p.cols);
     return hipGetLastError();
@@ -377,8 +386,7 @@ hipError_t launch_lora_add(const LoraArgs& in, int f32, hipStream_t stream) {
         if (a.rank <= 16) e = p.tiles == 4 ? shrink<1, 4>(a, p, stream) : shrink<1, 1>(a, p, stream);
         else if (a.rank <= 32) e = p.tiles == 4 ? shrink<2, 4>(a, p, stream) : shrink<2, 1>(a, p, stream);
         else if (a.rank <= 64) e = p.tiles == 4 ? shrink<4, 4>(a, p, stream) : shrink<4, 1>(a, p, stream);
-        else if (a.rank <= 128) e = p.tiles == 2 ? shrink<8, 2>(a, p, stream) : shrink<8, 1>(a, p, stream);
-        else e = shrink<16, 1>(a, p, stream);
+        else e = p.tiles == 2 ? shrink<8, 2>(a, p, stream) : shrink<8, 1>(a, p, stream);
         if (e != hipSuccess) return e;
     } else if (a.out == a.base) {
         return hipSuccess;

@@ -16,20 +16,34 @@
 
 namespace fp8g {
 
-// Number of bases that are <= id among start[0 .. count): the sequence's index
-// plus one.  All 64 lanes take part; the result is uniform.
-template <class Start>
-__device__ __forceinline__ int find_block(Start start, int count, int mult, int rows_log2, int id) {
+// The sequence of a block, its [start, end) and a word of its own.
+struct Sequence {
+    int index, start, end, word;      // index -1: the block belongs to none
+};
+
+// start(b), b <= count, ascending; word(b), b < count, read alongside so that
+// one round trip to memory finds everything.  All 64 lanes take part; the
+// result is uniform.
+template <class Start, class Word>
+__device__ __forceinline__ Sequence find_sequence(Start start, Word word, int count, int mult, int rows_log2, int id) {
     const int lane = threadIdx.x & 63;
-    int found = 0;
+    Sequence s = {-1, 0, 0, 0};
     for (int c = 0; c < count; c += 64) {
         const int b = c + lane;
-        const bool below = b < count && (int)(((int64_t)start(b) * mult) >> rows_log2) + b <= id;
-        const int n = __popcll(__ballot(below));
-        found += n;
+        int at = 0, end = 0, w = 0;
+        if (b < count) at = start(b), end = start(b + 1), w = word(b);
+        const bool below = b < count && (int)(((int64_t)at * mult) >> rows_log2) + b <= id;
+        const int n = __popcll(__ballot(below));      // bases ascend: the lowest n lanes
+        if (n > 0) {
+            s.index = c + n - 1;
+            s.start = __builtin_amdgcn_readlane(at, n - 1);
+            s.end = __builtin_amdgcn_readlane(end, n - 1);
+            s.word = __builtin_amdgcn_readlane(w, n - 1);
+        }
         if (n < 64) break;
     }
-    return __builtin_amdgcn_readfirstlane(found);
+    s.index = __builtin_amdgcn_readfirstlane(s.index);
+    return s;
 }
 
 }  // namespace fp8g
