@@ -98,14 +98,15 @@ __device__ __forceinline__ float over_groups_sum(float v) {
 struct AttnBlock {
     int seq, row0, rows, q0, queries, kv;
 };
+template <int ROWS_LOG2>
 __device__ __forceinline__ bool attn_block(const Kv4AttnArgs& a, int group, int id, AttnBlock& b) {
     auto start = [&](int i) { return min(max(a.q_start[i], 0), a.queries); };
-    const Sequence s = find_sequence(start, [&](int i) { return a.kv_len[i]; }, a.batch, group, ATTN_ROWS_LOG2, id);
+    const Sequence s = find_sequence(start, [&](int i) { return a.kv_len[i]; }, a.batch, group, ROWS_LOG2, id);
     if (s.index < 0) return false;
     b.seq = s.index;
     b.q0 = s.start;
     b.queries = s.end - s.start;
-    b.row0 = (id - ((int)(((int64_t)b.q0 * group) >> ATTN_ROWS_LOG2) + b.seq)) * ATTN_ROWS;
+    b.row0 = (id - ((int)(((int64_t)b.q0 * group) >> ROWS_LOG2) + b.seq)) << ROWS_LOG2;
     b.rows = b.queries * group;
     const int64_t room = (int64_t)a.max_pages * a.page_size;
     b.kv = (int)min((int64_t)max(s.word, 0), room);
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
     const int split = blockIdx.x % p.splits, rest = blockIdx.x / p.splits;
     const int h = rest % a.kv_heads, id = rest / a.kv_heads;
     AttnBlock b;
-    if (!attn_block(a, group, id, b)) return;
+    if (!attn_block<ATTN_ROWS_LOG2>(a, group, id, b)) return;
 
     // the lane's row, its query and the keys [lo, hi) that it sees
     const int row = b.row0 + n;
@@ -377,6 +378,283 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
     }
 }
 
+// ------------------------------------------------------------------ many rows
+//
+// Where a sequence has many rows, a workgroup takes 32 of them a wave and all
+// of its waves share the keys and values of a step of 64: they are turned into
+// bf16 once, in LDS, and read from there as operands of
+// v_mfma_f32_32x32x16_bf16, transposed as above:
+//   S^T[key, row]: lane l holds row l % 32, half e = l / 32, and in register i
+//                  of a 32-key tile the key 8 (i / 4) + 4 e + i % 4
+//   O^T[dim, row]: registers 8 u .. 8 u + 7 are the weights' operand for the
+//                  keys 16 u + {4 e + 0..3, 8 + 4 e + 0..3}; the values' rows in
+//                  LDS (one a dim) hold the keys in that order.
+// While a step is computed from one half of the LDS, the next one's codes are
+// turned into the other, and those of the one after are on their way.
+// The running maximum moves only when a row's maximum has grown by 2^8 or more:
+// weights up to 2^8 lose nothing in bf16 and float32, and the outputs are
+// rarely scaled.
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+constexpr float ATTN_SLACK = 8.0f;
+
+// 16-byte chunk c of row m, rows of CHUNKS chunks: neighbouring rows (reads of
+// one chunk) and rows 4 apart (writes of values) meet different banks.
+template <int CHUNKS>
+__device__ __forceinline__ int lds_at(int m, int c) {
+    if constexpr (CHUNKS == 16) return m * 16 + (c ^ (m & 15));
+    return m * CHUNKS + (c ^ (((m >> 1) ^ (m >> 4)) & 7));
+}
+
+template <int DK, int DV, int WAVES, bool SPLIT>
+__global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4AttnArgs a, AttnPlan p) {
+    constexpr int THREADS = 64 * WAVES, ROWS = 32 * WAVES, ROWS_LOG2 = WAVES == 8 ? 8 : 7;
+    constexpr int KC = DK / 8, KK = DK / 16, DT = DV / 32;
+    // keys: 8 bytes of codes (16 dims) a unit; values: VD dims of 8 keys a unit
+    constexpr int KU = ATTN_STEP * DK / 16, KN = (KU + THREADS - 1) / THREADS;
+    constexpr int VD = WAVES == 8 || DV == 64 ? 2 : 4, VU = 8 * DV / VD;
+    static_assert(VU <= THREADS, "one unit of values a thread");
+    __shared__ v4u s_k[2][ATTN_STEP * KC];
+    __shared__ v4u s_v[2][DV * 8];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, e = lane >> 5;
+    const int group = a.q_heads / a.kv_heads;
+    // long blocks (the last rows of a sequence see the most keys) first
+    const int split = blockIdx.x % p.splits, rest = blockIdx.x / p.splits;
+    const int h = rest % a.kv_heads, id = p.ids - 1 - rest / a.kv_heads;
+    AttnBlock b;
+    if (!attn_block<ROWS_LOG2>(a, group, id, b)) return;
+
+    const int first = b.kv - b.queries;
+    auto top_of = [&](int q) { return a.causal ? max(0, min(b.kv, first + q + 1)) : b.kv; };
+    auto low_of = [&](int q) { return a.window ? max(0, first + q + 1 - a.window) : 0; };
+    const int row = b.row0 + 32 * wave + n;
+    const bool real = row < b.rows;
+    const int qi = min(row, b.rows - 1) / group, head = h * group + min(row, b.rows - 1) % group;
+    const int hi = real ? top_of(qi) : 0, lo = low_of(qi);
+    // keys of the block, and of the wave's rows: any row's [w_lo, w_hi), every row's [in_lo, in_hi)
+    const int q_last = (min(b.row0 + ROWS, b.rows) - 1) / group;
+    const int all_lo = min(low_of(b.row0 / group), b.kv), all_hi = top_of(q_last);
+    const int w_row0 = b.row0 + 32 * wave, w_rows = min(32, b.rows - w_row0);
+    const int w_first = w_row0 / group, w_last = (w_row0 + max(w_rows, 1) - 1) / group;
+    const int w_lo = low_of(w_first), w_hi = w_rows > 0 ? top_of(w_last) : 0;
+    const int in_lo = low_of(w_last), in_hi = top_of(w_first);
+    const int64_t begin64 = (all_lo & ~(ATTN_STEP - 1)) + (int64_t)split * p.chunk;
+    const int end = (int)min((int64_t)all_hi, begin64 + p.chunk);
+    const int64_t target = (int64_t)(b.q0 + qi) * a.q_heads + head;
+    float* const part_ml = a.workspace + (int64_t)a.queries * a.q_heads * p.splits * DV;
+    if (SPLIT && begin64 >= end) {
+        if (e == 0 && real) part_ml[(target * p.splits + split) * 2] = -INFINITY;
+        return;
+    }
+    const int begin = (int)begin64, steps = begin < end ? (end - begin + ATTN_STEP - 1) / ATTN_STEP : 0;
+
+    // A negative scale turns the queries' signs, so that the largest product is
+    // the largest score; a scale of zero becomes one that changes nothing and
+    // keeps -inf * scale at -inf.
+    const float c2 = __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, 0x1p-120f);
+    bf16x8 q[KK];
+    {
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(b.q0 + qi) * a.q_stride + (int64_t)head * DK + 8 * e;
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int j = 0; j < KK; j++) {
+            const v4u w = *reinterpret_cast<const v4u*>(src + 16 * j);
+            q[j] = __builtin_bit_cast(bf16x8, v4u{w[0] ^ flip, w[1] ^ flip, w[2] ^ flip, w[3] ^ flip});
+        }
+    }
+
+    const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
+    auto page_of = [&](int key, int& at) {
+        const int whole = (int)divide(key, p.page);
+        at = key - whole * a.page_size;
+        return min(max(table[min(whole, a.max_pages - 1)], 0), a.pages - 1);
+    };
+    // Codes of a step.  Keys: unit i is piece i % KC/2 (8 bytes) of key i / (KC/2).
+    // Values: thread t has dims VD (t % (DV / VD)) .. and the keys of operand
+    // chunk t / (DV / VD): two runs of 4 that lie 8 apart.
+    struct Codes {
+        v2u k[KN];
+        uint32_t ks[KN], v[8], vs[2];
+    };
+    const int vq = threadIdx.x % (DV / VD), vc = threadIdx.x / (DV / VD);
+    const int vkey = 32 * (vc >> 2) + 16 * ((vc >> 1) & 1) + 4 * (vc & 1);
+    auto load = [&](Codes& s, int base) {
+#pragma unroll
+        for (int u = 0; u < KN; u++) {
+            const int i = threadIdx.x + u * THREADS;
+            if (KU % THREADS == 0 || i < KU) {
+                int at;
+                const int key = i / (KC / 2), piece = i % (KC / 2);
+                const int64_t ph = (int64_t)page_of(base + key, at) * a.kv_heads + h;
+                s.k[u] = *reinterpret_cast<const v2u*>(a.k_codes + (ph * a.page_size + at) * (DK / 2) + 8 * piece);
+                s.ks[u] = a.k_scales[(ph * (DK / 32) + (piece >> 1)) * a.page_size + at];
+            }
+        }
+        if (VU == THREADS || threadIdx.x < VU) {
+            int at;
+            const int64_t ph = (int64_t)page_of(base + vkey, at) * a.kv_heads + h;
+            const uint8_t* c = a.v_codes + (ph * a.page_size + at) * (DV / 2) + vq * (VD / 2);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint8_t* r = c + (j + (j & 4)) * (DV / 2);
+                s.v[j] = VD == 4 ? (uint32_t) * reinterpret_cast<const uint16_t*>(r) : (uint32_t)*r;
+            }
+            const uint8_t* sc = a.v_scales + (ph * (DV / 32) + vq / (32 / VD)) * a.page_size + at;
+            s.vs[0] = *reinterpret_cast<const uint32_t*>(sc);
+            s.vs[1] = *reinterpret_cast<const uint32_t*>(sc + 8);
+        }
+    };
+    auto turn = [&](Codes& s, int base, int buffer) {
+#pragma unroll
+        for (int u = 0; u < KN; u++) {
+            const int i = threadIdx.x + u * THREADS;
+            if (KU % THREADS == 0 || i < KU) {
+                const int key = i / (KC / 2), piece = i % (KC / 2);
+                const float scale = __builtin_bit_cast(float, s.ks[u] << 23);
+                s_k[buffer][lds_at<KC>(key, 2 * piece)] = __builtin_bit_cast(v4u, fp4x8(s.k[u][0], scale));
+                s_k[buffer][lds_at<KC>(key, 2 * piece + 1)] = __builtin_bit_cast(v4u, fp4x8(s.k[u][1], scale));
+            }
+        }
+        if (VU == THREADS || threadIdx.x < VU) {
+            if (base + ATTN_STEP > all_hi || base < all_lo) {
+                // values outside the block's keys: a scale of 2^-127 makes
+                // whatever they hold finite, and their weight of zero removes it
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    uint32_t keep = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int key = base + vkey + 8 * r + i;
+                        if (key < all_hi && key >= all_lo) keep |= 0xFFu << (8 * i);
+                    }
+                    s.vs[r] &= keep;
+                }
+            }
+            const float sc[8] = {scale_of<0>(s.vs[0]), scale_of<1>(s.vs[0]), scale_of<2>(s.vs[0]), scale_of<3>(s.vs[0]),
+                                 scale_of<0>(s.vs[1]), scale_of<1>(s.vs[1]), scale_of<2>(s.vs[1]), scale_of<3>(s.vs[1])};
+            auto pair = [&](auto sel) {
+                constexpr int SEL = decltype(sel)::value;
+                uint32_t x[8];
+#pragma unroll
+                for (int j = 0; j < 8; j++) x[j] = fp4x2<SEL>(s.v[j], sc[j]);
+                v4u even, odd;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    even[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x05040100u);
+                    odd[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x07060302u);
+                }
+                s_v[buffer][lds_at<8>(VD * vq + 2 * SEL, vc)] = even;
+                s_v[buffer][lds_at<8>(VD * vq + 2 * SEL + 1, vc)] = odd;
+            };
+            pair(std::integral_constant<int, 0>{});
+            if constexpr (VD == 4) pair(std::integral_constant<int, 1>{});
+        }
+    };
+
+    v16f o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
+    float m = -INFINITY, l = 0.0f;
+
+    Codes s;
+    if (steps > 0) load(s, begin);
+    if (steps > 0) turn(s, begin, 0);
+    if (steps > 1) load(s, begin + ATTN_STEP);
+    __syncthreads();
+    for (int t = 0; t < steps; t++) {
+        const int base = begin + t * ATTN_STEP, buffer = t & 1;
+        if (t + 1 < steps) turn(s, base + ATTN_STEP, buffer ^ 1);
+        if (t + 2 < steps) load(s, base + 2 * ATTN_STEP);
+        if (base < w_hi && base + ATTN_STEP > w_lo) {
+            v16f acc[2];
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) acc[x][i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < KK; j++)
+#pragma unroll
+                for (int x = 0; x < 2; x++)
+                    acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, s_k[buffer][lds_at<KC>(32 * x + n, 2 * j + e)]), q[j], acc[x], 0, 0, 0);
+            if (base + ATTN_STEP > min(in_hi, end) || base < in_lo) {
+                const int top = min(hi, end);
+#pragma unroll
+                for (int x = 0; x < 2; x++)
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const int key = base + 32 * x + 8 * (i >> 2) + 4 * e + (i & 3);
+                        if (key >= top || key < lo) acc[x][i] = -INFINITY;
+                    }
+            }
+            float top = acc[0][0];
+#pragma unroll
+            for (int x = 0; x < 2; x++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) top = __builtin_fmaxf(top, acc[x][i]);
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64)) * c2;
+            if (__any(top > m + ATTN_SLACK)) {
+                const float m_new = __builtin_fmaxf(m, top);
+                const float alpha = __builtin_amdgcn_exp2f(m - (m_new == -INFINITY ? 0.0f : m_new));
+                m = m_new;
+                l *= alpha;
+#pragma unroll
+                for (int d = 0; d < DT; d++) o[d] *= alpha;
+            }
+            const float m_use = m == -INFINITY ? 0.0f : m;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            bf16x8 w[4];
+#pragma unroll
+            for (int u = 0; u < 4; u++) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u >> 1][8 * (u & 1) + i], c2, -m_use));
+                    sum[i & 3] += x[i];
+                }
+                const v4u r = {bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]), bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7])};
+                w[u] = __builtin_bit_cast(bf16x8, r);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+#pragma unroll
+                for (int d = 0; d < DT; d++)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8, s_v[buffer][lds_at<8>(32 * d + n, 2 * u + e)]), w[u], o[d], 0, 0, 0);
+        }
+        __syncthreads();
+    }
+    l += __shfl_xor(l, 32, 64);
+    if (!real) return;
+    // register i of tile d: dim 32 d + 8 (i / 4) + 4 e + i % 4
+    if constexpr (SPLIT) {
+        float* dst = a.workspace + (target * p.splits + split) * DV + 4 * e;
+#pragma unroll
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<v4f*>(dst + 32 * d + 2 * i) = v4f{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+        if (e == 0) {
+            part_ml[(target * p.splits + split) * 2] = m;
+            part_ml[(target * p.splits + split) * 2 + 1] = l;
+        }
+    } else {
+        const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + target * DV + 4 * e;
+#pragma unroll
+        for (int d = 0; d < DT; d++)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<v2u*>(dst + 32 * d + 2 * i) =
+                    v2u{bf16x2_bits(o[d][i] * inv, o[d][i + 1] * inv), bf16x2_bits(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+        if (a.lse && e == 0) a.lse[target] = m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    }
+}
+
 // Joins the chunks of every row, in order: DV / 4 lanes a row.
 template <int DV>
 __global__ __launch_bounds__(ATTN_THREADS) void kv4_attention_join_kernel(Kv4AttnArgs a, AttnPlan p) {
@@ -407,23 +685,34 @@ __global__ __launch_bounds__(ATTN_THREADS) void kv4_attention_join_kernel(Kv4Att
     if (a.lse && lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
+// Many rows a sequence on average: blocks of 128 rows and more, not 16.
+constexpr int ATTN_WIDE_WAVES = 8;
+static bool attn_wide(const Kv4AttnArgs& a) {
+    return (int64_t)a.queries * (a.q_heads / a.kv_heads) >= 64 * (int64_t)a.batch;
+}
+
 static AttnPlan attn_plan(const Kv4AttnArgs& a) {
     AttnPlan p;
     const int group = a.q_heads / a.kv_heads;
-    p.ids = (int)((int64_t)a.queries * group / ATTN_ROWS) + a.batch;
+    const bool wide = attn_wide(a);
+    const int rows = wide ? 32 * ATTN_WIDE_WAVES : ATTN_ROWS;
+    p.ids = (int)((int64_t)a.queries * group / rows) + a.batch;
     p.page = fast_div((uint32_t)a.page_size);
     int64_t keys = (int64_t)a.max_pages * a.page_size;
-    if (a.window && keys > (int64_t)a.window + ATTN_ROWS + ATTN_STEP) keys = (int64_t)a.window + ATTN_ROWS + ATTN_STEP;
+    const int64_t span = (int64_t)a.window + rows + ATTN_STEP;
+    if (a.window && keys > span) keys = span;
     // blocks that certainly have rows
-    int64_t blocks = ((int64_t)a.queries * group + ATTN_ROWS - 1) / ATTN_ROWS;
+    int64_t blocks = ((int64_t)a.queries * group + rows - 1) / rows;
     const int some = a.batch < a.queries ? a.batch : a.queries;
     if (blocks < some) blocks = some;
     blocks *= a.kv_heads;
-    int64_t want = blocks >= 2048 ? 1 : 2048 / blocks;
+    const int64_t full = wide ? 512 : 2048;     // workgroups that fill the chip
+    int64_t want = blocks >= full ? 1 : full / blocks;
     const int64_t most = ((int64_t)1 << 30) / ((int64_t)p.ids * a.kv_heads);   // keeps the grid's size an int
     if (want > most) want = most < 1 ? 1 : most;
+    const int64_t least = wide ? 4 * ATTN_STEP : ATTN_CHUNK;
     int64_t chunk = ((keys + want - 1) / want + ATTN_CHUNK - 1) / ATTN_CHUNK * ATTN_CHUNK;
-    if (chunk < ATTN_CHUNK) chunk = ATTN_CHUNK;
+    if (chunk < least) chunk = least;
     p.chunk = (int)chunk;
     p.splits = (int)((keys + chunk - 1) / chunk);
     if (p.splits < 1) p.splits = 1;
@@ -436,20 +725,25 @@ int64_t kv4_attention_bytes(const Kv4AttnArgs& a) {
     return p.splits > 1 ? (int64_t)a.queries * a.q_heads * p.splits * (a.dv + 2) * 4 : 0;
 }
 
+template <int DK, int DV, bool SPLIT>
+static hipError_t launch_rows(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)p.ids * a.kv_heads * p.splits));
+    if (attn_wide(a))
+        kv4_attention_wide_kernel<DK, DV, ATTN_WIDE_WAVES, SPLIT><<<grid, dim3(64 * ATTN_WIDE_WAVES), 0, stream>>>(a, p);
+    else
+        kv4_attention_kernel<DK, DV, SPLIT><<<grid, dim3(ATTN_THREADS), 0, stream>>>(a, p);
+    return hipGetLastError();
+}
+
 template <int DK, int DV>
 static hipError_t launch_dims(const Kv4AttnArgs& a, hipStream_t stream) {
     const AttnPlan p = attn_plan(a);
-    const dim3 grid((unsigned)((int64_t)p.ids * a.kv_heads * p.splits)), block(ATTN_THREADS);
-    if (p.splits == 1) {
-        kv4_attention_kernel<DK, DV, false><<<grid, block, 0, stream>>>(a, p);
-        return hipGetLastError();
-    }
-    kv4_attention_kernel<DK, DV, true><<<grid, block, 0, stream>>>(a, p);
-    const hipError_t e = hipGetLastError();
+    if (p.splits == 1) return launch_rows<DK, DV, false>(a, p, stream);
+    const hipError_t e = launch_rows<DK, DV, true>(a, p, stream);
     if (e != hipSuccess) return e;
     constexpr int ROWS = ATTN_THREADS / (DV / 4);
     const int64_t rows = (int64_t)a.queries * a.q_heads;
-    kv4_attention_join_kernel<DV><<<dim3((unsigned)((rows + ROWS - 1) / ROWS)), block, 0, stream>>>(a, p);
+    kv4_attention_join_kernel<DV><<<dim3((unsigned)((rows + ROWS - 1) / ROWS)), dim3(ATTN_THREADS), 0, stream>>>(a, p);
     return hipGetLastError();
 }
 
