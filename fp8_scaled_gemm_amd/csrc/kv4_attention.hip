@@ -400,19 +400,21 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr float ATTN_SLACK = 8.0f;
 
 // 16-byte chunk c of row m, rows of CHUNKS chunks: neighbouring rows (reads of
-// one chunk) and rows 4 apart (writes of values) meet different banks.
+// one chunk) and rows 2 or 4 apart (writes of values) meet different banks, and
+// rows 32 apart are a constant apart.
 template <int CHUNKS>
 __device__ __forceinline__ int lds_at(int m, int c) {
     if constexpr (CHUNKS == 16) return m * 16 + (c ^ (m & 15));
-    return m * CHUNKS + (c ^ (((m >> 1) ^ (m >> 4)) & 7));
+    return m * CHUNKS + (c ^ (((m >> 1) ^ ((m >> 4) & 1)) & 7));
 }
 
 template <int DK, int DV, int WAVES, bool SPLIT>
 __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4AttnArgs a, AttnPlan p) {
     constexpr int THREADS = 64 * WAVES, ROWS = 32 * WAVES, ROWS_LOG2 = WAVES == 8 ? 8 : 7;
     constexpr int KC = DK / 8, KK = DK / 16, DT = DV / 32;
-    // keys: 8 bytes of codes (16 dims) a unit; values: VD dims of 8 keys a unit
-    constexpr int KU = ATTN_STEP * DK / 16, KN = (KU + THREADS - 1) / THREADS;
+    // keys: 8 bytes of codes (16 dims) a unit, 8 or 4 of them (a part of 128 or 64
+    // dims) side by side; values: VD dims of 8 keys a unit
+    constexpr int KN = DK == 192 ? 2 : 1;
     constexpr int VD = WAVES == 8 || DV == 64 ? 2 : 4, VU = 8 * DV / VD;
     static_assert(VU <= THREADS, "one unit of values a thread");
     __shared__ v4u s_k[2][ATTN_STEP * KC];
@@ -464,53 +466,74 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
         }
     }
 
-    const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
-    auto page_of = [&](int key, int& at) {
-        const int whole = (int)divide(key, p.page);
-        at = key - whole * a.page_size;
-        return min(max(table[min(whole, a.max_pages - 1)], 0), a.pages - 1);
-    };
-    // Codes of a step.  Keys: unit i is piece i % KC/2 (8 bytes) of key i / (KC/2).
-    // Values: thread t has dims VD (t % (DV / VD)) .. and the keys of operand
-    // chunk t / (DV / VD): two runs of 4 that lie 8 apart.
+    // Codes of a step.  Keys: unit i of a part of P pieces is piece i % P of key
+    // i / P.  Values: thread t has dims VD (t % (DV / VD)) .. and the keys of
+    // operand chunk t / (DV / VD): two runs of 4 that lie 8 apart.  A wave's keys
+    // lie in one run of 16, so in one page, and their place is the wave's, not
+    // the lane's: 64-bit scalars and 32-bit lane offsets that no step changes.
     struct Codes {
         v2u k[KN];
         uint32_t ks[KN], v[8], vs[2];
     };
+    struct Place {
+        int64_t head;     // page * kv_heads + h
+        int at;           // row in the page
+    };
+    const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
+    auto place_of = [&](int key) {
+        const int whole = (int)divide(key, p.page);
+        const int page = min(max(table[min(whole, a.max_pages - 1)], 0), a.pages - 1);
+        Place r;
+        r.head = (int64_t)page * a.kv_heads + h;
+        r.at = key - whole * a.page_size;
+        return r;
+    };
+    auto pieces = [](int u) { return DK == 64 || u == 1 ? 4 : 8; };
+    auto k_live = [&](int u) { return THREADS == ATTN_STEP * pieces(u) || threadIdx.x < ATTN_STEP * pieces(u); };
+    auto k_key = [&](int u) { return (int)threadIdx.x / pieces(u); };
+    auto k_piece = [&](int u) { return 8 * u + (int)threadIdx.x % pieces(u); };
     const int vq = threadIdx.x % (DV / VD), vc = threadIdx.x / (DV / VD);
     const int vkey = 32 * (vc >> 2) + 16 * ((vc >> 1) & 1) + 4 * (vc & 1);
+    // the wave's run of 16 keys of a step, by its first thread's key
+    int k_run[KN], k_off[KN], ks_off[KN];
+#pragma unroll
+    for (int u = 0; u < KN; u++) {
+        k_run[u] = __builtin_amdgcn_readfirstlane(k_key(u) & ~15) & (ATTN_STEP - 1);
+        k_off[u] = (k_key(u) & 15) * (DK / 2) + 8 * k_piece(u);
+        ks_off[u] = (k_piece(u) >> 1) * a.page_size + (k_key(u) & 15);
+    }
+    const int v_run = __builtin_amdgcn_readfirstlane(vkey & ~15) & (ATTN_STEP - 1);
+    const int v_off = (vkey & 15) * (DV / 2) + vq * (VD / 2), vs_off = vq / (32 / VD) * a.page_size + (vkey & 15);
     auto load = [&](Codes& s, int base) {
 #pragma unroll
         for (int u = 0; u < KN; u++) {
-            const int i = threadIdx.x + u * THREADS;
-            if (KU % THREADS == 0 || i < KU) {
-                int at;
-                const int key = i / (KC / 2), piece = i % (KC / 2);
-                const int64_t ph = (int64_t)page_of(base + key, at) * a.kv_heads + h;
-                s.k[u] = *reinterpret_cast<const v2u*>(a.k_codes + (ph * a.page_size + at) * (DK / 2) + 8 * piece);
-                s.ks[u] = a.k_scales[(ph * (DK / 32) + (piece >> 1)) * a.page_size + at];
+            const Place r = place_of(base + k_run[u]);
+            const uint8_t* c = a.k_codes + (r.head * a.page_size + r.at) * (DK / 2);
+            const uint8_t* sc = a.k_scales + r.head * (DK / 32) * a.page_size + r.at;
+            if (k_live(u)) {
+                s.k[u] = *reinterpret_cast<const v2u*>(c + (uint32_t)k_off[u]);
+                s.ks[u] = sc[(uint32_t)ks_off[u]];
             }
         }
+        const Place r = place_of(base + v_run);
+        const uint8_t* c = a.v_codes + (r.head * a.page_size + r.at) * (DV / 2);
+        const uint8_t* sc = a.v_scales + r.head * (DV / 32) * a.page_size + r.at;
         if (VU == THREADS || threadIdx.x < VU) {
-            int at;
-            const int64_t ph = (int64_t)page_of(base + vkey, at) * a.kv_heads + h;
-            const uint8_t* c = a.v_codes + (ph * a.page_size + at) * (DV / 2) + vq * (VD / 2);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const uint8_t* r = c + (j + (j & 4)) * (DV / 2);
-                s.v[j] = VD == 4 ? (uint32_t) * reinterpret_cast<const uint16_t*>(r) : (uint32_t)*r;
+                const uint8_t* w = c + (uint32_t)v_off + (j + (j & 4)) * (DV / 2);
+                s.v[j] = VD == 4 ? (uint32_t) * reinterpret_cast<const uint16_t*>(w) : (uint32_t)*w;
             }
-            const uint8_t* sc = a.v_scales + (ph * (DV / 32) + vq / (32 / VD)) * a.page_size + at;
-            s.vs[0] = *reinterpret_cast<const uint32_t*>(sc);
-            s.vs[1] = *reinterpret_cast<const uint32_t*>(sc + 8);
+            s.vs[0] = *reinterpret_cast<const uint32_t*>(sc + (uint32_t)vs_off);
+            s.vs[1] = *reinterpret_cast<const uint32_t*>(sc + (uint32_t)vs_off + 8);
         }
     };
-    auto turn = [&](Codes& s, int base, int buffer) {
+    auto turn = [&](Codes& s, int base, auto half) {
+        constexpr int buffer = decltype(half)::value;
 #pragma unroll
         for (int u = 0; u < KN; u++) {
-            const int i = threadIdx.x + u * THREADS;
-            if (KU % THREADS == 0 || i < KU) {
-                const int key = i / (KC / 2), piece = i % (KC / 2);
+            if (k_live(u)) {
+                const int key = k_key(u), piece = k_piece(u);
                 const float scale = __builtin_bit_cast(float, s.ks[u] << 23);
                 s_k[buffer][lds_at<KC>(key, 2 * piece)] = __builtin_bit_cast(v4u, fp4x8(s.k[u][0], scale));
                 s_k[buffer][lds_at<KC>(key, 2 * piece + 1)] = __builtin_bit_cast(v4u, fp4x8(s.k[u][1], scale));
@@ -560,26 +583,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     float m = -INFINITY, l = 0.0f;
 
     Codes s;
-    if (steps > 0) load(s, begin);
-    if (steps > 0) turn(s, begin, 0);
-    if (steps > 1) load(s, begin + ATTN_STEP);
-    __syncthreads();
-    for (int t = 0; t < steps; t++) {
-        const int base = begin + t * ATTN_STEP, buffer = t & 1;
-        if (t + 1 < steps) turn(s, base + ATTN_STEP, buffer ^ 1);
+    auto step = [&](int t, auto half) {
+        constexpr int buffer = decltype(half)::value;
+        const int base = begin + t * ATTN_STEP;
+        if (t + 1 < steps) turn(s, base + ATTN_STEP, std::integral_constant<int, buffer ^ 1>{});
         if (t + 2 < steps) load(s, base + 2 * ATTN_STEP);
         if (base < w_hi && base + ATTN_STEP > w_lo) {
             v16f acc[2];
-#pragma unroll
-            for (int x = 0; x < 2; x++)
-#pragma unroll
-                for (int i = 0; i < 16; i++) acc[x][i] = 0.0f;
+            const v16f zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < KK; j++)
 #pragma unroll
                 for (int x = 0; x < 2; x++)
                     acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        __builtin_bit_cast(bf16x8, s_k[buffer][lds_at<KC>(32 * x + n, 2 * j + e)]), q[j], acc[x], 0, 0, 0);
+                        __builtin_bit_cast(bf16x8, s_k[buffer][lds_at<KC>(n, 2 * j + e) + 32 * KC * x]), q[j], j ? acc[x] : zero, 0, 0, 0);
             if (base + ATTN_STEP > min(in_hi, end) || base < in_lo) {
                 const int top = min(hi, end);
 #pragma unroll
@@ -624,9 +641,19 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
 #pragma unroll
                 for (int d = 0; d < DT; d++)
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        __builtin_bit_cast(bf16x8, s_v[buffer][lds_at<8>(32 * d + n, 2 * u + e)]), w[u], o[d], 0, 0, 0);
+                        __builtin_bit_cast(bf16x8, s_v[buffer][lds_at<8>(n, 2 * u + e) + 32 * 8 * d]), w[u], o[d], 0, 0, 0);
         }
         __syncthreads();
+    };
+    typedef std::integral_constant<int, 0> Even;
+    typedef std::integral_constant<int, 1> Odd;
+    if (steps > 0) load(s, begin);
+    if (steps > 0) turn(s, begin, Even{});
+    if (steps > 1) load(s, begin + ATTN_STEP);
+    __syncthreads();
+    for (int t = 0; t < steps; t += 2) {
+        step(t, Even{});
+        if (t + 1 < steps) step(t + 1, Odd{});
     }
     l += __shfl_xor(l, 32, 64);
     if (!real) return;
