@@ -389,8 +389,13 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
 //   O^T[dim, row]: registers 8 u .. 8 u + 7 are the weights' operand for the
 //                  keys 16 u + {4 e + 0..3, 8 + 4 e + 0..3}; the values' rows in
 //                  LDS (one a dim) hold the keys in that order.
-// While a step is computed from one half of the LDS, the next one's codes are
-// turned into the other, and those of the one after are on their way.
+// The two waves of a SIMD take turns: waves 0 .. 3 multiply (the outputs of step
+// t and the scores of step t + 1, 32 matrix instructions) while waves 4 .. 7
+// work on the vector unit (maximum and weights of a step, codes of later steps
+// into LDS), then the other way round, a barrier between the phases.  Left to
+// themselves both wait for the matrix core together and leave it idle together.
+// With waves 4 .. 7 one phase behind, and turning codes one step further ahead,
+// two halves of LDS are enough: a half is written after both have read it.
 // The running maximum moves only when a row's maximum has grown by 2^8 or more:
 // weights up to 2^8 lose nothing in bf16 and float32, and the outputs are
 // rarely scaled.
@@ -398,6 +403,14 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr float ATTN_SLACK = 8.0f;
+
+// max over lanes l and l ^ 32: the swap leaves the lower half's values in both
+// halves of one register, the upper half's in both of the other
+__device__ __forceinline__ float across_halves(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
 
 // 16-byte chunk c of row m, rows of CHUNKS chunks: neighbouring rows (reads of
 // one chunk) and rows 2 or 4 apart (writes of values) meet different banks, and
@@ -413,10 +426,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     constexpr int THREADS = 64 * WAVES, ROWS = 32 * WAVES, ROWS_LOG2 = WAVES == 8 ? 8 : 7;
     constexpr int KC = DK / 8, KK = DK / 16, DT = DV / 32;
     // keys: 8 bytes of codes (16 dims) a unit, 8 or 4 of them (a part of 128 or 64
-    // dims) side by side; values: VD dims of 8 keys a unit
+    // dims) side by side; values: 4 dims of 4 keys a unit
     constexpr int KN = DK == 192 ? 2 : 1;
-    constexpr int VD = WAVES == 8 || DV == 64 ? 2 : 4, VU = 8 * DV / VD;
-    static_assert(VU <= THREADS, "one unit of values a thread");
+    constexpr int VU = ATTN_STEP / 4 * (DV / 4);
+    static_assert(WAVES == 8 && VU <= THREADS, "one unit of values a thread, and a wave's units in one run of 16 keys");
     __shared__ v4u s_k[2][ATTN_STEP * KC];
     __shared__ v4u s_v[2][DV * 8];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, e = lane >> 5;
@@ -434,13 +447,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     const bool real = row < b.rows;
     const int qi = min(row, b.rows - 1) / group, head = h * group + min(row, b.rows - 1) % group;
     const int hi = real ? top_of(qi) : 0, lo = low_of(qi);
-    // keys of the block, and of the wave's rows: any row's [w_lo, w_hi), every row's [in_lo, in_hi)
-    const int q_last = (min(b.row0 + ROWS, b.rows) - 1) / group;
-    const int all_lo = min(low_of(b.row0 / group), b.kv), all_hi = top_of(q_last);
-    const int w_row0 = b.row0 + 32 * wave, w_rows = min(32, b.rows - w_row0);
-    const int w_first = w_row0 / group, w_last = (w_row0 + max(w_rows, 1) - 1) / group;
-    const int w_lo = low_of(w_first), w_hi = w_rows > 0 ? top_of(w_last) : 0;
-    const int in_lo = low_of(w_last), in_hi = top_of(w_first);
+    // keys that some row of the block sees, and that every row sees
+    const int q_first = b.row0 / group, q_last = (min(b.row0 + ROWS, b.rows) - 1) / group;
+    const int all_lo = min(low_of(q_first), b.kv), all_hi = top_of(q_last);
+    const int in_lo = low_of(q_last), in_hi = top_of(q_first);
     const int64_t begin64 = (all_lo & ~(ATTN_STEP - 1)) + (int64_t)split * p.chunk;
     const int end = (int)min((int64_t)all_hi, begin64 + p.chunk);
     const int64_t target = (int64_t)(b.q0 + qi) * a.q_heads + head;
@@ -467,33 +477,22 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     }
 
     // Codes of a step.  Keys: unit i of a part of P pieces is piece i % P of key
-    // i / P.  Values: thread t has dims VD (t % (DV / VD)) .. and the keys of
-    // operand chunk t / (DV / VD): two runs of 4 that lie 8 apart.  A wave's keys
-    // lie in one run of 16, so in one page, and their place is the wave's, not
-    // the lane's: 64-bit scalars and 32-bit lane offsets that no step changes.
-    struct Codes {
+    // i / P.  Values: thread t has dims 4 (t % (DV / 4)) .. of the keys 4 (t / (DV /
+    // 4)) ..  A wave's keys lie in one run of 16, so in one page, and their place
+    // is the wave's, not the lane's: 64-bit scalars and 32-bit lane offsets that
+    // no step changes.
+    struct Keys {
         v2u k[KN];
-        uint32_t ks[KN], v[8], vs[2];
+        uint32_t ks[KN];
     };
-    struct Place {
-        int64_t head;     // page * kv_heads + h
-        int at;           // row in the page
-    };
-    const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
-    auto place_of = [&](int key) {
-        const int whole = (int)divide(key, p.page);
-        const int page = min(max(table[min(whole, a.max_pages - 1)], 0), a.pages - 1);
-        Place r;
-        r.head = (int64_t)page * a.kv_heads + h;
-        r.at = key - whole * a.page_size;
-        return r;
+    struct Values {
+        uint32_t v[4], vs;
     };
     auto pieces = [](int u) { return DK == 64 || u == 1 ? 4 : 8; };
     auto k_live = [&](int u) { return THREADS == ATTN_STEP * pieces(u) || threadIdx.x < ATTN_STEP * pieces(u); };
     auto k_key = [&](int u) { return (int)threadIdx.x / pieces(u); };
     auto k_piece = [&](int u) { return 8 * u + (int)threadIdx.x % pieces(u); };
-    const int vq = threadIdx.x % (DV / VD), vc = threadIdx.x / (DV / VD);
-    const int vkey = 32 * (vc >> 2) + 16 * ((vc >> 1) & 1) + 4 * (vc & 1);
+    const int vq = threadIdx.x % (DV / 4), vkey = threadIdx.x / (DV / 4) * 4;
     // the wave's run of 16 keys of a step, by its first thread's key
     int k_run[KN], k_off[KN], ks_off[KN];
 #pragma unroll
@@ -503,75 +502,98 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
         ks_off[u] = (k_piece(u) >> 1) * a.page_size + (k_key(u) & 15);
     }
     const int v_run = __builtin_amdgcn_readfirstlane(vkey & ~15) & (ATTN_STEP - 1);
-    const int v_off = (vkey & 15) * (DV / 2) + vq * (VD / 2), vs_off = vq / (32 / VD) * a.page_size + (vkey & 15);
-    auto load = [&](Codes& s, int base) {
+    const int v_off = (vkey & 15) * (DV / 2) + vq * 2, vs_off = vq / 8 * a.page_size + (vkey & 15);
+    const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
+    // cells (a row of a head) of a page, and of the heads in front of this one
+    const int64_t page_cells = (int64_t)a.kv_heads * a.page_size, head_cells = (int64_t)h * a.page_size;
+    const uint8_t* const k_codes = a.k_codes + head_cells * (DK / 2);
+    const uint8_t* const k_scales = a.k_scales + head_cells * (DK / 32);
+    const uint8_t* const v_codes = a.v_codes + head_cells * (DV / 2);
+    const uint8_t* const v_scales = a.v_scales + head_cells * (DV / 32);
+    const int last_page = a.pages - 1, last_slot = a.max_pages - 1;
+    // The table's entry for a run of keys, and the run's row in the page; looked up
+    // a round before it is used: a scalar load waited for on the spot would stop
+    // the wave for its whole latency.
+    struct Run {
+        int entry, at;
+    };
+    auto find = [&](int key) {
+        const int whole = (int)divide(key, p.page);
+        return Run{table[min(whole, last_slot)], key - whole * a.page_size};
+    };
+    Run k_at[KN], v_at;
+    auto find_keys = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < KN; u++) k_at[u] = u > 0 && k_run[u] == k_run[0] ? k_at[0] : find(base + k_run[u]);
+    };
+    auto find_values = [&](int base) { v_at = find(base + v_run); };
+    auto load_keys = [&](Keys& s) {
 #pragma unroll
         for (int u = 0; u < KN; u++) {
-            const Place r = place_of(base + k_run[u]);
-            const uint8_t* c = a.k_codes + (r.head * a.page_size + r.at) * (DK / 2);
-            const uint8_t* sc = a.k_scales + r.head * (DK / 32) * a.page_size + r.at;
+            const int64_t cell = min(max(k_at[u].entry, 0), last_page) * page_cells;
+            const uint8_t* c = k_codes + (cell + k_at[u].at) * (DK / 2);
+            const uint8_t* sc = k_scales + cell * (DK / 32) + k_at[u].at;
             if (k_live(u)) {
                 s.k[u] = *reinterpret_cast<const v2u*>(c + (uint32_t)k_off[u]);
                 s.ks[u] = sc[(uint32_t)ks_off[u]];
             }
         }
-        const Place r = place_of(base + v_run);
-        const uint8_t* c = a.v_codes + (r.head * a.page_size + r.at) * (DV / 2);
-        const uint8_t* sc = a.v_scales + r.head * (DV / 32) * a.page_size + r.at;
+    };
+    auto load_values = [&](Values& s) {
+        const int64_t cell = min(max(v_at.entry, 0), last_page) * page_cells;
+        const uint8_t* c = v_codes + (cell + v_at.at) * (DV / 2);
+        const uint8_t* sc = v_scales + cell * (DV / 32) + v_at.at;
         if (VU == THREADS || threadIdx.x < VU) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const uint8_t* w = c + (uint32_t)v_off + (j + (j & 4)) * (DV / 2);
-                s.v[j] = VD == 4 ? (uint32_t) * reinterpret_cast<const uint16_t*>(w) : (uint32_t)*w;
-            }
-            s.vs[0] = *reinterpret_cast<const uint32_t*>(sc + (uint32_t)vs_off);
-            s.vs[1] = *reinterpret_cast<const uint32_t*>(sc + (uint32_t)vs_off + 8);
+            for (int j = 0; j < 4; j++) s.v[j] = *reinterpret_cast<const uint16_t*>(c + (uint32_t)v_off + j * (DV / 2));
+            s.vs = *reinterpret_cast<const uint32_t*>(sc + (uint32_t)vs_off);
         }
     };
-    auto turn = [&](Codes& s, int base, auto half) {
-        constexpr int buffer = decltype(half)::value;
+    auto turn_keys = [&](const Keys& s, int buffer) {
 #pragma unroll
         for (int u = 0; u < KN; u++) {
             if (k_live(u)) {
-                const int key = k_key(u), piece = k_piece(u);
                 const float scale = __builtin_bit_cast(float, s.ks[u] << 23);
-                s_k[buffer][lds_at<KC>(key, 2 * piece)] = __builtin_bit_cast(v4u, fp4x8(s.k[u][0], scale));
-                s_k[buffer][lds_at<KC>(key, 2 * piece + 1)] = __builtin_bit_cast(v4u, fp4x8(s.k[u][1], scale));
+                s_k[buffer][lds_at<KC>(k_key(u), 2 * k_piece(u))] = __builtin_bit_cast(v4u, fp4x8(s.k[u][0], scale));
+                s_k[buffer][lds_at<KC>(k_key(u), 2 * k_piece(u) + 1)] = __builtin_bit_cast(v4u, fp4x8(s.k[u][1], scale));
             }
         }
+    };
+    // A run of 4 keys is half a chunk of the values' rows: runs 0, 2 of 16 keys
+    // (e = 0) and 1, 3 (e = 1).
+    const int v_chunk = 2 * (vkey >> 4) + ((vkey >> 2) & 1), v_half = (vkey >> 3) & 1;
+    auto turn_values = [&](Values& s, int base, int buffer, bool edge) {
         if (VU == THREADS || threadIdx.x < VU) {
-            if (base + ATTN_STEP > all_hi || base < all_lo) {
+            if (edge) {
+                asm volatile("");
                 // values outside the block's keys: a scale of 2^-127 makes
                 // whatever they hold finite, and their weight of zero removes it
+                uint32_t keep = 0;
 #pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    uint32_t keep = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int key = base + vkey + 8 * r + i;
-                        if (key < all_hi && key >= all_lo) keep |= 0xFFu << (8 * i);
-                    }
-                    s.vs[r] &= keep;
+                for (int i = 0; i < 4; i++) {
+                    const int key = base + vkey + i;
+                    if (key < all_hi && key >= all_lo) keep |= 0xFFu << (8 * i);
                 }
+                s.vs &= keep;
             }
-            const float sc[8] = {scale_of<0>(s.vs[0]), scale_of<1>(s.vs[0]), scale_of<2>(s.vs[0]), scale_of<3>(s.vs[0]),
-                                 scale_of<0>(s.vs[1]), scale_of<1>(s.vs[1]), scale_of<2>(s.vs[1]), scale_of<3>(s.vs[1])};
+            const float sc[4] = {scale_of<0>(s.vs), scale_of<1>(s.vs), scale_of<2>(s.vs), scale_of<3>(s.vs)};
             auto pair = [&](auto sel) {
                 constexpr int SEL = decltype(sel)::value;
-                uint32_t x[8];
+                uint32_t x[4];
 #pragma unroll
-                for (int j = 0; j < 8; j++) x[j] = fp4x2<SEL>(s.v[j], sc[j]);
-                v4u even, odd;
+                for (int j = 0; j < 4; j++) x[j] = fp4x2<SEL>(s.v[j], sc[j]);
+                v2u even, odd;
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
+                for (int j = 0; j < 2; j++) {
                     even[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x05040100u);
                     odd[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x07060302u);
                 }
-                s_v[buffer][lds_at<8>(VD * vq + 2 * SEL, vc)] = even;
-                s_v[buffer][lds_at<8>(VD * vq + 2 * SEL + 1, vc)] = odd;
+                v2u* const rows = reinterpret_cast<v2u*>(s_v[buffer]) + v_half;
+                rows[2 * lds_at<8>(4 * vq + 2 * SEL, v_chunk)] = even;
+                rows[2 * lds_at<8>(4 * vq + 2 * SEL + 1, v_chunk)] = odd;
             };
             pair(std::integral_constant<int, 0>{});
-            if constexpr (VD == 4) pair(std::integral_constant<int, 1>{});
+            pair(std::integral_constant<int, 1>{});
         }
     };
 
@@ -582,78 +604,140 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
         for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
     float m = -INFINITY, l = 0.0f;
 
-    Codes s;
-    auto step = [&](int t, auto half) {
-        constexpr int buffer = decltype(half)::value;
-        const int base = begin + t * ATTN_STEP;
-        if (t + 1 < steps) turn(s, base + ATTN_STEP, std::integral_constant<int, buffer ^ 1>{});
-        if (t + 2 < steps) load(s, base + 2 * ATTN_STEP);
-        if (base < w_hi && base + ATTN_STEP > w_lo) {
-            v16f acc[2];
-            const v16f zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    auto scores = [&](v16f (&acc)[2], int buffer) {
+        const v16f zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-            for (int j = 0; j < KK; j++)
+        for (int j = 0; j < KK; j++)
 #pragma unroll
-                for (int x = 0; x < 2; x++)
-                    acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        __builtin_bit_cast(bf16x8, s_k[buffer][lds_at<KC>(n, 2 * j + e) + 32 * KC * x]), q[j], j ? acc[x] : zero, 0, 0, 0);
-            if (base + ATTN_STEP > min(in_hi, end) || base < in_lo) {
-                const int top = min(hi, end);
-#pragma unroll
-                for (int x = 0; x < 2; x++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const int key = base + 32 * x + 8 * (i >> 2) + 4 * e + (i & 3);
-                        if (key >= top || key < lo) acc[x][i] = -INFINITY;
-                    }
-            }
-            float top = acc[0][0];
+            for (int x = 0; x < 2; x++)
+                acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, s_k[buffer][lds_at<KC>(n, 2 * j + e) + 32 * KC * x]), q[j], j ? acc[x] : zero, 0, 0, 0);
+    };
+    // the largest score of the lane's half of its row, after the mask of an edge step
+    auto largest = [&](v16f (&acc)[2], int base, bool edge) {
+        if (edge) {
+            asm volatile("");        // a branch: the compiler would compare every score of every step
+            const int from = lo - base - 4 * e, to = min(hi, end) - base - 4 * e;
 #pragma unroll
             for (int x = 0; x < 2; x++)
 #pragma unroll
-                for (int i = 0; i < 16; i++) top = __builtin_fmaxf(top, acc[x][i]);
-            top = __builtin_fmaxf(top, __shfl_xor(top, 32, 64)) * c2;
-            if (__any(top > m + ATTN_SLACK)) {
-                const float m_new = __builtin_fmaxf(m, top);
-                const float alpha = __builtin_amdgcn_exp2f(m - (m_new == -INFINITY ? 0.0f : m_new));
-                m = m_new;
-                l *= alpha;
-#pragma unroll
-                for (int d = 0; d < DT; d++) o[d] *= alpha;
-            }
-            const float m_use = m == -INFINITY ? 0.0f : m;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            bf16x8 w[4];
-#pragma unroll
-            for (int u = 0; u < 4; u++) {
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u >> 1][8 * (u & 1) + i], c2, -m_use));
-                    sum[i & 3] += x[i];
+                for (int i = 0; i < 16; i++) {
+                    const int key = 32 * x + 8 * (i >> 2) + (i & 3);
+                    if (key >= to || key < from) acc[x][i] = -INFINITY;
                 }
-                const v4u r = {bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]), bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7])};
-                w[u] = __builtin_bit_cast(bf16x8, r);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-#pragma unroll
-            for (int u = 0; u < 4; u++)
-#pragma unroll
-                for (int d = 0; d < DT; d++)
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                        __builtin_bit_cast(bf16x8, s_v[buffer][lds_at<8>(n, 2 * u + e) + 32 * 8 * d]), w[u], o[d], 0, 0, 0);
         }
-        __syncthreads();
+        float top = acc[0][0];
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) top = __builtin_fmaxf(top, acc[x][i]);
+        return top;
     };
-    typedef std::integral_constant<int, 0> Even;
-    typedef std::integral_constant<int, 1> Odd;
-    if (steps > 0) load(s, begin);
-    if (steps > 0) turn(s, begin, Even{});
-    if (steps > 1) load(s, begin + ATTN_STEP);
-    __syncthreads();
-    for (int t = 0; t < steps; t += 2) {
-        step(t, Even{});
-        if (t + 1 < steps) step(t + 1, Odd{});
+    // the row's maximum moves to the new largest score where that is far above it
+    auto raise = [&](float top) {
+        top = across_halves(top) * c2;
+        if (__any(top > m + ATTN_SLACK)) {
+            const float m_new = __builtin_fmaxf(m, top);
+            const float alpha = __builtin_amdgcn_exp2f(m - (m_new == -INFINITY ? 0.0f : m_new));
+            m = m_new;
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < DT; d++) o[d] *= alpha;
+        }
+    };
+    auto weights = [&](const v16f (&acc)[2], bf16x8 (&w)[4]) {
+        const float m_use = m == -INFINITY ? 0.0f : m;      // a row that has seen nothing yet
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[u >> 1][8 * (u & 1) + i], c2, -m_use));
+                sum[i & 3] += x[i];
+            }
+            const v4u r = {bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]), bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7])};
+            w[u] = __builtin_bit_cast(bf16x8, r);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    };
+    auto outputs = [&](const bf16x8 (&w)[4], int buffer) {
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+#pragma unroll
+            for (int d = 0; d < DT; d++)
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, s_v[buffer][lds_at<8>(n, 2 * u + e) + 32 * 8 * d]), w[u], o[d], 0, 0, 0);
+    };
+
+    if (steps > 0) {
+        // steps [j0, j1) lie inside what every row of the block sees
+        const int j0 = in_lo > begin ? (in_lo - begin + ATTN_STEP - 1) / ATTN_STEP : 0;
+        const int j1 = min(in_hi, end) > begin ? (min(in_hi, end) - begin) / ATTN_STEP : 0;
+        auto base_of = [&](int t) { return begin + t * ATTN_STEP; };
+        auto edge = [&](int t) { return t < j0 || t >= j1; };
+        const int late = wave >= WAVES / 2;      // the waves one phase behind
+        Keys keys;
+        Values values;
+        v16f acc[2];
+        bf16x8 w[4];
+        find_keys(base_of(0));
+        find_values(base_of(0));
+        load_keys(keys);
+        load_values(values);
+        find_keys(base_of(1));
+        find_values(base_of(1));
+        turn_keys(keys, 0);
+        load_keys(keys);
+        find_keys(base_of(2));
+        turn_values(values, base_of(0), 0, true);
+        load_values(values);
+        find_values(base_of(2));
+        turn_keys(keys, 1);
+        load_keys(keys);
+        find_keys(base_of(3));
+        __syncthreads();
+        scores(acc, 0);
+        raise(largest(acc, base_of(0), true));
+        weights(acc, w);
+        __syncthreads();
+        // codes of the keys of step t + 2 + late and the values of t + 1 + late
+        // into LDS, the next ones into registers
+        auto turn = [&](int t) {
+            turn_keys(keys, (t + late) & 1);
+            turn_values(values, base_of(t + 1 + late), (t + 1 + late) & 1, edge(t + 1 + late));
+            load_keys(keys);             // of step t + 3 + late
+            load_values(values);         // of step t + 2 + late
+            find_keys(base_of(t + 4 + late));
+            find_values(base_of(t + 3 + late));
+        };
+        if (late) {
+            turn(-1);
+            __syncthreads();
+        }
+        for (int t = 0; t + 1 < steps; t++) {
+            __builtin_amdgcn_s_setprio(1);
+            outputs(w, t & 1);
+            scores(acc, (t + 1) & 1);
+            // operands 8 reads ahead of the products: the compiler's own order
+            // waits for each pair of reads
+            constexpr int READS = 4 * DT + 2 * KK, READ_AHEAD = 8;
+            __builtin_amdgcn_sched_group_barrier(0x100, READ_AHEAD, 0);
+#pragma unroll
+            for (int i = 0; i < READS - READ_AHEAD; i++) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, READ_AHEAD, 0);
+            __builtin_amdgcn_s_setprio(0);
+            __syncthreads();
+            raise(largest(acc, base_of(t + 1), edge(t + 1)));
+            weights(acc, w);
+            turn(t);
+            __syncthreads();
+        }
+        outputs(w, (steps - 1) & 1);
+        if (!late) __syncthreads();
     }
     l += __shfl_xor(l, 32, 64);
     if (!real) return;
