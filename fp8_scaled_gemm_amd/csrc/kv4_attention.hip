@@ -168,19 +168,28 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
         }
     }
 
-    const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
-    auto page_of = [&](int key, int& at) {   // at: the key's row in its page
-        const int slot = min((int)divide(key, p.page), a.max_pages - 1);
-        at = key - (int)divide(key, p.page) * a.page_size;
-        return min(max(table[slot], 0), a.pages - 1);
+    // A lane's four keys and its run of 16 for the values: their pages, looked up
+    // a step before the codes are asked for
+    struct Run {
+        int entry, at;
     };
+    const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
+    auto find = [&](int key) {
+        const int whole = (int)divide(key, p.page);
+        return Run{table[min(whole, a.max_pages - 1)], key - whole * a.page_size};
+    };
+    auto head_of = [&](const Run& r) { return (int64_t)min(max(r.entry, 0), a.pages - 1) * a.kv_heads + h; };
     typedef AttnStep<DK, DV> Step;
-    auto load = [&](Step& s, int base) {
-        int at;
+    Run k_at, v_at;
+    auto look = [&](int base) {
+        k_at = find(base + 4 * n);
+        v_at = find(base + 16 * g);
+    };
+    auto load = [&](Step& s) {
         {
-            const int64_t ph = (int64_t)page_of(base + 4 * n, at) * a.kv_heads + h;
-            const uint8_t* c = a.k_codes + (ph * a.page_size + at) * (DK / 2);
-            const uint8_t* sc = a.k_scales + ph * (DK / 32) * a.page_size + at;
+            const int64_t ph = head_of(k_at);
+            const uint8_t* c = a.k_codes + (ph * a.page_size + k_at.at) * (DK / 2);
+            const uint8_t* sc = a.k_scales + ph * (DK / 32) * a.page_size + k_at.at;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const uint8_t* r = c + i * (DK / 2);
@@ -200,9 +209,9 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
             s.ks[0] = *reinterpret_cast<const uint32_t*>(sc + (DK == 64 ? g >> 1 : g) * a.page_size);
             if constexpr (DK == 192) s.ks[1] = *reinterpret_cast<const uint32_t*>(sc + (4 + (g >> 1)) * a.page_size);
         }
-        const int64_t ph = (int64_t)page_of(base + 16 * g, at) * a.kv_heads + h;
-        const uint8_t* c = a.v_codes + (ph * a.page_size + at) * (DV / 2);
-        const uint8_t* sc = a.v_scales + ph * (DV / 32) * a.page_size + at;
+        const int64_t ph = head_of(v_at);
+        const uint8_t* c = a.v_codes + (ph * a.page_size + v_at.at) * (DV / 2);
+        const uint8_t* sc = a.v_scales + ph * (DV / 32) * a.page_size + v_at.at;
 #pragma unroll
         for (int i = 0; i < 16; i++) {
             if constexpr (DV == 64)
@@ -221,10 +230,17 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
 
     Step s;
     int base = (int)begin + ATTN_STEP * wave;
-    if (base < end) load(s, base);
+    if (base < end) {
+        look(base);
+        load(s);
+        look(base + ATTN_CHUNK);        // behind the last page: its last entry, unused
+    }
     for (; base < end; base += ATTN_CHUNK) {
         Step next;
-        if (base + ATTN_CHUNK < end) load(next, base + ATTN_CHUNK);
+        if (base + ATTN_CHUNK < end) {
+            load(next);
+            look(base + 2 * ATTN_CHUNK);
+        }
         // scores
         v4f acc[4];
 #pragma unroll
@@ -512,14 +528,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     const uint8_t* const v_scales = a.v_scales + head_cells * (DV / 32);
     const int last_page = a.pages - 1, last_slot = a.max_pages - 1;
     // The table's entry for a run of keys, and the run's row in the page; looked up
-    // a round before it is used: a scalar load waited for on the spot would stop
-    // the wave for its whole latency.
+    // a round before it is used.  The entry stays in a vector register until then:
+    // were it known to be the wave's, the compiler would move it to a scalar at
+    // once and wait for it on the spot, a memory latency a round.
     struct Run {
         int entry, at;
     };
+    int zero;
+    asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
     auto find = [&](int key) {
         const int whole = (int)divide(key, p.page);
-        return Run{table[min(whole, last_slot)], key - whole * a.page_size};
+        return Run{table[min(whole, last_slot) + zero], key - whole * a.page_size};
+    };
+    auto page_cell = [&](const Run& r) {
+        return min(max(__builtin_amdgcn_readfirstlane(r.entry), 0), last_page) * page_cells;
     };
     Run k_at[KN], v_at;
     auto find_keys = [&](int base) {
@@ -530,7 +552,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     auto load_keys = [&](Keys& s) {
 #pragma unroll
         for (int u = 0; u < KN; u++) {
-            const int64_t cell = min(max(k_at[u].entry, 0), last_page) * page_cells;
+            const int64_t cell = page_cell(k_at[u]);
             const uint8_t* c = k_codes + (cell + k_at[u].at) * (DK / 2);
             const uint8_t* sc = k_scales + cell * (DK / 32) + k_at[u].at;
             if (k_live(u)) {
@@ -540,7 +562,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
         }
     };
     auto load_values = [&](Values& s) {
-        const int64_t cell = min(max(v_at.entry, 0), last_page) * page_cells;
+        const int64_t cell = page_cell(v_at);
         const uint8_t* c = v_codes + (cell + v_at.at) * (DV / 2);
         const uint8_t* sc = v_scales + cell * (DV / 32) + v_at.at;
         if (VU == THREADS || threadIdx.x < VU) {
