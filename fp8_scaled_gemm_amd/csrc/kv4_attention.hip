@@ -47,6 +47,7 @@ constexpr int ATTN_THREADS = 256;
 constexpr int ATTN_ROWS_LOG2 = 4, ATTN_ROWS = 1 << ATTN_ROWS_LOG2;
 constexpr int ATTN_STEP = 64;                      // keys of a wave's step
 constexpr int ATTN_CHUNK = 4 * ATTN_STEP;          // keys of a workgroup's step
+constexpr float ATTN_SLACK = 8.0f;                 // growth of a maximum that is left to the weights, in powers of two
 
 // n / d for n < 2^31 by a multiply: q = (mulhi(n, mul) + n) >> shift
 struct FastDiv {
@@ -85,9 +86,18 @@ __device__ __forceinline__ float scale_of(uint32_t w) {
     else r = (w << 23) & 0x7F800000u;
     return __builtin_bit_cast(float, r);
 }
+// max over lanes l and l ^ 32: the swap leaves the lower half's values in both
+// halves of one register, the upper half's in both of the other
+__device__ __forceinline__ float across_halves(float v) {
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
 __device__ __forceinline__ float over_groups_max(float v) {
-    v = __builtin_fmaxf(v, __shfl_xor(v, 16, 64));
-    return __builtin_fmaxf(v, __shfl_xor(v, 32, 64));
+    const uint32_t u = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);    // lanes l and l ^ 16
+    return across_halves(__builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1])));
 }
 __device__ __forceinline__ float over_groups_sum(float v) {
     v += __shfl_xor(v, 16, 64);
@@ -157,39 +167,58 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
         return;
     }
 
+    // A negative scale turns the queries' signs, so that the largest product is
+    // the largest score; a scale of zero becomes one that changes nothing and
+    // keeps -inf * scale at -inf.
+    const float c2 = __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, 0x1p-120f);
     // queries: dims in the order of the keys' pieces
     bf16x8 q[KW];
     {
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
         const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(b.q0 + qi) * a.q_stride + (int64_t)head * DK;
 #pragma unroll
         for (int j = 0; j < KW; j++) {
             const int d = DK == 64 ? 16 * g + 8 * j : (j < 4 ? 32 * g + 8 * j : 128 + 16 * g + 8 * (j - 4));
-            q[j] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const v4u*>(src + d));
+            const v4u w = *reinterpret_cast<const v4u*>(src + d);
+            q[j] = __builtin_bit_cast(bf16x8, v4u{w[0] ^ flip, w[1] ^ flip, w[2] ^ flip, w[3] ^ flip});
         }
     }
 
-    // A lane's four keys and its run of 16 for the values: their pages, looked up
-    // a step before the codes are asked for
+    // A lane's four keys and its run of 16 for the values: their pages' entries
+    // are asked for a step before the codes, and in front of the codes of the
+    // step before, so that waiting for them does not wait for those.
     struct Run {
         int entry, at;
     };
     const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
+    // cells (a row of a head) of a page, and of the heads in front of this one
+    const uint32_t page_cells = (uint32_t)a.kv_heads * a.page_size;
+    const int64_t head_cells = (int64_t)h * a.page_size;
+    const uint8_t* const k_codes = a.k_codes + head_cells * (DK / 2);
+    const uint8_t* const k_scales = a.k_scales + head_cells * (DK / 32);
+    const uint8_t* const v_codes = a.v_codes + head_cells * (DV / 2);
+    const uint8_t* const v_scales = a.v_scales + head_cells * (DV / 32);
+    const int last_page = a.pages - 1, last_slot = a.max_pages - 1;
+    const int ks0 = (DK == 64 ? g >> 1 : g) * a.page_size, ks1 = (4 + (g >> 1)) * a.page_size;
+    const int vs0 = (DV == 64 ? n >> 3 : n >> 2) * a.page_size;
     auto find = [&](int key) {
         const int whole = (int)divide(key, p.page);
-        return Run{table[min(whole, a.max_pages - 1)], key - whole * a.page_size};
+        return Run{table[min(whole, last_slot)], key - whole * a.page_size};
     };
-    auto head_of = [&](const Run& r) { return (int64_t)min(max(r.entry, 0), a.pages - 1) * a.kv_heads + h; };
+    auto cell_of = [&](const Run& r) { return (uint64_t)(uint32_t)min(max(r.entry, 0), last_page) * page_cells; };
     typedef AttnStep<DK, DV> Step;
     Run k_at, v_at;
     auto look = [&](int base) {
         k_at = find(base + 4 * n);
         v_at = find(base + 16 * g);
     };
-    auto load = [&](Step& s) {
+    auto load = [&](Step& s, int base) {
+        const Run kr = k_at, vr = v_at;
+        look(base + ATTN_CHUNK);        // behind the last page: its last entry, unused
         {
-            const int64_t ph = head_of(k_at);
-            const uint8_t* c = a.k_codes + (ph * a.page_size + k_at.at) * (DK / 2);
-            const uint8_t* sc = a.k_scales + ph * (DK / 32) * a.page_size + k_at.at;
+            const uint64_t cell = cell_of(kr);
+            const uint8_t* c = k_codes + (cell + kr.at) * (DK / 2);
+            const uint8_t* sc = k_scales + cell * (DK / 32) + kr.at;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const uint8_t* r = c + i * (DK / 2);
@@ -206,12 +235,12 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
                     }
                 }
             }
-            s.ks[0] = *reinterpret_cast<const uint32_t*>(sc + (DK == 64 ? g >> 1 : g) * a.page_size);
-            if constexpr (DK == 192) s.ks[1] = *reinterpret_cast<const uint32_t*>(sc + (4 + (g >> 1)) * a.page_size);
+            s.ks[0] = *reinterpret_cast<const uint32_t*>(sc + ks0);
+            if constexpr (DK == 192) s.ks[1] = *reinterpret_cast<const uint32_t*>(sc + ks1);
         }
-        const int64_t ph = head_of(v_at);
-        const uint8_t* c = a.v_codes + (ph * a.page_size + v_at.at) * (DV / 2);
-        const uint8_t* sc = a.v_scales + ph * (DV / 32) * a.page_size + v_at.at;
+        const uint64_t cell = cell_of(vr);
+        const uint8_t* c = v_codes + (cell + vr.at) * (DV / 2);
+        const uint8_t* sc = v_scales + cell * (DV / 32) + vr.at;
 #pragma unroll
         for (int i = 0; i < 16; i++) {
             if constexpr (DV == 64)
@@ -219,28 +248,15 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
             else
                 s.v[i] = *reinterpret_cast<const uint32_t*>(c + i * (DV / 2) + 4 * n);
         }
-        s.vs = *reinterpret_cast<const v4u*>(sc + (DV == 64 ? n >> 3 : n >> 2) * a.page_size);
+        s.vs = *reinterpret_cast<const v4u*>(sc + vs0);
     };
 
     v4f o[DT];
 #pragma unroll
     for (int d = 0; d < DT; d++) o[d] = v4f{0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
-    const float c2 = a.scale * 1.4426950408889634f;   // scores in powers of two
 
-    Step s;
-    int base = (int)begin + ATTN_STEP * wave;
-    if (base < end) {
-        look(base);
-        load(s);
-        look(base + ATTN_CHUNK);        // behind the last page: its last entry, unused
-    }
-    for (; base < end; base += ATTN_CHUNK) {
-        Step next;
-        if (base + ATTN_CHUNK < end) {
-            load(next);
-            look(base + 2 * ATTN_CHUNK);
-        }
+    auto step = [&](Step& s, int base) {
         // scores
         v4f acc[4];
 #pragma unroll
@@ -262,12 +278,8 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
             }
         }
         // acc[i][r]: key base + 16 g + 4 r + i of row n
-        float w[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) w[i][r] = acc[i][r] * c2;
         if (base + ATTN_STEP > in_hi || base < in_lo || base + ATTN_STEP > end) {
+            asm volatile("");       // a branch: the compiler would compare every score of every step
             // a step that some row sees only a part of.  Values outside the
             // block's keys get a scale of 2^-127: whatever their bytes hold is
             // then finite, and a weight of zero removes it.
@@ -277,7 +289,7 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
                     const int key = base + 16 * g + 4 * r + i;
-                    if (key >= top || key < lo) w[i][r] = -INFINITY;
+                    if (key >= top || key < lo) acc[i][r] = -INFINITY;
                 }
 #pragma unroll
             for (int r = 0; r < 4; r++) {
@@ -290,26 +302,30 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
                 s.vs[r] &= keep;
             }
         }
-        float top = w[0][0];
+        float top = acc[0][0];
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) top = __builtin_fmaxf(top, w[i][r]);
-        const float m_new = __builtin_fmaxf(m, over_groups_max(top));
-        const float m_use = m_new == -INFINITY ? 0.0f : m_new;   // a row that has seen nothing yet
-        const float alpha = __builtin_amdgcn_exp2f(m - m_use);
-        m = m_new;
-        float sum = 0.0f;
+            for (int r = 0; r < 4; r++) top = __builtin_fmaxf(top, acc[i][r]);
+        top = over_groups_max(top) * c2;
+        // the maximum moves where a row's has grown by 2^8: weights up to that
+        // lose nothing, and the outputs are rarely scaled
+        if (__any(top > m + ATTN_SLACK)) {
+            const float m_new = __builtin_fmaxf(m, top);
+            const float alpha = __builtin_amdgcn_exp2f(m - (m_new == -INFINITY ? 0.0f : m_new));
+            m = m_new;
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < DT; d++) o[d] *= alpha;
+        }
+        const float m_use = m == -INFINITY ? 0.0f : m;      // a row that has seen nothing yet
+        float w[4][4];
 #pragma unroll
         for (int i = 0; i < 4; i++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                w[i][r] = __builtin_amdgcn_exp2f(w[i][r] - m_use);
-                sum += w[i][r];
-            }
-        l = l * alpha + sum;
+            for (int r = 0; r < 4; r++) w[i][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][r], c2, -m_use));
 #pragma unroll
-        for (int d = 0; d < DT; d++) o[d] *= alpha;
+        for (int r = 0; r < 4; r++) l += (w[0][r] + w[1][r]) + (w[2][r] + w[3][r]);
         // values: 8 keys (16 g + 8 u ..) at a time
 #pragma unroll
         for (int u = 0; u < 2; u++) {
@@ -344,7 +360,24 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
                 pair(std::integral_constant<int, 3>{});
             }
         }
-        s = next;
+    };
+    // two steps' codes in flight, each step's asked for as soon as its place is free
+    Step even, odd;
+    int base = (int)begin + ATTN_STEP * wave;
+    if (base < end) {
+        look(base);
+        load(even, base);
+        if (base + ATTN_CHUNK < end) load(odd, base + ATTN_CHUNK);
+        while (true) {
+            step(even, base);
+            if (base + 2 * ATTN_CHUNK < end) load(even, base + 2 * ATTN_CHUNK);
+            base += ATTN_CHUNK;
+            if (base >= end) break;
+            step(odd, base);
+            if (base + 2 * ATTN_CHUNK < end) load(odd, base + 2 * ATTN_CHUNK);
+            base += ATTN_CHUNK;
+            if (base >= end) break;
+        }
     }
     // join the waves: o[d][r] is dim DT (4 g + r) + d of row n
     l = over_groups_sum(l);
@@ -417,16 +450,6 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
 // rarely scaled.
 
 typedef float v16f __attribute__((ext_vector_type(16)));
-
-constexpr float ATTN_SLACK = 8.0f;
-
-// max over lanes l and l ^ 32: the swap leaves the lower half's values in both
-// halves of one register, the upper half's in both of the other
-__device__ __forceinline__ float across_halves(float v) {
-    const uint32_t u = __builtin_bit_cast(uint32_t, v);
-    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
-}
 
 // 16-byte chunk c of row m, rows of CHUNKS chunks: neighbouring rows (reads of
 // one chunk) and rows 2 or 4 apart (writes of values) meet different banks, and
