@@ -140,7 +140,9 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
     __shared__ float s_m[4][ATTN_ROWS], s_l[4][ATTN_ROWS];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int group = a.q_heads / a.kv_heads;
-    const int split = blockIdx.x % p.splits, rest = blockIdx.x / p.splits;
+    // Chunk by chunk: workgroups go to the XCDs in turn, and later chunks, which
+    // shorter sequences do not have, would otherwise all fall to the same ones.
+    const int blocks = p.ids * a.kv_heads, split = blockIdx.x / blocks, rest = blockIdx.x - split * blocks;
     const int h = rest % a.kv_heads, id = rest / a.kv_heads;
     AttnBlock b;
     if (!attn_block<ATTN_ROWS_LOG2>(a, group, id, b)) return;
@@ -473,8 +475,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     __shared__ v4u s_v[2][DV * 8];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, e = lane >> 5;
     const int group = a.q_heads / a.kv_heads;
-    // long blocks (the last rows of a sequence see the most keys) first
-    const int split = blockIdx.x % p.splits, rest = blockIdx.x / p.splits;
+    // chunk by chunk, and long blocks (the last rows of a sequence see the most
+    // keys) first
+    const int blocks = p.ids * a.kv_heads, split = blockIdx.x / blocks, rest = blockIdx.x - split * blocks;
     const int h = rest % a.kv_heads, id = p.ids - 1 - rest / a.kv_heads;
     AttnBlock b;
     if (!attn_block<ROWS_LOG2>(a, group, id, b)) return;
