@@ -826,17 +826,33 @@ __global__ __launch_bounds__(ATTN_THREADS) void kv4_attention_join_kernel(Kv4Att
     if (query < a.q_start[0] || query >= a.q_start[a.batch]) return;   // of no sequence
     const float* part_o = a.workspace + row * p.splits * DV + 4 * lane;
     const float* part_ml = a.workspace + rows * p.splits * DV + row * p.splits * 2;
-    float m = -INFINITY;
-    for (int s = 0; s < p.splits; s++) m = __builtin_fmaxf(m, part_ml[2 * s]);
-    const float mu = m == -INFINITY ? 0.0f : m;
+    constexpr int AHEAD = 8;            // chunks in flight
+    float m = -INFINITY, l = 0.0f;
     v4f o = {0, 0, 0, 0};
-    float l = 0.0f;
-    for (int s = 0; s < p.splits; s++) {
-        const float ms = part_ml[2 * s];
-        if (ms == -INFINITY) continue;      // an empty chunk has written no more than this
-        const float f = __builtin_amdgcn_exp2f(ms - mu);
-        l += part_ml[2 * s + 1] * f;
-        o += *reinterpret_cast<const v4f*>(part_o + (int64_t)s * DV) * f;
+    for (int s0 = 0; s0 < p.splits; s0 += AHEAD) {
+        float ms[AHEAD], ls[AHEAD];
+        v4f os[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++) {
+            const int s = min(s0 + u, p.splits - 1);
+            ms[u] = part_ml[2 * s], ls[u] = part_ml[2 * s + 1];
+            os[u] = *reinterpret_cast<const v4f*>(part_o + (int64_t)s * DV);
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++)
+            if (s0 + u < p.splits) top = __builtin_fmaxf(top, ms[u]);
+        const float mu = top == -INFINITY ? 0.0f : top, f0 = __builtin_amdgcn_exp2f(m - mu);
+        l *= f0, o *= f0;
+        m = top;
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++) {
+            // an empty chunk has written -inf and no more: the rest may be anything
+            if (s0 + u >= p.splits || ms[u] == -INFINITY) continue;
+            const float f = __builtin_amdgcn_exp2f(ms[u] - mu);
+            l += ls[u] * f;
+            o += os[u] * f;
+        }
     }
     const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
     *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.out) + row * DV + 4 * lane) =
@@ -865,7 +881,7 @@ static AttnPlan attn_plan(const Kv4AttnArgs& a) {
     const int some = a.batch < a.queries ? a.batch : a.queries;
     if (blocks < some) blocks = some;
     blocks *= a.kv_heads;
-    const int64_t full = wide ? 512 : 2048;     // workgroups that fill the chip
+    const int64_t full = wide ? 512 : 1024;     // workgroups that fill the chip
     int64_t want = blocks >= full ? 1 : full / blocks;
     const int64_t most = ((int64_t)1 << 30) / ((int64_t)p.ids * a.kv_heads);   // keeps the grid's size an int
     if (want > most) want = most < 1 ? 1 : most;
