@@ -49,19 +49,6 @@ constexpr int ATTN_STEP = 64;                      // keys of a wave's step
 constexpr int ATTN_CHUNK = 4 * ATTN_STEP;          // keys of a workgroup's step
 constexpr float ATTN_SLACK = 8.0f;                 // growth of a maximum that is left to the weights, in powers of two
 
-// n / d for n < 2^31 by a multiply: q = (mulhi(n, mul) + n) >> shift
-struct FastDiv {
-    uint32_t mul, shift;
-};
-static FastDiv fast_div(uint32_t d) {
-    FastDiv f;
-    f.shift = 0;
-    while ((1ull << f.shift) < d) f.shift++;
-    f.mul = (uint32_t)((((1ull << f.shift) - d) << 32) / d + 1);
-    return f;
-}
-__device__ __forceinline__ uint32_t divide(uint32_t n, FastDiv f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
-
 struct AttnPlan {
     int ids, chunk, splits;
     FastDiv page;

@@ -1,4 +1,5 @@
-// Row blocks of ragged sequences, found on the device (gfx950 only).
+// Row blocks of ragged sequences, found on the device, and division by a number
+// that a launch knows (gfx950 only).
 //
 // Sequence b owns the rows start[b] * mult .. start[b + 1] * mult - 1 of a
 // launch; a workgroup handles a block of `rows` of them.  How many blocks a
@@ -45,5 +46,18 @@ __device__ __forceinline__ Sequence find_sequence(Start start, Word word, int co
     s.index = __builtin_amdgcn_readfirstlane(s.index);
     return s;
 }
+
+// n / d for n < 2^31 by a multiply: (mulhi(n, mul) + n) >> shift
+struct FastDiv {
+    uint32_t mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+    FastDiv f;
+    f.shift = 0;
+    while ((1ull << f.shift) < d) f.shift++;
+    f.mul = (uint32_t)((((1ull << f.shift) - d) << 32) / d + 1);
+    return f;
+}
+__device__ __forceinline__ uint32_t divide(uint32_t n, FastDiv f) { return (__umulhi(n, f.mul) + n) >> f.shift; }
 
 }  // namespace fp8g
