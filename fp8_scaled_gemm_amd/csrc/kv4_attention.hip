@@ -16,16 +16,21 @@
 // never leave their lane:
 //   S^T[key, row] = K Q^T,   O^T[dim, row] = V^T P^T
 // with the row as the matrix core's N: lane l holds row l % 16, g = l / 16.
-// * Keys: lane (m, g) is row m of the first operand.  It loads the 16 bytes of
+// * Keys: lane (m, g) is row m of the first operand and takes the 16 bytes of
 //   dims 32 g .. 32 g + 31 (one scale) of a key; the four 8-dim pieces are its
 //   operands of four products.  The order of dims along K is free as long as
 //   the queries follow it.
 // * In a step of 64 keys, product tile i (of 4) takes keys 4 m + i: the lane's
 //   four keys are neighbours (4 scales in one load), and the result holds, in
 //   lane group g, the 16 neighbouring keys 16 g + 4 r + i.
-// * Values: lane (m, g) loads dims 8 m .. 8 m + 7 of those 16 keys (4 bytes
+// * Values: lane (m, g) takes dims 8 m .. 8 m + 7 of those 16 keys (4 bytes
 //   each, 16 scales in one load) and turns 8 keys x 8 dims into eight operands
 //   with one convert and one byte permute for each pair of elements.
+// * Codes come as they lie in memory, 16 keys of a head in one run of 512 to 1536
+//   bytes, and each wave turns them around in LDS of its own: loads in operand
+//   order touch 64 places each and kept the address unit of a CU busier than
+//   its memory.  While a step is computed from LDS the next one's codes travel
+//   into the registers that it came from.
 // E2M1 with a power-of-two scale is exact in bf16, one convert instruction for
 // two elements; only the softmax weights are rounded (to bf16).
 
@@ -110,21 +115,28 @@ __device__ __forceinline__ bool attn_block(const Kv4AttnArgs& a, int group, int 
     return b.row0 < b.rows;
 }
 
+// A wave's codes of a step in LDS.  Keys: 16-byte chunks, exchanged within groups
+// of 8 or 16 so that reads of one chunk of keys 4 apart meet different banks.
+// Values: a run of 16 keys and 64 bytes, so that the four runs do, too.
 template <int DK, int DV>
-struct AttnStep {
-    // one step's codes and scales, as loaded
-    static constexpr int KW = DK / 32;    // dwords of a lane's piece of a key
-    uint32_t k[4][KW];
-    uint32_t ks[DK == 192 ? 2 : 1];
-    uint32_t v[16];
-    v4u vs;
+struct AttnTile {
+    static constexpr int K_CHUNKS = DK / 32, K_BYTES = ATTN_STEP * DK / 2;
+    static constexpr int V_RUN = 16 * DV / 2 + 64, BYTES = K_BYTES + 4 * V_RUN;
+    static __device__ __forceinline__ int key_at(int chunk) {      // chunk = key * K_CHUNKS + c
+        const int m = chunk / (4 * K_CHUNKS);
+        return 16 * (DK == 128 ? chunk ^ (m & 15) : chunk ^ ((m >> 1) & 7));
+    }
 };
 
 template <int DK, int DV, bool SPLIT>
 __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnArgs a, AttnPlan p) {
     constexpr int KW = DK / 32, DT = DV / 16;   // products along the head dim; 16-dim tiles of the output
-    __shared__ float s_o[4][ATTN_ROWS][DV + 4];
+    typedef AttnTile<DK, DV> Tile;
+    // the waves' tiles; at the end their outputs
+    constexpr int SHARED = 4 * Tile::BYTES > 4 * ATTN_ROWS * (DV + 4) * 4 ? 4 * Tile::BYTES : 4 * ATTN_ROWS * (DV + 4) * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t shared[SHARED];
     __shared__ float s_m[4][ATTN_ROWS], s_l[4][ATTN_ROWS];
+    float(*const s_o)[ATTN_ROWS][DV + 4] = reinterpret_cast<float(*)[ATTN_ROWS][DV + 4]>(shared);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int group = a.q_heads / a.kv_heads;
     // Chunk by chunk: workgroups go to the XCDs in turn, and later chunks, which
@@ -173,71 +185,76 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
         }
     }
 
-    // A lane's four keys and its run of 16 for the values: their pages' entries
-    // are asked for a step before the codes, and in front of the codes of the
-    // step before, so that waiting for them does not wait for those.
-    struct Run {
-        int entry, at;
-    };
+    // A step is four runs of 16 keys, each in one page.  Lane l looks up run l % 4;
+    // the entries are asked for a step before the codes, and in front of the
+    // codes of the step before, so that waiting for them does not wait for those.
     const int32_t* table = a.page_table + (int64_t)b.seq * a.max_pages;
     // cells (a row of a head) of a page, and of the heads in front of this one
-    const uint32_t page_cells = (uint32_t)a.kv_heads * a.page_size;
-    const int64_t head_cells = (int64_t)h * a.page_size;
+    const int64_t page_cells = (int64_t)a.kv_heads * a.page_size, head_cells = (int64_t)h * a.page_size;
     const uint8_t* const k_codes = a.k_codes + head_cells * (DK / 2);
     const uint8_t* const k_scales = a.k_scales + head_cells * (DK / 32);
     const uint8_t* const v_codes = a.v_codes + head_cells * (DV / 2);
     const uint8_t* const v_scales = a.v_scales + head_cells * (DV / 32);
     const int last_page = a.pages - 1, last_slot = a.max_pages - 1;
-    const int ks0 = (DK == 64 ? g >> 1 : g) * a.page_size, ks1 = (4 + (g >> 1)) * a.page_size;
+    struct Run {
+        int64_t cell;      // the page's first
+        int at;            // the run's row in the page
+    };
+    auto look = [&](int base) { return table[min((int)divide(base + 16 * (lane & 3), p.page), last_slot)]; };
+    auto run_of = [&](int entry, int base, int r) {
+        const int page = min(max(__builtin_amdgcn_readlane(entry, r), 0), last_page), key = base + 16 * r;
+        return Run{page * page_cells, key - (int)divide(key, p.page) * a.page_size};
+    };
+    struct Step {
+        v4u k[DK / 32], v[DV / 32], vs;
+        uint32_t ks[DK == 192 ? 2 : 1];
+    };
+    // the lane's scales: keys 4 n .. (run n / 4) of its groups of dims; values: run g
+    const int ks0 = (DK == 64 ? g >> 1 : g) * a.page_size + 4 * (n & 3), ks1 = (4 + (g >> 1)) * a.page_size + 4 * (n & 3);
     const int vs0 = (DV == 64 ? n >> 3 : n >> 2) * a.page_size;
-    auto find = [&](int key) {
-        const int whole = (int)divide(key, p.page);
-        return Run{table[min(whole, last_slot)], key - whole * a.page_size};
+    auto pick = [](int64_t x0, int64_t x1, int64_t x2, int64_t x3, int r) {
+        const int64_t lo = r & 1 ? x1 : x0, hi = r & 1 ? x3 : x2;
+        return r & 2 ? hi : lo;
     };
-    auto cell_of = [&](const Run& r) { return (uint64_t)(uint32_t)min(max(r.entry, 0), last_page) * page_cells; };
-    typedef AttnStep<DK, DV> Step;
-    Run k_at, v_at;
-    auto look = [&](int base) {
-        k_at = find(base + 4 * n);
-        v_at = find(base + 16 * g);
-    };
+    int entry = 0;
     auto load = [&](Step& s, int base) {
-        const Run kr = k_at, vr = v_at;
-        look(base + ATTN_CHUNK);        // behind the last page: its last entry, unused
-        {
-            const uint64_t cell = cell_of(kr);
-            const uint8_t* c = k_codes + (cell + kr.at) * (DK / 2);
-            const uint8_t* sc = k_scales + cell * (DK / 32) + kr.at;
+        Run run[4];
+        int64_t ks_at[4], vs_at[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const uint8_t* r = c + i * (DK / 2);
-                if constexpr (DK == 64) {
-                    const v2u w = *reinterpret_cast<const v2u*>(r + 8 * g);
-                    s.k[i][0] = w[0], s.k[i][1] = w[1];
-                } else {
-                    const v4u w = *reinterpret_cast<const v4u*>(r + 16 * g);
+        for (int r = 0; r < 4; r++) {
+            run[r] = run_of(entry, base, r);
+            ks_at[r] = run[r].cell * (DK / 32) + run[r].at;
+            vs_at[r] = run[r].cell * (DV / 32) + run[r].at;
+        }
+        entry = look(base + ATTN_CHUNK);        // behind the last page: its last entry, unused
+        // load j, half e: 512 bytes, part (2 j + e) % (DIM / 64) of run (2 j + e) / (DIM / 64)
+        auto codes = [&](auto dim, const uint8_t* from, v4u* to) {
+            constexpr int DIM = decltype(dim)::value, PER = DIM / 64;
 #pragma unroll
-                    for (int j = 0; j < 4; j++) s.k[i][j] = w[j];
-                    if constexpr (DK == 192) {
-                        const v2u x = *reinterpret_cast<const v2u*>(r + 64 + 8 * g);
-                        s.k[i][4] = x[0], s.k[i][5] = x[1];
-                    }
-                }
+            for (int j = 0; j < DIM / 32; j++) {
+                const Run &r0 = run[2 * j / PER], &r1 = run[(2 * j + 1) / PER];
+                const int64_t p0 = (r0.cell + r0.at) * (DIM / 2) + 2 * j % PER * 512;
+                const int64_t p1 = (r1.cell + r1.at) * (DIM / 2) + (2 * j + 1) % PER * 512 - 512;
+                const uint8_t* src = from + (2 * j / PER == (2 * j + 1) / PER ? p0 : lane < 32 ? p0 : p1);
+                to[j] = *reinterpret_cast<const v4u*>(src + (uint32_t)(16 * lane));
             }
-            s.ks[0] = *reinterpret_cast<const uint32_t*>(sc + ks0);
-            if constexpr (DK == 192) s.ks[1] = *reinterpret_cast<const uint32_t*>(sc + ks1);
-        }
-        const uint64_t cell = cell_of(vr);
-        const uint8_t* c = v_codes + (cell + vr.at) * (DV / 2);
-        const uint8_t* sc = v_scales + cell * (DV / 32) + vr.at;
+        };
+        codes(std::integral_constant<int, DK>{}, k_codes, s.k);
+        codes(std::integral_constant<int, DV>{}, v_codes, s.v);
+        const uint8_t* sc = k_scales + pick(ks_at[0], ks_at[1], ks_at[2], ks_at[3], n >> 2);
+        s.ks[0] = *reinterpret_cast<const uint32_t*>(sc + ks0);
+        if constexpr (DK == 192) s.ks[1] = *reinterpret_cast<const uint32_t*>(sc + ks1);
+        s.vs = *reinterpret_cast<const v4u*>(v_scales + pick(vs_at[0], vs_at[1], vs_at[2], vs_at[3], g) + vs0);
+    };
+    uint8_t* const tile = shared + wave * Tile::BYTES;
+    auto keep = [&](const Step& s) {
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            if constexpr (DV == 64)
-                s.v[i] = *reinterpret_cast<const uint16_t*>(c + i * (DV / 2) + 2 * n);
-            else
-                s.v[i] = *reinterpret_cast<const uint32_t*>(c + i * (DV / 2) + 4 * n);
+        for (int j = 0; j < DK / 32; j++) *reinterpret_cast<v4u*>(tile + Tile::key_at(64 * j + lane)) = s.k[j];
+#pragma unroll
+        for (int j = 0; j < DV / 32; j++) {
+            const int half = 2 * j + (lane >> 5), run = half / (DV / 64), part = half % (DV / 64);
+            *reinterpret_cast<v4u*>(tile + Tile::K_BYTES + run * Tile::V_RUN + 512 * part + 16 * (lane & 31)) = s.v[j];
         }
-        s.vs = *reinterpret_cast<const v4u*>(sc + vs0);
     };
 
     v4f o[DT];
@@ -245,26 +262,53 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
     for (int d = 0; d < DT; d++) o[d] = v4f{0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
 
-    auto step = [&](Step& s, int base) {
+    // what a step still needs beside the codes in LDS
+    auto step = [&](const uint32_t (&ks)[DK == 192 ? 2 : 1], v4u vs, int base) {
         // scores
         v4f acc[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) acc[i] = v4f{0, 0, 0, 0};
-        const float k0[4] = {scale_of<0>(s.ks[0]), scale_of<1>(s.ks[0]), scale_of<2>(s.ks[0]), scale_of<3>(s.ks[0])};
+        const float k0[4] = {scale_of<0>(ks[0]), scale_of<1>(ks[0]), scale_of<2>(ks[0]), scale_of<3>(ks[0])};
+        uint32_t kc[4][KW];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int chunk = (4 * n + i) * Tile::K_CHUNKS;
+            if constexpr (DK == 64) {
+                const v2u w = *reinterpret_cast<const v2u*>(tile + Tile::key_at(chunk + (g >> 1)) + 8 * (g & 1));
+                kc[i][0] = w[0], kc[i][1] = w[1];
+            } else {
+                const v4u w = *reinterpret_cast<const v4u*>(tile + Tile::key_at(chunk + g));
+#pragma unroll
+                for (int j = 0; j < 4; j++) kc[i][j] = w[j];
+                if constexpr (DK == 192) {
+                    const v2u x = *reinterpret_cast<const v2u*>(tile + Tile::key_at(chunk + 4 + (g >> 1)) + 8 * (g & 1));
+                    kc[i][4] = x[0], kc[i][5] = x[1];
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 4; i++) {
 #pragma unroll
             for (int j = 0; j < (KW < 4 ? KW : 4); j++)
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4x8(s.k[i][j], k0[i]), q[j], acc[i], 0, 0, 0);
+                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4x8(kc[i][j], k0[i]), q[j], acc[i], 0, 0, 0);
         }
         if constexpr (DK == 192) {
-            const float k1[4] = {scale_of<0>(s.ks[1]), scale_of<1>(s.ks[1]), scale_of<2>(s.ks[1]), scale_of<3>(s.ks[1])};
+            const float k1[4] = {scale_of<0>(ks[1]), scale_of<1>(ks[1]), scale_of<2>(ks[1]), scale_of<3>(ks[1])};
 #pragma unroll
             for (int i = 0; i < 4; i++) {
 #pragma unroll
                 for (int j = 4; j < 6; j++)
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4x8(s.k[i][j], k1[i]), q[j], acc[i], 0, 0, 0);
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4x8(kc[i][j], k1[i]), q[j], acc[i], 0, 0, 0);
             }
+        }
+        uint32_t vcode[16];
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            const uint8_t* w = tile + Tile::K_BYTES + g * Tile::V_RUN + i * (DV / 2);
+            if constexpr (DV == 64)
+                vcode[i] = *reinterpret_cast<const uint16_t*>(w + 2 * n);
+            else
+                vcode[i] = *reinterpret_cast<const uint32_t*>(w + 4 * n);
         }
         // acc[i][r]: key base + 16 g + 4 r + i of row n
         if (base + ATTN_STEP > in_hi || base < in_lo || base + ATTN_STEP > end) {
@@ -288,7 +332,7 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
                     const int key = base + 16 * g + 4 * r + i;
                     if (key < all_hi && key >= all_lo) keep |= 0xFFu << (8 * i);
                 }
-                s.vs[r] &= keep;
+                vs[r] &= keep;
             }
         }
         float top = acc[0][0];
@@ -324,7 +368,7 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
             float sc[8];
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-                const uint32_t q4 = s.vs[2 * u + e];
+                const uint32_t q4 = vs[2 * u + e];
                 sc[4 * e + 0] = scale_of<0>(q4), sc[4 * e + 1] = scale_of<1>(q4);
                 sc[4 * e + 2] = scale_of<2>(q4), sc[4 * e + 3] = scale_of<3>(q4);
             }
@@ -332,7 +376,7 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
                 constexpr int SEL = decltype(sel)::value;
                 uint32_t x[8];
 #pragma unroll
-                for (int j = 0; j < 8; j++) x[j] = fp4x2<SEL>(s.v[8 * u + j], sc[j]);
+                for (int j = 0; j < 8; j++) x[j] = fp4x2<SEL>(vcode[8 * u + j], sc[j]);
                 v4u even, odd;
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
@@ -350,26 +394,24 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
             }
         }
     };
-    // two steps' codes in flight, each step's asked for as soon as its place is free
-    Step even, odd;
+    Step s;
     int base = (int)begin + ATTN_STEP * wave;
     if (base < end) {
-        look(base);
-        load(even, base);
-        if (base + ATTN_CHUNK < end) load(odd, base + ATTN_CHUNK);
-        while (true) {
-            step(even, base);
-            if (base + 2 * ATTN_CHUNK < end) load(even, base + 2 * ATTN_CHUNK);
-            base += ATTN_CHUNK;
-            if (base >= end) break;
-            step(odd, base);
-            if (base + 2 * ATTN_CHUNK < end) load(odd, base + 2 * ATTN_CHUNK);
-            base += ATTN_CHUNK;
-            if (base >= end) break;
-        }
+        entry = look(base);
+        load(s, base);
+    }
+    for (; base < end; base += ATTN_CHUNK) {
+        keep(s);
+        uint32_t ks[DK == 192 ? 2 : 1];
+#pragma unroll
+        for (int i = 0; i < (DK == 192 ? 2 : 1); i++) ks[i] = s.ks[i];
+        const v4u vs = s.vs;
+        if (base + ATTN_CHUNK < end) load(s, base + ATTN_CHUNK);
+        step(ks, vs, base);
     }
     // join the waves: o[d][r] is dim DT (4 g + r) + d of row n
     l = over_groups_sum(l);
+    __syncthreads();        // the tiles' place becomes the outputs'
 #pragma unroll
     for (int r = 0; r < 4; r++)
 #pragma unroll
@@ -868,8 +910,12 @@ static AttnPlan attn_plan(const Kv4AttnArgs& a) {
     const int some = a.batch < a.queries ? a.batch : a.queries;
     if (blocks < some) blocks = some;
     blocks *= a.kv_heads;
-    const int64_t full = wide ? 512 : 1024;     // workgroups that fill the chip
+    // Two workgroups a CU fill the chip; more and smaller chunks cost more than
+    // they balance (measured with 1024 and 2048).  A chunk of at most 16384 keys
+    // keeps one long sequence among short ones from being the whole time.
+    constexpr int64_t full = 512, longest = 16384;
     int64_t want = blocks >= full ? 1 : full / blocks;
+    if (want < (keys + longest - 1) / longest) want = (keys + longest - 1) / longest;
     const int64_t most = ((int64_t)1 << 30) / ((int64_t)p.ids * a.kv_heads);   // keeps the grid's size an int
     if (want > most) want = most < 1 ? 1 : most;
     const int64_t least = wide ? 4 * ATTN_STEP : ATTN_CHUNK;
