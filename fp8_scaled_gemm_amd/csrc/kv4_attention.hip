@@ -471,11 +471,10 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
 //                  LDS (one a dim) hold the keys in that order.
 // The two waves of a SIMD take turns: waves 0 .. 3 multiply (the outputs of step
 // t and the scores of step t + 1, 32 matrix instructions) while waves 4 .. 7
-// work on the vector unit (maximum and weights of a step, codes of later steps
-// into LDS), then the other way round, a barrier between the phases.  Left to
-// themselves both wait for the matrix core together and leave it idle together.
-// With waves 4 .. 7 one phase behind, and turning codes one step further ahead,
-// two halves of LDS are enough: a half is written after both have read it.
+// work out maxima and weights on the vector unit, then the other way round, a
+// barrier between the phases.  Between its matrix instructions a wave has time
+// for what is left: it turns codes of step t + 2 (keys) and t + 1 (values) into
+// the halves of the LDS that both groups have left, and asks for the next ones.
 // The running maximum moves only when a row's maximum has grown by 2^8 or more:
 // weights up to 2^8 lose nothing in bf16 and float32, and the outputs are
 // rarely scaled.
@@ -500,8 +499,13 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     constexpr int KN = DK == 192 ? 2 : 1;
     constexpr int VU = ATTN_STEP / 4 * (DV / 4);
     static_assert(WAVES == 8 && VU <= THREADS, "one unit of values a thread, and a wave's units in one run of 16 keys");
-    __shared__ v4u s_k[2][ATTN_STEP * KC];
-    __shared__ v4u s_v[2][DV * 8];
+    // the halves as arrays of their own, chosen at compile time: the compiler then
+    // knows that writes to one do not meet reads of the other, and moves them
+    __shared__ v4u s_k0[ATTN_STEP * KC], s_k1[ATTN_STEP * KC], s_v0[DV * 8], s_v1[DV * 8];
+    typedef std::integral_constant<int, 0> Even;
+    typedef std::integral_constant<int, 1> Odd;
+    auto keys_in = [&](auto half) { if constexpr (decltype(half)::value) return reinterpret_cast<char*>(s_k1); else return reinterpret_cast<char*>(s_k0); };
+    auto values_in = [&](auto half) { if constexpr (decltype(half)::value) return reinterpret_cast<char*>(s_v1); else return reinterpret_cast<char*>(s_v0); };
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, n = lane & 31, e = lane >> 5;
     const int group = a.q_heads / a.kv_heads;
     // chunk by chunk, and long blocks (the last rows of a sequence see the most
@@ -589,11 +593,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     struct Run {
         int entry, at;
     };
-    int zero;
-    asm volatile("v_mov_b32 %0, 0" : "=v"(zero));
+    int opaque;
+    asm volatile("v_mov_b32 %0, 0" : "=v"(opaque));
     auto find = [&](int key) {
         const int whole = (int)divide(key, p.page);
-        return Run{table[min(whole, last_slot) + zero], key - whole * a.page_size};
+        return Run{table[min(whole, last_slot) + opaque], key - whole * a.page_size};
     };
     auto page_cell = [&](const Run& r) {
         return min(max(__builtin_amdgcn_readfirstlane(r.entry), 0), last_page) * page_cells;
@@ -626,51 +630,49 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
             s.vs = *reinterpret_cast<const uint32_t*>(sc + (uint32_t)vs_off);
         }
     };
-    auto turn_keys = [&](const Keys& s, int buffer) {
+    // The lane's places in LDS, in bytes.  Every other place of a step is one of
+    // these with an exclusive or of a few bits and a constant added: few registers,
+    // where the compiler would keep one for each.
+    int k_read = 16 * lds_at<KC>(n, e), v_read = 16 * lds_at<8>(n, e), k_write[KN];
+#pragma unroll
+    for (int u = 0; u < KN; u++) k_write[u] = 16 * lds_at<KC>(k_key(u), 2 * k_piece(u));
+    // chunk `part` of each unit
+    auto turn_keys = [&](const Keys& s, auto half, int part) {
 #pragma unroll
         for (int u = 0; u < KN; u++) {
             if (k_live(u)) {
                 const float scale = __builtin_bit_cast(float, s.ks[u] << 23);
-                s_k[buffer][lds_at<KC>(k_key(u), 2 * k_piece(u))] = __builtin_bit_cast(v4u, fp4x8(s.k[u][0], scale));
-                s_k[buffer][lds_at<KC>(k_key(u), 2 * k_piece(u) + 1)] = __builtin_bit_cast(v4u, fp4x8(s.k[u][1], scale));
+                *reinterpret_cast<v4u*>(keys_in(half) + (k_write[u] ^ (16 * part))) = __builtin_bit_cast(v4u, fp4x8(s.k[u][part], scale));
             }
         }
     };
     // A run of 4 keys is half a chunk of the values' rows: runs 0, 2 of 16 keys
     // (e = 0) and 1, 3 (e = 1).
-    const int v_chunk = 2 * (vkey >> 4) + ((vkey >> 2) & 1), v_half = (vkey >> 3) & 1;
-    auto turn_values = [&](Values& s, int base, int buffer, bool edge) {
+    int v_write = 16 * lds_at<8>(4 * vq, 2 * (vkey >> 4) + ((vkey >> 2) & 1)) + 8 * ((vkey >> 3) & 1);
+    auto value_scales = [&](const Values& s, int base, float (&sc)[4]) {
+        // values outside the block's keys: a scale of 2^-127 makes whatever they
+        // hold finite, and their weight of zero removes it
+        auto first_bytes = [](int n) { return n <= 0 ? 0u : n >= 4 ? ~0u : (1u << (8 * n)) - 1u; };
+        const uint32_t vs = s.vs & first_bytes(all_hi - base - vkey) & ~first_bytes(all_lo - base - vkey);
+        sc[0] = scale_of<0>(vs), sc[1] = scale_of<1>(vs), sc[2] = scale_of<2>(vs), sc[3] = scale_of<3>(vs);
+    };
+    // dims 2 part, 2 part + 1 of the unit's 4
+    auto turn_values = [&](const Values& s, const float (&sc)[4], auto half, auto part) {
         if (VU == THREADS || threadIdx.x < VU) {
-            if (edge) {
-                asm volatile("");
-                // values outside the block's keys: a scale of 2^-127 makes
-                // whatever they hold finite, and their weight of zero removes it
-                uint32_t keep = 0;
+            constexpr int SEL = decltype(part)::value;
+            uint32_t x[4];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int key = base + vkey + i;
-                    if (key < all_hi && key >= all_lo) keep |= 0xFFu << (8 * i);
-                }
-                s.vs &= keep;
+            for (int j = 0; j < 4; j++) x[j] = fp4x2<SEL>(s.v[j], sc[j]);
+            v2u even, odd;
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                even[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x05040100u);
+                odd[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x07060302u);
             }
-            const float sc[4] = {scale_of<0>(s.vs), scale_of<1>(s.vs), scale_of<2>(s.vs), scale_of<3>(s.vs)};
-            auto pair = [&](auto sel) {
-                constexpr int SEL = decltype(sel)::value;
-                uint32_t x[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) x[j] = fp4x2<SEL>(s.v[j], sc[j]);
-                v2u even, odd;
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    even[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x05040100u);
-                    odd[j] = __builtin_amdgcn_perm(x[2 * j + 1], x[2 * j], 0x07060302u);
-                }
-                v2u* const rows = reinterpret_cast<v2u*>(s_v[buffer]) + v_half;
-                rows[2 * lds_at<8>(4 * vq + 2 * SEL, v_chunk)] = even;
-                rows[2 * lds_at<8>(4 * vq + 2 * SEL + 1, v_chunk)] = odd;
-            };
-            pair(std::integral_constant<int, 0>{});
-            pair(std::integral_constant<int, 1>{});
+            // rows 2 SEL and 2 SEL + 1 of the unit's 4, 128 bytes each
+            char* const to = values_in(half) + (v_write ^ (16 * SEL)) + 256 * SEL;
+            *reinterpret_cast<v2u*>(to) = even;
+            *reinterpret_cast<v2u*>(to + 128) = odd;
         }
     };
 
@@ -681,14 +683,21 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
         for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
     float m = -INFINITY, l = 0.0f;
 
-    auto scores = [&](v16f (&acc)[2], int buffer) {
-        const v16f zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    // operand j, x of the scores (16 dims of 32 keys), and u, d of the outputs
+    auto key_operand = [&](auto half, int j, int x) {
+        const int flip = DK == 128 ? 2 * j : (2 * j) & 7, add = 2 * j - flip + 32 * KC * x;
+        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const v4u*>(keys_in(half) + (k_read ^ (16 * flip)) + 16 * add));
+    };
+    auto value_operand = [&](auto half, int u, int d) {
+        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const v4u*>(values_in(half) + (v_read ^ (32 * u)) + 4096 * d));
+    };
+    const v16f zero = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    auto scores = [&](v16f (&acc)[2], auto half) {
 #pragma unroll
         for (int j = 0; j < KK; j++)
 #pragma unroll
             for (int x = 0; x < 2; x++)
-                acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, s_k[buffer][lds_at<KC>(n, 2 * j + e) + 32 * KC * x]), q[j], j ? acc[x] : zero, 0, 0, 0);
+                acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_operand(half, j, x), q[j], j ? acc[x] : zero, 0, 0, 0);
     };
     // the largest score of the lane's half of its row, after the mask of an edge step
     auto largest = [&](v16f (&acc)[2], int base, bool edge) {
@@ -738,13 +747,12 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     };
-    auto outputs = [&](const bf16x8 (&w)[4], int buffer) {
+    auto outputs = [&](const bf16x8 (&w)[4], auto half) {
 #pragma unroll
         for (int u = 0; u < 4; u++)
 #pragma unroll
             for (int d = 0; d < DT; d++)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, s_v[buffer][lds_at<8>(n, 2 * u + e) + 32 * 8 * d]), w[u], o[d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(value_operand(half, u, d), w[u], o[d], 0, 0, 0);
     };
 
     if (steps > 0) {
@@ -764,56 +772,95 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
         load_values(values);
         find_keys(base_of(1));
         find_values(base_of(1));
-        turn_keys(keys, 0);
+        turn_keys(keys, Even{}, 0);
+        turn_keys(keys, Even{}, 1);
         load_keys(keys);
         find_keys(base_of(2));
-        turn_values(values, base_of(0), 0, true);
+        float sc[4];
+        value_scales(values, base_of(0), sc);
+        turn_values(values, sc, Even{}, Even{});
+        turn_values(values, sc, Even{}, Odd{});
         load_values(values);
         find_values(base_of(2));
-        turn_keys(keys, 1);
+        turn_keys(keys, Odd{}, 0);
+        turn_keys(keys, Odd{}, 1);
         load_keys(keys);
         find_keys(base_of(3));
         __syncthreads();
-        scores(acc, 0);
+        scores(acc, Even{});
         raise(largest(acc, base_of(0), true));
         weights(acc, w);
         __syncthreads();
-        // codes of the keys of step t + 2 + late and the values of t + 1 + late
-        // into LDS, the next ones into registers
-        auto turn = [&](int t) {
-            turn_keys(keys, (t + late) & 1);
-            turn_values(values, base_of(t + 1 + late), (t + 1 + late) & 1, edge(t + 1 + late));
-            load_keys(keys);             // of step t + 3 + late
-            load_values(values);         // of step t + 2 + late
-            find_keys(base_of(t + 4 + late));
-            find_values(base_of(t + 3 + late));
-        };
-        if (late) {
-            turn(-1);
-            __syncthreads();
-        }
-        for (int t = 0; t + 1 < steps; t++) {
+        auto round = [&](int t, auto half) {
+            typedef std::integral_constant<int, decltype(half)::value ^ 1> Other;
             __builtin_amdgcn_s_setprio(1);
-            outputs(w, t & 1);
-            scores(acc, (t + 1) & 1);
-            // operands 8 reads ahead of the products: the compiler's own order
-            // waits for each pair of reads
-            constexpr int READS = 4 * DT + 2 * KK, READ_AHEAD = 8;
-            __builtin_amdgcn_sched_group_barrier(0x100, READ_AHEAD, 0);
+            // The products in eight groups, their operands read 6 or 4 ahead, and with
+            // each group a slice of the rest: the compiler's own order waits for
+            // each pair of reads and leaves the rest behind the last product.
+            constexpr int PRODUCTS = 4 * DT + 2 * KK, AHEAD = DK == 192 ? 4 : 6, GROUP = PRODUCTS / 8;
+            // places worked out anew in every round, not kept from before the loop
+            asm volatile("" : "+v"(k_read), "+v"(v_read), "+v"(v_write));
 #pragma unroll
-            for (int i = 0; i < READS - READ_AHEAD; i++) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            for (int u = 0; u < KN; u++) asm volatile("" : "+v"(k_write[u]));
+            auto operand = [&](int i) {
+                return i < 4 * DT ? value_operand(half, i / DT, i % DT) : key_operand(Other{}, (i - 4 * DT) >> 1, (i - 4 * DT) & 1);
+            };
+            bf16x8 ring[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; i++) ring[i] = operand(i);
+            float sc[4];
+#pragma unroll
+            for (int gr = 0; gr < 8; gr++) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = gr * GROUP; i < (gr + 1) * GROUP; i++) {
+                    const bf16x8 x = ring[i % AHEAD];
+                    if (i < 4 * DT) {
+                        o[i % DT] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, w[i / DT], o[i % DT], 0, 0, 0);
+                    } else {
+                        const int j = i - 4 * DT;
+                        acc[j & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, q[j >> 1], j < 2 ? zero : acc[j & 1], 0, 0, 0);
+                    }
+                    if (i + AHEAD < PRODUCTS) ring[i % AHEAD] = operand(i + AHEAD);
+                }
+                if (gr == 0) turn_keys(keys, half, 0);                       // of step t + 2
+                if (gr == 1) turn_keys(keys, half, 1);
+                if (gr == 2) value_scales(values, base_of(t + 1), sc);
+                if (gr == 3) turn_values(values, sc, Other{}, Even{});
+                if (gr == 4) turn_values(values, sc, Other{}, Odd{});
+                if (gr == 5) load_keys(keys);                                // of step t + 3
+                if (gr == 6) load_values(values);                            // of step t + 2
+                if (gr == 7) {
+                    find_keys(base_of(t + 4));
+                    find_values(base_of(t + 3));
+                }
+#pragma unroll
+                for (int i = 0; i < GROUP; i++) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x004, 5, 0);
+                }
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, READ_AHEAD, 0);
+            __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_setprio(0);
             __syncthreads();
             raise(largest(acc, base_of(t + 1), edge(t + 1)));
             weights(acc, w);
-            turn(t);
             __syncthreads();
+        };
+        if (late) __syncthreads();
+        int t = 0;
+        for (; t + 2 < steps; t += 2) {
+            round(t, Even{});
+            round(t + 1, Odd{});
         }
-        outputs(w, (steps - 1) & 1);
+        if (t + 1 < steps) {
+            round(t, Even{});
+            outputs(w, Odd{});
+        } else {
+            outputs(w, Even{});
+        }
         if (!late) __syncthreads();
     }
     l += __shfl_xor(l, 32, 64);
