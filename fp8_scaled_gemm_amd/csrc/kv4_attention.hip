@@ -936,10 +936,12 @@ __global__ __launch_bounds__(ATTN_THREADS) void kv4_attention_join_kernel(Kv4Att
     if (a.lse && lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
-// Many rows a sequence on average: blocks of 128 rows and more, not 16.
+// Many rows a sequence on average: blocks of 256 rows, not 16.  8 sequences of
+// 8192 keys, 8 key heads, us with 16 / 256 rows: 48 / 84 at 64 rows a key head,
+// 78 / 109 at 128, 121 / 112 at 160, 115 / 116 at 192.
 constexpr int ATTN_WIDE_WAVES = 8;
 static bool attn_wide(const Kv4AttnArgs& a) {
-    return (int64_t)a.queries * (a.q_heads / a.kv_heads) >= 64 * (int64_t)a.batch;
+    return (int64_t)a.queries * (a.q_heads / a.kv_heads) >= 160 * (int64_t)a.batch;
 }
 
 static AttnPlan attn_plan(const Kv4AttnArgs& a) {

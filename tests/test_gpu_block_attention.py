@@ -89,6 +89,17 @@ def test_prefill(gpu_lib, dk, dv, causal, window, q_heads, kv_heads):
     check(gpu_lib, [200, 131, 64], [200, 400, 70], q_heads, kv_heads, dk, dv, 16, causal, window, dk + q_heads)
 
 
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 33)])
+@pytest.mark.parametrize("q_lens,kv_lens,q_heads,kv_heads", [
+    ([200], [200], 2, 2),                       # one chunk of keys
+    ([400, 260], [700, 260], 2, 2),             # several
+    ([300, 0, 90], [120, 5, 90], 3, 1),         # rows in front of the first key
+    ([17, 130], [0, 513], 40, 2)])              # a sequence without keys
+def test_prefill_blocks(gpu_lib, dk, dv, causal, window, q_lens, kv_lens, q_heads, kv_heads):
+    check(gpu_lib, q_lens, kv_lens, q_heads, kv_heads, dk, dv, 32, causal, window, dk + len(q_lens))
+
+
 def test_long_context_is_split(gpu_lib):
     check(gpu_lib, [1], [5000], 4, 1, 128, 128, 16, True, 0, 1)
     check(gpu_lib, [2, 1, 1], [4100, 40, 0], 4, 2, 64, 64, 64, True, 0, 2)

@@ -68,6 +68,12 @@ def test_append_and_gather(gpu_lib, dk, dv, T, H, page, dtype):
             assert got.dtype == dt and np.array_equal(host(got), w)
 
 
+@pytest.mark.parametrize("T,H,dk,dv", [(1030, 2, 128, 128), (2049, 1, 192, 128), (1500, 3, 64, 64)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_append_many_rows(gpu_lib, T, H, dk, dv, dtype):
+    test_append_and_gather(gpu_lib, dk, dv, T, H, 32, dtype)
+
+
 def test_append_past_32_bit_offsets(gpu_lib):
     H, dk, page = 8, 128, 64
     pages = (1 << 32) // (H * page * dk // 2) + 4
@@ -209,6 +215,62 @@ def test_lora_keeps_what_other_adapters_hold_out(gpu_lib):
     args[2][1], args[3][1], args[1][20:40] = float("nan"), float("nan"), float("inf")
     ref[1][20:40] = 0
     lora_check(gpu_lib.lora_add(*args), ref, 256, 16, BF)
+
+
+def test_binding_refuses(gpu_lib):
+    """Wrong types, shapes, devices and layouts are errors of Python's own kinds;
+    what the library refuses keeps its status."""
+    _, args = lora_case(7, 8, 64, 64, 16, 2, [0, 8], [1], BF)
+    base, x, A, B, scale, start, adapter = args
+
+    def bad(kind, **change):
+        names = dict(base=base, x=x, A=A, B=B, scale=scale, seg_start=start, seg_adapter=adapter)
+        with pytest.raises(kind):
+            gpu_lib.lora_add(**{**names, **change})
+
+    bad(TypeError, x=x.float())
+    bad(TypeError, base=base.half())
+    bad(TypeError, A=None)
+    bad(TypeError, seg_start=start.long())
+    bad(ValueError, x=x.cpu())
+    bad(ValueError, x=x[:, :32])
+    bad(ValueError, B=B.transpose(1, 2))
+    bad(ValueError, A=A.transpose(1, 2).contiguous().transpose(1, 2))
+    bad(ValueError, out=base[:4])
+    bad(ValueError, x=x[0])
+    with pytest.raises(gpu_lib.Fp8gError) as e:
+        gpu_lib.lora_add(*args, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 6
+    with pytest.raises(gpu_lib.Fp8gError):
+        gpu_lib.lora_add(base, x[:, :60].contiguous(), A[:, :, :60].contiguous(), B, scale, start, adapter)
+    cache = gpu_lib.kv4_cache(4, 2, 16, 128, 128)
+    rows_ = torch.zeros(3, 2, 128, device="cuda", dtype=BF)
+    slots = torch.arange(3, device="cuda")
+    for change in ({"k": rows_[:, :1]}, {"v": rows_.transpose(1, 2).contiguous().transpose(1, 2)}, {"slots": slots[:2]}):
+        with pytest.raises(ValueError):
+            gpu_lib.kv4_append(**{**dict(cache=cache, k=rows_, v=rows_, slots=slots), **change})
+    with pytest.raises(TypeError):
+        gpu_lib.kv4_append(cache, rows_, rows_, slots.int())
+    with pytest.raises(TypeError):
+        gpu_lib.kv4_gather(cache, slots, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        gpu_lib.kv4_gather(gpu_lib.KV4Cache(*cache[:3], cache.v_scale[:, :, :2]), slots)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")   # noqa: E731
+    q, table = torch.zeros(1, 4, 128, device="cuda", dtype=BF), torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(gpu_lib.Fp8gError) as e:
+        gpu_lib.kv4_attention(q, cache, table, ints(0, 1), ints(5), causal=False, window=3)
+    assert e.value.status == 2
+    with pytest.raises(TypeError):
+        gpu_lib.kv4_attention(q.float(), cache, table, ints(0, 1), ints(5))
+    with pytest.raises(ValueError):
+        gpu_lib.kv4_attention(q, cache, table, ints(0, 1, 1), ints(5))
+    angle = torch.zeros(4, 64, device="cuda")
+    with pytest.raises(ValueError):
+        gpu_lib.qk_norm_rope(q, q, None, None, torch.zeros(3, 1, dtype=torch.int32, device="cuda"), angle)
+    with pytest.raises(TypeError):
+        gpu_lib.qk_norm_rope(q, q, None, None, torch.zeros(1, dtype=torch.int64, device="cuda"), angle)
+    # a call after the refusals works
+    assert torch.equal(gpu_lib.lora_add(*args), gpu_lib.lora_add(*args))
 
 
 def test_block_step_in_a_graph(gpu_lib):
