@@ -21,6 +21,10 @@
 // and a CU gets 16 bytes a clock (measured, from L1 and L2 alike), against 28
 // for 64-byte and 45 for whole runs.  So shrink, and expand for long segments,
 // load whole 128-byte lines and turn them around in LDS.
+//
+// Measured: 8192 tokens, 7 segments, k 8192, n 2048, rank 64, bf16: shrink 33 us (x
+// read once: 4.0 TB/s), expand 26 us; 64 adapters of rank 16 for 64 tokens, k = n =
+// 4096: 5.1 and 6.5 us, of which reading A and B takes 3 at a large copy's rate.
 
 #include "device_common.h"
 #include "launch_block.h"
@@ -34,17 +38,16 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int LORA_THREADS = 256;
-constexpr int LORA_MAX_SPLITS = 16;
 
-// The block's tokens [t0, t1), at most 16 TT, and its adapter (-1: none).
+// The block's tokens [t0, t1), at most 64 or 16, and its adapter (-1: none).
 // Tokens in front of the first segment and behind the last are segments
 // without an adapter.
 struct LoraBlock {
     int t0, t1, adapter;
 };
-template <int TT>
+template <bool WIDE>
 __device__ __forceinline__ LoraBlock lora_block(const LoraArgs& a, int id) {
-    constexpr int LOG2 = TT == 8 ? 7 : TT == 4 ? 6 : 4;
+    constexpr int LOG2 = WIDE ? 6 : 4;
     const int S = a.segments;
     auto start = [&](int v) {   // starts of the S + 2 segments, and the end
         if (v <= 0) return 0;
@@ -54,8 +57,8 @@ __device__ __forceinline__ LoraBlock lora_block(const LoraArgs& a, int id) {
     const Sequence q = find_sequence(
         start, [&](int v) { return v >= 1 && v <= S ? a.seg_adapter[v - 1] : -1; }, S + 2, 1, LOG2, id);
     LoraBlock b;
-    b.t0 = q.start + (id - ((q.start >> LOG2) + q.index)) * (16 * TT);
-    b.t1 = min(q.end, b.t0 + 16 * TT);
+    b.t0 = q.start + (id - ((q.start >> LOG2) + q.index)) * (1 << LOG2);
+    b.t1 = min(q.end, b.t0 + (1 << LOG2));
     b.adapter = q.word;
     if (b.adapter >= a.adapters) b.adapter = -1;
     return b;
@@ -66,16 +69,16 @@ __device__ __forceinline__ LoraBlock lora_block(const LoraArgs& a, int id) {
 // of 16 rows off each other's banks.
 __device__ __forceinline__ int tile_at(int m, int c) { return m * 8 + (c ^ ((m >> 1) & 7)); }
 
-// Short segments: 16 TT tokens a block, RT 16-row tiles of the rank; the waves
+// Short segments: 16 tokens a block, RT 16-row tiles of the rank; the waves
 // take turns over units of 64 k, each on its own.
-template <int RT, int TT>
+template <int RT>
 __global__ __launch_bounds__(LORA_THREADS, 2) void lora_shrink_kernel(LoraArgs a, int splits, int k_split, int rank_blocks) {
-    __shared__ v4u tiles[4][RT + TT][128];      // a wave's own; then the waves' sums
+    __shared__ v4u tiles[4][RT + 1][128];      // a wave's own; then the waves' sums
     // A block's parts lie 8 workgroups apart: on one XCD, whose L2 they share.
     const int parts = splits * rank_blocks, line = blockIdx.x >> 3;
     const int id = (line / parts) * 8 + (blockIdx.x & 7), rest = line % parts;
     const int split = rest / rank_blocks, rank0 = (rest - split * rank_blocks) * (16 * RT);
-    const LoraBlock b = lora_block<TT>(a, id);
+    const LoraBlock b = lora_block<false>(a, id);
     if (b.t0 >= b.t1 || b.adapter < 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
     const int k0 = split * k_split, len = min(a.k - k0, k_split);
@@ -85,27 +88,21 @@ __global__ __launch_bounds__(LORA_THREADS, 2) void lora_shrink_kernel(LoraArgs a
     const int lr = lane >> 3, lc = lane & 7;
     const int ranks = min(a.rank - rank0, 16 * RT);
     const uint16_t* A = static_cast<const uint16_t*>(a.A) + ((int64_t)b.adapter * a.rank + rank0 + lr) * a.k + k0 + 8 * lc;
-    const uint16_t* x[TT][2];
+    const uint16_t* x[2];
 #pragma unroll
-    for (int t = 0; t < TT; t++)
+    for (int e = 0; e < 2; e++)
+        x[e] = static_cast<const uint16_t*>(a.x) + (int64_t)min(b.t0 + 8 * e + lr, b.t1 - 1) * a.k + k0 + 8 * lc;
+    v4f acc[RT];
 #pragma unroll
-        for (int e = 0; e < 2; e++)
-            x[t][e] = static_cast<const uint16_t*>(a.x) + (int64_t)min(b.t0 + 16 * t + 8 * e + lr, b.t1 - 1) * a.k + k0 + 8 * lc;
-    v4f acc[RT][TT];
-#pragma unroll
-    for (int r = 0; r < RT; r++)
-#pragma unroll
-        for (int t = 0; t < TT; t++) acc[r][t] = v4f{0, 0, 0, 0};
+    for (int r = 0; r < RT; r++) acc[r] = v4f{0, 0, 0, 0};
     // Units of 64 of k, AHEAD of them at a time and the next on their way.
-    constexpr int AHEAD = RT + TT <= 2 ? 4 : RT + TT <= 3 ? 2 : 1;
+    constexpr int AHEAD = RT == 1 ? 4 : RT == 2 ? 2 : 1;
     struct Unit {
-        v4u w[RT][2], x[TT][2];
+        v4u w[RT][2], x[2];
     };
     auto load = [&](Unit& s, int at, bool live) {
 #pragma unroll
-        for (int t = 0; t < TT; t++)
-#pragma unroll
-            for (int e = 0; e < 2; e++) s.x[t][e] = live ? *reinterpret_cast<const v4u*>(x[t][e] + at) : v4u{0, 0, 0, 0};
+        for (int e = 0; e < 2; e++) s.x[e] = live ? *reinterpret_cast<const v4u*>(x[e] + at) : v4u{0, 0, 0, 0};
 #pragma unroll
         for (int r = 0; r < RT; r++)
 #pragma unroll
@@ -118,20 +115,15 @@ __global__ __launch_bounds__(LORA_THREADS, 2) void lora_shrink_kernel(LoraArgs a
         for (int e = 0; e < 2; e++) {
 #pragma unroll
             for (int r = 0; r < RT; r++) tile[r][tile_at(8 * e + lr, lc)] = s.w[r][e];
-#pragma unroll
-            for (int t = 0; t < TT; t++) tile[RT + t][tile_at(8 * e + lr, lc)] = s.x[t][e];
+            tile[RT][tile_at(8 * e + lr, lc)] = s.x[e];
         }
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-            bf16x8 xf[TT];
-#pragma unroll
-            for (int t = 0; t < TT; t++) xf[t] = __builtin_bit_cast(bf16x8, tile[RT + t][tile_at(m, 4 * j + g)]);
+            const bf16x8 xf = __builtin_bit_cast(bf16x8, tile[RT][tile_at(m, 4 * j + g)]);
 #pragma unroll
             for (int r = 0; r < RT; r++) {
                 const bf16x8 w = __builtin_bit_cast(bf16x8, tile[r][tile_at(m, 4 * j + g)]);
-#pragma unroll
-                for (int t = 0; t < TT; t++)
-                    acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xf[t], acc[r][t], 0, 0, 0);
+                acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xf, acc[r], 0, 0, 0);
             }
         }
     };
@@ -159,63 +151,59 @@ __global__ __launch_bounds__(LORA_THREADS, 2) void lora_shrink_kernel(LoraArgs a
     v4f* sums = reinterpret_cast<v4f*>(tiles);
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < RT; r++)
-#pragma unroll
-        for (int t = 0; t < TT; t++) sums[(wave * RT * TT + t * RT + r) * 64 + lane] = acc[r][t];
+    for (int r = 0; r < RT; r++) sums[(wave * RT + r) * 64 + lane] = acc[r];
     __syncthreads();
     const float scale = a.scale[b.adapter];
-    for (int i = threadIdx.x; i < RT * TT * 64; i += LORA_THREADS) {
+    for (int i = threadIdx.x; i < RT * 64; i += LORA_THREADS) {
         const int tile = i >> 6, l = i & 63;
-        const v4f h = ((sums[i] + sums[RT * TT * 64 + i]) + (sums[2 * RT * TT * 64 + i] + sums[3 * RT * TT * 64 + i])) * scale;
-        const int tok = b.t0 + 16 * (tile / RT) + (l & 15), rank = 16 * (tile % RT) + 4 * (l >> 4);
+        const v4f h = ((sums[i] + sums[RT * 64 + i]) + (sums[2 * RT * 64 + i] + sums[3 * RT * 64 + i])) * scale;
+        const int tok = b.t0 + (l & 15), rank = 16 * tile + 4 * (l >> 4);
         if (tok < b.t1 && rank < ranks)             // ranks is a multiple of 8: 4 of them are inside or outside
             *reinterpret_cast<v4f*>(a.workspace + ((int64_t)split * a.tokens + tok) * a.rank + rank0 + rank) = h;
     }
 }
 
-// Long segments: a block of 64 TT tokens, 16 TT of them a wave.  The waves share
+// Long segments: a block of 64 tokens, 16 of them a wave.  The waves share
 // the adapter's tile of a unit of 64 k in LDS, so that it crosses the caches
 // once a block, and turn their own tokens' tiles around in LDS of their own.
-// DEPTH units are in flight in registers.
-template <int RT, int TT, int DEPTH>
+// DEPTH units are in flight in registers.  Blocks of 128 tokens, which read the
+// adapter half as often, came out even: shrink 38.5 instead of 44 us at 8192 x
+// 8192, rank 64, but the more slices of k that fill the chip again cost expand 3,
+// and 37 instead of 34 us in all at 4096 x 4096, rank 32, n 5120.
+template <int RT>
 __global__ __launch_bounds__(LORA_THREADS, 2) void lora_shrink_wide_kernel(LoraArgs a, int splits, int k_split, int rank_blocks) {
+    constexpr int DEPTH = 4;
     constexpr int NA = RT * 128 < LORA_THREADS ? 1 : RT * 128 / LORA_THREADS;   // chunks of the adapter's tile a thread
     __shared__ v4u at_tile[2][RT * 128];
-    __shared__ v4u x_tile[4][TT * 128];
+    __shared__ v4u x_tile[4][128];
     const int parts = splits * rank_blocks, line = blockIdx.x >> 3;
     const int id = (line / parts) * 8 + (blockIdx.x & 7), rest = line % parts;
     const int split = rest / rank_blocks, rank0 = (rest - split * rank_blocks) * (16 * RT);
-    const LoraBlock b = lora_block<4 * TT>(a, id);
+    const LoraBlock b = lora_block<true>(a, id);
     if (b.t0 >= b.t1 || b.adapter < 0) return;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, m = lane & 15, g = lane >> 4;
     const int k0 = split * k_split, len = min(a.k - k0, k_split);
-    const int lr = lane >> 3, lc = lane & 7, t0 = b.t0 + 16 * TT * wave;
+    const int lr = lane >> 3, lc = lane & 7, t0 = b.t0 + 16 * wave;
     const int ranks = min(a.rank - rank0, 16 * RT);
     const uint16_t* A = static_cast<const uint16_t*>(a.A) + ((int64_t)b.adapter * a.rank + rank0) * a.k + k0 + 8 * lc;
-    const uint16_t *arow[NA], *x[TT][2];
+    const uint16_t *arow[NA], *x[2];
 #pragma unroll
     for (int e = 0; e < NA; e++) arow[e] = A + (int64_t)min((int)(threadIdx.x >> 3) + 32 * e, ranks - 1) * a.k;
 #pragma unroll
-    for (int t = 0; t < TT; t++)
+    for (int e = 0; e < 2; e++)
+        x[e] = static_cast<const uint16_t*>(a.x) + (int64_t)min(t0 + 8 * e + lr, b.t1 - 1) * a.k + k0 + 8 * lc;
+    v4f acc[RT];
 #pragma unroll
-        for (int e = 0; e < 2; e++)
-            x[t][e] = static_cast<const uint16_t*>(a.x) + (int64_t)min(t0 + 16 * t + 8 * e + lr, b.t1 - 1) * a.k + k0 + 8 * lc;
-    v4f acc[RT][TT];
-#pragma unroll
-    for (int r = 0; r < RT; r++)
-#pragma unroll
-        for (int t = 0; t < TT; t++) acc[r][t] = v4f{0, 0, 0, 0};
+    for (int r = 0; r < RT; r++) acc[r] = v4f{0, 0, 0, 0};
     struct Unit {
-        v4u w[NA], x[TT][2];
+        v4u w[NA], x[2];
     };
     const int units = (len + 63) >> 6;
     auto load = [&](Unit& s, int u) {
         const int at = 64 * u;
         const bool live = at + 8 * lc < len;         // k is a multiple of 8
 #pragma unroll
-        for (int t = 0; t < TT; t++)
-#pragma unroll
-            for (int e = 0; e < 2; e++) s.x[t][e] = live ? *reinterpret_cast<const v4u*>(x[t][e] + at) : v4u{0, 0, 0, 0};
+        for (int e = 0; e < 2; e++) s.x[e] = live ? *reinterpret_cast<const v4u*>(x[e] + at) : v4u{0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < NA; e++) s.w[e] = live ? *reinterpret_cast<const v4u*>(arow[e] + at) : v4u{0, 0, 0, 0};
     };
@@ -236,37 +224,28 @@ __global__ __launch_bounds__(LORA_THREADS, 2) void lora_shrink_wide_kernel(LoraA
                 if (r < 16 * RT) tile[(r & ~15) * 8 + tile_at(r & 15, lc)] = ring[d].w[e];
             }
 #pragma unroll
-            for (int t = 0; t < TT; t++)
-#pragma unroll
-                for (int e = 0; e < 2; e++) x_tile[wave][t * 128 + tile_at(8 * e + lr, lc)] = ring[d].x[t][e];
+            for (int e = 0; e < 2; e++) x_tile[wave][tile_at(8 * e + lr, lc)] = ring[d].x[e];
             if (u + DEPTH < units) load(ring[d], u + DEPTH);
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < 2; j++) {
-                bf16x8 xf[TT];
-#pragma unroll
-                for (int t = 0; t < TT; t++) xf[t] = __builtin_bit_cast(bf16x8, x_tile[wave][t * 128 + tile_at(m, 4 * j + g)]);
+                const bf16x8 xf = __builtin_bit_cast(bf16x8, x_tile[wave][tile_at(m, 4 * j + g)]);
 #pragma unroll
                 for (int r = 0; r < RT; r++) {
                     const bf16x8 w = __builtin_bit_cast(bf16x8, tile[r * 128 + tile_at(m, 4 * j + g)]);
-#pragma unroll
-                    for (int t = 0; t < TT; t++)
-                        acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xf[t], acc[r][t], 0, 0, 0);
+                    acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, xf, acc[r], 0, 0, 0);
                 }
             }
         }
     }
     // lane: token m, ranks 16 r + 4 g + i
     const float scale = a.scale[b.adapter];
+    const int tok = t0 + m;
+    if (tok >= b.t1) return;
+    float* dst = a.workspace + ((int64_t)split * a.tokens + tok) * a.rank + rank0 + 4 * g;
 #pragma unroll
-    for (int t = 0; t < TT; t++) {
-        const int tok = t0 + 16 * t + m;
-        if (tok >= b.t1) continue;
-        float* dst = a.workspace + ((int64_t)split * a.tokens + tok) * a.rank + rank0 + 4 * g;
-#pragma unroll
-        for (int r = 0; r < RT; r++)    // ranks is a multiple of 8: 4 of them are inside or outside
-            if (16 * r + 4 * g < ranks) *reinterpret_cast<v4f*>(dst + 16 * r) = acc[r][t] * scale;
-    }
+    for (int r = 0; r < RT; r++)    // ranks is a multiple of 8: 4 of them are inside or outside
+        if (16 * r + 4 * g < ranks) *reinterpret_cast<v4f*>(dst + 16 * r) = acc[r] * scale;
 }
 
 // 16 bytes of a row of base or out: UNIT consecutive elements, aligned to
@@ -392,7 +371,7 @@ __global__ __launch_bounds__(LORA_THREADS) void lora_expand_kernel(LoraArgs a, i
     constexpr int UNITS = 16 / Out::UNIT, ESZ = Out::ESZ;
     extern __shared__ uint16_t pieces[];
     const int id = blockIdx.x / col_blocks, part = blockIdx.x - id * col_blocks;
-    const LoraBlock b = lora_block<1>(a, id);
+    const LoraBlock b = lora_block<false>(a, id);
     if (b.t0 >= b.t1) return;
     const int n0 = part * cols, n1 = min(a.n, n0 + cols);
     if (b.adapter < 0) return copy_block<F32>(a, b, n0, n1);
@@ -479,7 +458,7 @@ __global__ __launch_bounds__(LORA_THREADS, F32 ? 2 : 3) void lora_expand_wide_ke
     extern __shared__ uint16_t pieces[];
     const int line = blockIdx.x >> 3;      // a block's column parts: on one XCD, which then holds its h
     const int id = (line / col_blocks) * 8 + (blockIdx.x & 7), part = line % col_blocks;
-    const LoraBlock b = lora_block<4>(a, id);
+    const LoraBlock b = lora_block<true>(a, id);
     if (b.t0 >= b.t1) return;
     const int n0 = part * cols, n1 = min(a.n, n0 + cols);
     if (b.adapter < 0) return copy_block<F32>(a, b, n0, n1);
@@ -523,11 +502,10 @@ __global__ __launch_bounds__(LORA_THREADS, F32 ? 2 : 3) void lora_expand_wide_ke
     // pieces of h: each from a multiple of 64 on, zeros behind the rank
     const int stride = rank_steps * 64, row = PIECES * stride + 8;
     stage_pieces<PIECES, 4, 2>(a, b, splits, pieces, 64, stride, row);
-    const int tail = stride - a.rank;
-    for (int i = threadIdx.x; i < 64 * PIECES * tail; i += LORA_THREADS) {
-        const int t = i / (PIECES * tail), j = i - t * (PIECES * tail);
-        pieces[t * row + (j / tail) * stride + a.rank + j % tail] = 0;
-    }
+#pragma unroll
+    for (int p = 0; p < PIECES; p++)    // rank and stride are multiples of 8: 16 bytes at a time, 4 threads a token
+        for (int r = a.rank + 8 * (threadIdx.x & 3); r < stride; r += 32)
+            *reinterpret_cast<v4u*>(&pieces[(threadIdx.x >> 2) * row + p * stride + r]) = v4u{0, 0, 0, 0};
     const uint16_t* h = pieces + (16 * wave + m) * row + 8 * g;
     int buffer = 0;
     for (int strip = 0; strip < strips; strip++) {
@@ -544,6 +522,7 @@ __global__ __launch_bounds__(LORA_THREADS, F32 ? 2 : 3) void lora_expand_wide_ke
             else if (strip + 1 < strips) load(n + TILE, 0);
 #pragma unroll
             for (int j = 0; j < 2; j++) {
+                if (64 * rs + 32 * j >= a.rank) break;
                 bf16x8 x[PIECES];
 #pragma unroll
                 for (int p = 0; p < PIECES; p++) x[p] = *reinterpret_cast<const bf16x8*>(h + p * stride + 64 * rs + 32 * j);
@@ -589,24 +568,34 @@ static int lora_blocks(const LoraArgs& a, int tiles) {
     const int full = (a.tokens + 16 * tiles - 1) / (16 * tiles), some = a.segments < a.tokens ? a.segments : a.tokens;
     return full > some ? full : some;
 }
-// Segments of 32 tokens and more on average take larger blocks.
-static bool lora_wide(const LoraArgs& a) { return a.tokens / (a.segments > 0 ? a.segments : 1) >= 32; }
+// The forms for long segments, by the average segment.  Shrink + expand, us, wide
+// against narrow, k 4096, n 2048 (4096 tokens) or 4096 (the others):
+//   4096 tokens, rank 64:  8 tokens a segment 90 / 71, 16: 54 / 66, 64: 33 / 42
+//   4096 tokens, rank 16:  16: 42 / 39, 64: 27 / 24, 128: 19 / 24
+//   4096 tokens, rank 8:   128: 19 / 25
+//   1024 tokens, rank 64:  128: 19 / 22;  256 tokens in one: 14 / 12;  64: 13 / 11
+static bool lora_wide(const LoraArgs& a) {
+    const int64_t segment = a.tokens / (a.segments > 0 ? a.segments : 1);
+    return a.tokens >= 512 && segment >= 16 && segment * a.rank >= 1024;
+}
 
 struct LoraPlan {
     int tiles, splits, k_split, rank_blocks;
 };
 static LoraPlan lora_plan(const LoraArgs& a) {
     LoraPlan p;
-    // 128 tokens a block read the adapter half as often as 64, which waste less
-    // on the last block of a segment
-    p.tiles = !lora_wide(a) ? 1 : a.tokens / (a.segments > 0 ? a.segments : 1) >= 256 ? 8 : 4;
+    p.tiles = lora_wide(a) ? 4 : 1;
     p.rank_blocks = a.rank <= 64 ? 1 : p.tiles > 1 ? (a.rank + 63) / 64 : (a.rank + 127) / 128;
     const int blocks = lora_blocks(a, p.tiles) * p.rank_blocks;
     // two workgroups a CU at once, of at least 256 of k each
+    // expand reads every slice of h in each of its column parts: 16 instead of 8
+    // cost a wide one 2 to 4 us of 16; with 4 shrink loses what expand gains
+    const int max_splits = p.tiles > 1 ? 8 : 16;
     int splits = 512 / blocks;
-    const int most = (a.k + 255) / 256;
+    int most = (a.k + 255) / 256;
+    most = most > max_splits ? max_splits : most;
     splits = splits > most ? most : splits;
-    splits = splits > LORA_MAX_SPLITS ? LORA_MAX_SPLITS : splits < 1 ? 1 : splits;
+    splits = splits < 1 ? 1 : splits;             // k may be 0
     p.k_split = ((a.k + splits - 1) / splits + 127) / 128 * 128;
     p.splits = a.k > 0 ? (a.k + p.k_split - 1) / p.k_split : 0;
     return p;
@@ -621,13 +610,10 @@ template <int RT>
 static hipError_t shrink(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
     const dim3 grid((unsigned)((lora_ids(a, p.tiles) + 7) / 8 * 8 * p.splits * p.rank_blocks)), block(LORA_THREADS);
     if (p.tiles == 1) {
-        lora_shrink_kernel<RT, 1><<<grid, block, 0, stream>>>(a, p.splits, p.k_split, p.rank_blocks);
+        lora_shrink_kernel<RT><<<grid, block, 0, stream>>>(a, p.splits, p.k_split, p.rank_blocks);
     } else {
         constexpr int R = RT < 4 ? RT : 4;      // rank blocks of 64
-        if (p.tiles == 8)
-            lora_shrink_wide_kernel<R, 2, 3><<<grid, block, 0, stream>>>(a, p.splits, p.k_split, p.rank_blocks);
-        else
-            lora_shrink_wide_kernel<R, 1, 4><<<grid, block, 0, stream>>>(a, p.splits, p.k_split, p.rank_blocks);
+        lora_shrink_wide_kernel<R><<<grid, block, 0, stream>>>(a, p.splits, p.k_split, p.rank_blocks);
     }
     return hipGetLastError();
 }
@@ -636,7 +622,9 @@ template <bool F32>
 static hipError_t expand(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
     const bool wide = lora_wide(a);
     const int tiles = wide ? 4 : 1, blocks = lora_blocks(a, tiles), unit = wide ? 128 : 256;
-    // wide: what fits on the chip at once, three workgroups a CU
+    // wide: what fits on the chip at once, three workgroups a CU (expand of 8192
+    // tokens, rank 64, n 4096: 34 us; two a CU 38, four 39).  narrow: 2048 in all,
+    // as its workgroups live short (a quarter or half of that is slower).
     int col_blocks = wide ? 768 / blocks : (2048 + blocks - 1) / blocks;
     if (col_blocks < 1) col_blocks = 1;
     const int most = (a.n + unit - 1) / unit;

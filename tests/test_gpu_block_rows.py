@@ -202,6 +202,21 @@ def test_lora_long_segments(gpu_lib, dtype, T):
     lora_check(gpu_lib.lora_add(*args), ref, 2056, 64, dtype)
 
 
+# Long segments at ranks that end inside a unit of 32 or 64, empty segments and
+# tokens of no segment between them, an odd number of columns.
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("rank", [8, 24, 40, 64, 72, 200, 256])
+@pytest.mark.parametrize("T,n,k", [(530, 129, 72), (777, 1001, 8)])
+def test_lora_long_segments_ranks(gpu_lib, dtype, rank, T, n, k):
+    ref, args = lora_case(8, T, n, k, rank, 3, [5, 200, 200, T - 65, T - 1], [2, 1, -1, 0], dtype)
+    say("lora_add", dtype, rank, T, n, k)
+    got = gpu_lib.lora_add(*args)
+    lora_check(got, ref, k, rank, dtype)
+    base = args[0]
+    gpu_lib.lora_add(*args, out=base)
+    assert torch.equal(base, got)
+
+
 @pytest.mark.parametrize("k,rank,N", [(0, 16, 2), (32, 0, 2), (32, 16, 0)])
 def test_lora_nothing_to_add(gpu_lib, k, rank, N):
     ref, args = lora_case(4, 20, 100, k, rank, N, [0, 20], [0], BF)
