@@ -573,10 +573,11 @@ static int lora_blocks(const LoraArgs& a, int tiles) {
 //   4096 tokens, rank 64:  8 tokens a segment 90 / 71, 16: 54 / 66, 64: 33 / 42
 //   4096 tokens, rank 16:  16: 42 / 39, 64: 27 / 24, 128: 19 / 24
 //   4096 tokens, rank 8:   128: 19 / 25
+//   4096 tokens, rank 32:  16: 43 / 44, 32: 27 / 28;  1024 tokens: 64: 20 / 16
 //   1024 tokens, rank 64:  128: 19 / 22;  256 tokens in one: 14 / 12;  64: 13 / 11
 static bool lora_wide(const LoraArgs& a) {
-    const int64_t segment = a.tokens / (a.segments > 0 ? a.segments : 1);
-    return a.tokens >= 512 && segment >= 16 && segment * a.rank >= 1024;
+    const int segment = a.tokens / (a.segments > 0 ? a.segments : 1);
+    return a.tokens >= 512 && segment >= (a.rank > 32 ? 16 : 128);
 }
 
 struct LoraPlan {
