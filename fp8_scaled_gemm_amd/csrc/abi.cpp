@@ -206,11 +206,11 @@ const char* fp8g_status_string(int status) {
     switch (status) {
         case FP8G_OK: return "ok";
         case FP8G_ERR_NULL: return "a required pointer is NULL";
-        case FP8G_ERR_SHAPE: return "invalid shape (negative extent, or k / cols not a multiple of 32 for MXFP8)";
-        case FP8G_ERR_ALIGN: return "a pointer is not 16-byte aligned";
+        case FP8G_ERR_SHAPE: return "invalid shape (negative extent, k / cols not a multiple of 32 for MXFP8, a stride below its row, or arguments that exclude each other)";
+        case FP8G_ERR_ALIGN: return "a pointer is not aligned (16 bytes; index arrays: their element)";
         case FP8G_ERR_DTYPE: return "unknown output dtype, operand format, input dtype, granularity or element size";
         case FP8G_ERR_OVERLAP: return "an output overlaps an input or another output";
-        case FP8G_ERR_UNSUPPORTED: return "outside the library's limits (GEMM: k % 16, k >= 2^23, m >= 2^31, a 256-row panel of D over 2^31 bytes; quantizer rows >= 2^31; size overflow)";
+        case FP8G_ERR_UNSUPPORTED: return "outside the library's limits (GEMM: k % 16, k >= 2^23, m >= 2^31, a 256-row panel of D over 2^31 bytes; quantizer rows >= 2^31; head dims, ranks, page sizes or a workspace that fp8g_block.h does not allow; size overflow)";
         case FP8G_ERR_HIP: return "the HIP runtime rejected the launch";
         default: return "unknown status";
     }

@@ -15,6 +15,10 @@
 // HBM-bound: a lane holds 8 elements (16 bytes of bf16, 4 bytes of codes), a
 // block of 32 lies in 4 neighbouring lanes, and a thread has 4 of them in flight.
 // Keys and values go in one launch.
+//
+// Measured: 16384 tokens x 16 heads x (192 + 128) bf16, append 47 us, gather 47 us,
+// 4.5 TB/s (a 2 GB copy: 4.95); 57 and 49 before 16 tokens lay side by side,
+// four chunks were in flight and divisions were multiplies.
 
 #include "device_common.h"
 #include "launch_block.h"

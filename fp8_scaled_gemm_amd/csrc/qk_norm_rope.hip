@@ -18,6 +18,10 @@
 // passed through) instead of exchanging them over the lanes.  The loads of a
 // row come before its store in the same wave, and a wave holds whole rows, so
 // a row may be written in place.
+//
+// Measured: 8192 tokens x 72 heads x 128 bf16, three axes, 66 us, 4.7 TB/s (a 2 GB
+// copy on the same card: 4.95); 411 us before C and S lay in LDS and rows were in
+// flight while others are worked out.
 
 #include "device_common.h"
 #include "launch_block.h"
