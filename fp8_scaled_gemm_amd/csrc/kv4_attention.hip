@@ -101,6 +101,14 @@ __device__ __forceinline__ float over_groups_sum(float v) {
     return v + __shfl_xor(v, 32, 64);
 }
 
+// A maximum of -inf alone does not say that a row has seen nothing: maxima drop
+// NaN, and a row of nothing but NaN scores has one, too, with a sum of NaN.  Its
+// part goes to the join with a maximum of NaN, where -inf stands for no part.
+__device__ __forceinline__ bool saw_nothing(float m, float l) { return m == -INFINITY && l == 0.0f; }
+__device__ __forceinline__ float part_max(float m, float l) {
+    return m == -INFINITY && !saw_nothing(m, l) ? __builtin_nanf("") : m;
+}
+
 // What a block of rows sees.
 struct AttnBlock {
     int seq, row0, rows, q0, queries, kv;
@@ -450,16 +458,20 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
 #pragma unroll
         for (int d = 0; d < DT; d += 4) *reinterpret_cast<v4f*>(dst + d) = v4f{r[d], r[d + 1], r[d + 2], r[d + 3]};
         if (tl == 0) {
-            part_ml[(target * p.splits + split) * 2] = mm;
+            part_ml[(target * p.splits + split) * 2] = part_max(mm, ll);
             part_ml[(target * p.splits + split) * 2 + 1] = ll;
         }
     } else {
-        const float inv = ll > 0.0f ? 1.0f / ll : (mm == -INFINITY ? 0.0f : 1.0f / ll);
+        // a row without keys may hold NaN from values that others of its block see
+        const bool none = saw_nothing(mm, ll);
+        const float inv = 1.0f / ll;
+#pragma unroll
+        for (int d = 0; d < DT; d++) r[d] = none ? 0.0f : r[d] * inv;
         uint16_t* dst = static_cast<uint16_t*>(a.out) + target * DV + DT * tl;
 #pragma unroll
         for (int d = 0; d < DT; d += 4)
-            *reinterpret_cast<v2u*>(dst + d) = v2u{bf16x2_bits(r[d] * inv, r[d + 1] * inv), bf16x2_bits(r[d + 2] * inv, r[d + 3] * inv)};
-        if (a.lse && tl == 0) a.lse[target] = mm == -INFINITY ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f;
+            *reinterpret_cast<v2u*>(dst + d) = v2u{bf16x2_bits(r[d], r[d + 1]), bf16x2_bits(r[d + 2], r[d + 3])};
+        if (a.lse && tl == 0) a.lse[target] = none ? -INFINITY : (mm + __builtin_amdgcn_logf(ll)) * 0.6931471805599453f;
     }
 }
 
@@ -885,19 +897,21 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<v4f*>(dst + 32 * d + 2 * i) = v4f{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
         if (e == 0) {
-            part_ml[(target * p.splits + split) * 2] = m;
+            part_ml[(target * p.splits + split) * 2] = part_max(m, l);
             part_ml[(target * p.splits + split) * 2 + 1] = l;
         }
     } else {
-        const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+        const bool none = saw_nothing(m, l);
+        const float inv = 1.0f / l;
+        auto result = [&](float x) { return none ? 0.0f : x * inv; };
         uint16_t* dst = static_cast<uint16_t*>(a.out) + target * DV + 4 * e;
 #pragma unroll
         for (int d = 0; d < DT; d++)
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<v2u*>(dst + 32 * d + 2 * i) =
-                    v2u{bf16x2_bits(o[d][i] * inv, o[d][i + 1] * inv), bf16x2_bits(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-        if (a.lse && e == 0) a.lse[target] = m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+                    v2u{bf16x2_bits(result(o[d][i]), result(o[d][i + 1])), bf16x2_bits(result(o[d][i + 2]), result(o[d][i + 3]))};
+        if (a.lse && e == 0) a.lse[target] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
     }
 }
 
@@ -934,17 +948,18 @@ __global__ __launch_bounds__(ATTN_THREADS) void kv4_attention_join_kernel(Kv4Att
         m = top;
 #pragma unroll
         for (int u = 0; u < AHEAD; u++) {
-            // an empty chunk has written -inf and no more: the rest may be anything
+            // a chunk without keys of the row has -inf, and the rest may be anything
             if (s0 + u >= p.splits || ms[u] == -INFINITY) continue;
             const float f = __builtin_amdgcn_exp2f(ms[u] - mu);
             l += ls[u] * f;
             o += os[u] * f;
         }
     }
-    const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
+    const bool none = saw_nothing(m, l);
+    const float inv = none ? 0.0f : 1.0f / l;
     *reinterpret_cast<v2u*>(static_cast<uint16_t*>(a.out) + row * DV + 4 * lane) =
         v2u{bf16x2_bits(o[0] * inv, o[1] * inv), bf16x2_bits(o[2] * inv, o[3] * inv)};
-    if (a.lse && lane == 0) a.lse[row] = m == -INFINITY ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
 // Many rows a sequence on average: blocks of 256 rows, not 16.  8 sequences of

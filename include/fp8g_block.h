@@ -157,7 +157,8 @@ int kv4_gather(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v
  *   key j  if  j < kv_len[b]  and (not causal or j <= p)
  *              and (window == 0 or j > p - window).
  *   s_j = scale * q . k_j;  out = sum_j softmax(s)_j v_j;  lse = log sum_j exp s_j
- * over the keys it sees; a query that sees none has out = 0, lse = -inf.
+ * over the keys it sees; a query that sees none has out = 0, lse = -inf, one
+ * with a score of NaN or +inf NaN in both.
  * Query head h reads key head h / (q_heads / kv_heads).
  * Products on the bf16 matrix cores (keys and values are exact in bf16, the
  * softmax weights are rounded to bf16), sums and statistics in fp32.
@@ -173,6 +174,8 @@ int kv4_gather(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v
  *          not written
  * lse      device, fp32 [queries, q_heads], or NULL
  * Bytes of a page beyond kv_len, and in front of the window, may hold anything.
+ * A value that is no finite number (scale codes from 254 on) may also give NaN
+ * to queries of its sequence that do not see it but whose neighbours do.
  * Limits (ERR_UNSUPPORTED): other dims; page_size % 16 != 0; q_heads not a
  * multiple of kv_heads; max_pages * page_size > 2^30; queries * q_heads >=
  * 2^31; batch > 2^20; strides not a multiple of 16 bytes; a workspace smaller
