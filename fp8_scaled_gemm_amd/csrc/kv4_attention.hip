@@ -183,18 +183,19 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
 
     // A negative scale turns the queries' signs, so that the largest product is
     // the largest score; a scale of zero becomes one that changes nothing and
-    // keeps -inf * scale at -inf.
+    // keeps -inf * scale at -inf; a scale of NaN becomes that, too, and turns the
+    // queries to NaN, so that rows without keys stay without.
     const float c2 = __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, 0x1p-120f);
     // queries: dims in the order of the keys' pieces
     bf16x8 q[KW];
     {
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, spoil = a.scale != a.scale ? 0x7FFF7FFFu : 0u;
         const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(b.q0 + qi) * a.q_stride + (int64_t)head * DK;
 #pragma unroll
         for (int j = 0; j < KW; j++) {
             const int d = DK == 64 ? 16 * g + 8 * j : (j < 4 ? 32 * g + 8 * j : 128 + 16 * g + 8 * (j - 4));
             const v4u w = *reinterpret_cast<const v4u*>(src + d);
-            q[j] = __builtin_bit_cast(bf16x8, v4u{w[0] ^ flip, w[1] ^ flip, w[2] ^ flip, w[3] ^ flip});
+            q[j] = __builtin_bit_cast(bf16x8, v4u{(w[0] ^ flip) | spoil, (w[1] ^ flip) | spoil, (w[2] ^ flip) | spoil, (w[3] ^ flip) | spoil});
         }
     }
 
@@ -561,16 +562,17 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
 
     // A negative scale turns the queries' signs, so that the largest product is
     // the largest score; a scale of zero becomes one that changes nothing and
-    // keeps -inf * scale at -inf.
+    // keeps -inf * scale at -inf; a scale of NaN becomes that, too, and turns the
+    // queries to NaN, so that rows without keys stay without.
     const float c2 = __builtin_fmaxf(__builtin_fabsf(a.scale) * 1.4426950408889634f, 0x1p-120f);
     bf16x8 q[KK];
     {
         const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(b.q0 + qi) * a.q_stride + (int64_t)head * DK + 8 * e;
-        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+        const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, spoil = a.scale != a.scale ? 0x7FFF7FFFu : 0u;
 #pragma unroll
         for (int j = 0; j < KK; j++) {
             const v4u w = *reinterpret_cast<const v4u*>(src + 16 * j);
-            q[j] = __builtin_bit_cast(bf16x8, v4u{w[0] ^ flip, w[1] ^ flip, w[2] ^ flip, w[3] ^ flip});
+            q[j] = __builtin_bit_cast(bf16x8, v4u{(w[0] ^ flip) | spoil, (w[1] ^ flip) | spoil, (w[2] ^ flip) | spoil, (w[3] ^ flip) | spoil});
         }
     }
 

@@ -88,3 +88,10 @@ def test_rows_without_keys_stay_zero(gpu_lib, q_lens, kv_lens):
     spoiled = np.zeros(out[1].shape, bool)
     spoiled[q_lens[0] - kv_lens[0]:q_lens[0], :4] = True
     check(*out, spoiled)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_lens,kv_lens,split", SHAPES + [([300, 40], [120, 90], False), ([40, 3, 1], [12, 900, 0], True)])
+def test_scale(gpu_lib, q_lens, kv_lens, split, causal):
+    out = attention(gpu_lib, q_lens, kv_lens, split, lambda q, paged: None, scale=float("nan"), causal=causal)
+    check(*out, ~np.isinf(out[3][0]))           # all but rows that see no key
