@@ -313,7 +313,10 @@ __device__ __forceinline__ void copy_block(const LoraArgs& a, const LoraBlock& b
 
 // h of a block's tokens in LDS, as bf16 pieces: row = pieces * rank elements up
 // to a multiple of `fill`, zeros behind them, and 8 more that keep rows off each
-// other's banks.  The slices are summed in order.
+// other's banks.  The slices are summed in order.  All pieces but the last are cut
+// to bf16's finite range: what would round to infinity leaves its rest to the next
+// one, and an infinite or NaN h passes on to the last (infinity less infinity would
+// make a NaN of it).
 template <int PIECES, int ITEMS, int SLICES>   // so many loads of a thread in flight
 __device__ __forceinline__ void stage_pieces(const LoraArgs& a, const LoraBlock& b, int splits, uint16_t* pieces, int tokens,
                                              int stride, int row) {
@@ -351,7 +354,10 @@ __device__ __forceinline__ void stage_pieces(const LoraArgs& a, const LoraBlock&
             if (i0 + e * LORA_THREADS >= tokens * quads) break;
 #pragma unroll
             for (int q = 0; q < PIECES; q++) {
-                const uint32_t lo = bf16x2_bits(h[e][0], h[e][1]), hi = bf16x2_bits(h[e][2], h[e][3]);
+                auto piece = [&](float v) {
+                    return q + 1 < PIECES ? __builtin_amdgcn_fmed3f(v, -0x1.FEp127f, 0x1.FEp127f) : v;
+                };
+                const uint32_t lo = bf16x2_bits(piece(h[e][0]), piece(h[e][1])), hi = bf16x2_bits(piece(h[e][2]), piece(h[e][3]));
                 *reinterpret_cast<v2u*>(&pieces[tok[e] * row + q * stride + r[e]]) = v2u{lo, hi};
                 h[e] -= v4f{__builtin_bit_cast(float, lo << 16), __builtin_bit_cast(float, lo & 0xFFFF0000u),
                             __builtin_bit_cast(float, hi << 16), __builtin_bit_cast(float, hi & 0xFFFF0000u)};

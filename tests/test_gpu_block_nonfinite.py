@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from block_util import BF16_HALF, F32_HALF, Paged, bf16, close, host, rng
+from block_util import BF16_HALF, F32_HALF, Paged, bf16, close, half_ulp, host, rng, typed
 from gpu_util import say
 from oracle import block
 
@@ -95,3 +95,39 @@ def test_rows_without_keys_stay_zero(gpu_lib, q_lens, kv_lens):
 def test_scale(gpu_lib, q_lens, kv_lens, split, causal):
     out = attention(gpu_lib, q_lens, kv_lens, split, lambda q, paged: None, scale=float("nan"), causal=causal)
     check(*out, ~np.isinf(out[3][0]))           # all but rows that see no key
+
+
+# short segments and long ones (those at rank 64), two pieces of h and three
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,rank", [(40, 16), (600, 64)])
+def test_adapter_sums_at_the_end_of_float32(gpu_lib, dtype, T, rank):
+    r = rng(T, rank)
+    n, k, N = 200, 256, 2
+    base64, base = typed(r.standard_normal((T, n)), dtype)
+    x64, x = bf16(r.standard_normal((T, k)))
+    A64, A = bf16(r.standard_normal((N, rank, k)) * k ** -0.5)
+    B64, B = bf16(0.25 * np.sign(r.standard_normal((N, n, rank))))
+    # columns 7 and 8 of x count in rank 3 of adapter 0 only
+    for a in (A64, A):
+        a[0, :, 7:9] = 0.0
+        a[0, 3, 7], a[0, 3, 8] = 255 / 128, 0.75
+    over, most, nan = 5, 11, 13
+    for t, pair in ((over, (3e38, 3e38)), (most, (2.0 ** 127, 2.0 ** 120)), (nan, (float("nan"), 0.0))):
+        x[t, 7], x[t, 8] = pair
+        x64[t, 7:9] = x[t, 7:9].double().numpy()
+    # most: h = 255.75 * 2^120, above every bf16 number and below 2^128
+    cuts, adapters = [0, 20, T], [0, 1]
+    say("lora_add", T, rank, dtype, "not finite")
+    got = host(gpu_lib.lora_add(base.cuda(), x.cuda(), A.cuda(), B.cuda(), torch.ones(N, device="cuda"),
+                                torch.tensor(cuts, dtype=torch.int32).cuda(), torch.tensor(adapters, dtype=torch.int32).cuda()))
+    assert np.isnan(got[nan]).all()
+    # 1.2e39 in float32
+    assert np.array_equal(got[over], np.inf * np.sign(B64[0, :, 3]))
+    rest = np.ones(T, bool)
+    rest[[over, nan]] = False
+    x64[~rest] = 0.0
+    want, low, full = block.lora_add(base64, x64, A64, B64, np.ones(N), cuts, adapters)
+    # as in test_gpu_block_rows.py
+    tol = half_ulp(dtype) * np.abs(want) * 1.01 + (2.0 ** -16 if dtype == torch.bfloat16 else 2.0 ** -22) * low + \
+        (k + 3 * rank + 8) * F32_HALF * full + 2 * F32_HALF * np.abs(base64)
+    close(got[rest], want[rest], tol[rest], "lora_add")
