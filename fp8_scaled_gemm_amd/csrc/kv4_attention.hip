@@ -57,11 +57,13 @@ constexpr int ATTN_THREADS = 256;
 constexpr int ATTN_ROWS_LOG2 = 4, ATTN_ROWS = 1 << ATTN_ROWS_LOG2;
 constexpr int ATTN_STEP = 64;                      // keys of a wave's step
 constexpr int ATTN_CHUNK = 4 * ATTN_STEP;          // keys of a workgroup's step
+constexpr int ATTN_LONGEST = 16384;                // keys of a chunk, where there are splits enough
 constexpr float ATTN_SLACK = 8.0f;                 // growth of a maximum that is left to the weights, in powers of two
 
+// fill: chunks of a block's keys that fill the chip; splits: the most that it can have
 struct AttnPlan {
-    int ids, chunk, splits;
-    FastDiv page;
+    int ids, fill, splits;
+    FastDiv page, by_fill, by_splits;
 };
 
 // Two E2M1 elements (byte SEL of codes) times 2^(scale - 127), as bf16.
@@ -99,6 +101,23 @@ __device__ __forceinline__ float over_groups_max(float v) {
 __device__ __forceinline__ float over_groups_sum(float v) {
     v += __shfl_xor(v, 16, 64);
     return v + __shfl_xor(v, 32, 64);
+}
+
+// Chunk `split` of the keys [lo, hi) that a block sees: equal parts of whole
+// workgroup steps.  The lengths are known here only; the host knows no more than
+// how wide the page table is.
+struct AttnPart {
+    int begin, end;
+};
+template <bool SPLIT>
+__device__ __forceinline__ AttnPart attn_part(const AttnPlan& p, int split, int lo, int hi) {
+    const int from = lo & ~(ATTN_STEP - 1);
+    if (!SPLIT) return AttnPart{from, hi};
+    const int steps = (max(hi - from, 0) + ATTN_CHUNK - 1) / ATTN_CHUNK;
+    int per = (int)divide(steps + p.fill - 1, p.by_fill);
+    if (per > ATTN_LONGEST / ATTN_CHUNK) per = max(ATTN_LONGEST / ATTN_CHUNK, (int)divide(steps + p.splits - 1, p.by_splits));
+    const int64_t begin = from + (int64_t)split * per * ATTN_CHUNK;
+    return AttnPart{(int)min(begin, (int64_t)hi), (int)min(begin + per * ATTN_CHUNK, (int64_t)hi)};
 }
 
 // A maximum of -inf alone does not say that a row has seen nothing: maxima drop
@@ -171,8 +190,8 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
     const int q_first = b.row0 / group, q_last = (min(b.row0 + ATTN_ROWS, b.rows) - 1) / group;
     const int all_lo = min(low_of(q_first), b.kv), all_hi = top_of(q_last);   // of the union
     const int in_lo = low_of(q_last), in_hi = top_of(q_first);                // of the intersection
-    const int64_t begin = (all_lo & ~(ATTN_STEP - 1)) + (int64_t)split * p.chunk;
-    const int end = (int)min((int64_t)all_hi, begin + p.chunk);
+    const AttnPart part = attn_part<SPLIT>(p, split, all_lo, all_hi);
+    const int begin = part.begin, end = part.end;
     const int64_t out_row = (int64_t)(b.q0 + qi) * a.q_heads + head;
     float* const part_o = a.workspace;
     float* const part_ml = a.workspace + (int64_t)a.queries * a.q_heads * p.splits * DV;
@@ -409,7 +428,7 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
         }
     };
     Step s;
-    int base = (int)begin + ATTN_STEP * wave;
+    int base = begin + ATTN_STEP * wave;
     if (base < end) {
         entry = look(base);
         load(s, base);
@@ -550,15 +569,15 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     const int q_first = b.row0 / group, q_last = (min(b.row0 + ROWS, b.rows) - 1) / group;
     const int all_lo = min(low_of(q_first), b.kv), all_hi = top_of(q_last);
     const int in_lo = low_of(q_last), in_hi = top_of(q_first);
-    const int64_t begin64 = (all_lo & ~(ATTN_STEP - 1)) + (int64_t)split * p.chunk;
-    const int end = (int)min((int64_t)all_hi, begin64 + p.chunk);
+    const AttnPart part = attn_part<SPLIT>(p, split, all_lo, all_hi);
+    const int begin = part.begin, end = part.end;
     const int64_t target = (int64_t)(b.q0 + qi) * a.q_heads + head;
     float* const part_ml = a.workspace + (int64_t)a.queries * a.q_heads * p.splits * DV;
-    if (SPLIT && begin64 >= end) {
+    if (SPLIT && begin >= end) {
         if (e == 0 && real) part_ml[(target * p.splits + split) * 2] = -INFINITY;
         return;
     }
-    const int begin = (int)begin64, steps = begin < end ? (end - begin + ATTN_STEP - 1) / ATTN_STEP : 0;
+    const int steps = begin < end ? (end - begin + ATTN_STEP - 1) / ATTN_STEP : 0;
 
     // A negative scale turns the queries' signs, so that the largest product is
     // the largest score; a scale of zero becomes one that changes nothing and
@@ -930,28 +949,41 @@ __global__ __launch_bounds__(ATTN_THREADS) void kv4_attention_join_kernel(Kv4Att
     const float* part_o = a.workspace + row * p.splits * DV + 4 * lane;
     const float* part_ml = a.workspace + rows * p.splits * DV + row * p.splits * 2;
     constexpr int AHEAD = 8;            // chunks in flight
-    float m = -INFINITY, l = 0.0f;
-    v4f o = {0, 0, 0, 0};
-    for (int s0 = 0; s0 < p.splits; s0 += AHEAD) {
-        float ms[AHEAD], ls[AHEAD];
-        v4f os[AHEAD];
+    float ms[AHEAD], ls[AHEAD];
+    v4f os[AHEAD];
+    auto load = [&](int s0) {
 #pragma unroll
         for (int u = 0; u < AHEAD; u++) {
             const int s = min(s0 + u, p.splits - 1);
             ms[u] = part_ml[2 * s], ls[u] = part_ml[2 * s + 1];
             os[u] = *reinterpret_cast<const v4f*>(part_o + (int64_t)s * DV);
         }
+    };
+    // The chunks in front of the last that holds keys of the row: a table far
+    // wider than the context leaves most of them empty.  Found by the row's lanes
+    // together, a maximum each, while the first chunks travel.
+    load(0);
+    int used = p.splits <= AHEAD ? p.splits : 0;
+    for (int s0 = 0; s0 < p.splits && p.splits > AHEAD; s0 += LANES) {
+        const bool holds = s0 + lane < p.splits && part_ml[2 * (s0 + lane)] != -INFINITY;
+        const uint64_t all = __ballot(holds) >> (threadIdx.x & 63 & ~(LANES - 1)) & ((1ull << LANES) - 1);
+        if (all) used = s0 + 64 - __builtin_clzll(all);
+    }
+    float m = -INFINITY, l = 0.0f;
+    v4f o = {0, 0, 0, 0};
+    for (int s0 = 0; s0 < used; s0 += AHEAD) {
+        if (s0 > 0) load(s0);
         float top = m;
 #pragma unroll
         for (int u = 0; u < AHEAD; u++)
-            if (s0 + u < p.splits) top = __builtin_fmaxf(top, ms[u]);
+            if (s0 + u < used) top = __builtin_fmaxf(top, ms[u]);
         const float mu = top == -INFINITY ? 0.0f : top, f0 = __builtin_amdgcn_exp2f(m - mu);
         l *= f0, o *= f0;
         m = top;
 #pragma unroll
         for (int u = 0; u < AHEAD; u++) {
             // a chunk without keys of the row has -inf, and the rest may be anything
-            if (s0 + u >= p.splits || ms[u] == -INFINITY) continue;
+            if (s0 + u >= used || ms[u] == -INFINITY) continue;
             const float f = __builtin_amdgcn_exp2f(ms[u] - mu);
             l += ls[u] * f;
             o += os[u] * f;
@@ -988,19 +1020,37 @@ static AttnPlan attn_plan(const Kv4AttnArgs& a) {
     if (blocks < some) blocks = some;
     blocks *= a.kv_heads;
     // Two workgroups a CU fill the chip; more and smaller chunks cost more than
-    // they balance (measured with 1024 and 2048).  A chunk of at most 16384 keys
-    // keeps one long sequence among short ones from being the whole time.
-    constexpr int64_t full = 512, longest = 16384;
-    int64_t want = blocks >= full ? 1 : full / blocks;
-    if (want < (keys + longest - 1) / longest) want = (keys + longest - 1) / longest;
+    // they balance (measured with 1024 and 2048).
+    // A chunk of at most 16384 keys keeps one long sequence among short ones from
+    // being the whole time.  64 heads over 8, dims 128, us with 8192 / 16384 / 32768 /
+    // 65536: 131072 keys beside 63 sequences of 2048 171 / 171 / 238 / 357; 32 sequences
+    // of 32768 to 131072 keys 554 / 570 / 616 / 629; 64 of 4165 to 16384 165 / 161 / 161 /
+    // 161.  But a wide table says little about the contexts, and every split has its
+    // workgroups, empty or not, and its place in the workspace: at most 16 splits for
+    // that, and a workspace of 64 MB, what rows that need splits to fill the chip take
+    // at most.  With a table of 2^20 keys and 8 / 16 / 64 splits: the 64 sequences 168 /
+    // 172 / 184 us, one of 2^20 keys beside 63 of 2048 1031 / 607 / 617.
+    constexpr int64_t full = 512, longest_splits = 16, room = 64 << 20;
+    const int64_t steps = (keys + ATTN_CHUNK - 1) / ATTN_CHUNK;
+    int64_t fill = blocks >= full ? 1 : full / blocks;
     const int64_t most = ((int64_t)1 << 30) / ((int64_t)p.ids * a.kv_heads);   // keeps the grid's size an int
-    if (want > most) want = most < 1 ? 1 : most;
-    const int64_t least = wide ? 4 * ATTN_STEP : ATTN_CHUNK;
-    int64_t chunk = ((keys + want - 1) / want + ATTN_CHUNK - 1) / ATTN_CHUNK * ATTN_CHUNK;
-    if (chunk < least) chunk = least;
-    p.chunk = (int)chunk;
-    p.splits = (int)((keys + chunk - 1) / chunk);
-    if (p.splits < 1) p.splits = 1;
+    if (fill > most) fill = most < 1 ? 1 : most;
+    if (steps > 0) {
+        const int64_t each = (steps + fill - 1) / fill;
+        fill = (steps + each - 1) / each;
+    } else {
+        fill = 1;
+    }
+    int64_t splits = (keys + ATTN_LONGEST - 1) / ATTN_LONGEST;
+    if (splits > longest_splits) splits = longest_splits;
+    const int64_t fits = room / ((int64_t)a.queries * a.q_heads * (a.dv + 2) * 4);
+    if (splits > fits) splits = fits;
+    if (splits > most) splits = most;
+    if (splits < fill) splits = fill;
+    p.fill = (int)fill;
+    p.splits = (int)splits;
+    p.by_fill = fast_div((uint32_t)fill);
+    p.by_splits = fast_div((uint32_t)splits);
     return p;
 }
 

@@ -192,7 +192,8 @@ int kv4_attention(const void* q, int64_t q_stride, int64_t queries, int64_t q_he
                   int causal, int64_t window, void* out, float* lse, void* workspace, int64_t workspace_bytes,
                   hipStream_t stream);
 
-/* Bytes of workspace kv4_attention needs; -1 for sizes it refuses. */
+/* Bytes of workspace kv4_attention needs; -1 for sizes it refuses.  At most 69
+ * MB, however long the table's rows are. */
 int64_t kv4_attention_workspace(int64_t queries, int64_t q_heads, int64_t kv_heads, int64_t dk, int64_t dv,
                                 int64_t batch, int64_t max_pages, int64_t page_size, int64_t window);
 
