@@ -18,7 +18,7 @@ def wide_tables(request, monkeypatch):
     class Wide(block_util.Paged):
         def __init__(self, *args, **kwargs):
             super().__init__(*args, **kwargs)
-            more = request.param // self.page - self.max_pages
+            more = max(0, request.param // self.page - self.max_pages)
             wild = rng(3).choice([-7, 1 << 30, -(1 << 31), 0], size=(len(self.table), more)).astype(np.int32)
             self.table = np.concatenate([self.table, wild], 1)
             self.max_pages += more
