@@ -51,16 +51,30 @@ int hip_status(hipError_t e) { return e == hipSuccess ? FP8G_OK : FP8G_ERR_HIP; 
 
 constexpr int64_t LIM28 = (int64_t)1 << 28, LIM31 = (int64_t)1 << 31;
 
+fp8g::LoraArgs lora_sizes(int64_t tokens, int64_t n, int64_t k, int64_t rank, int64_t adapters, int64_t segments) {
+    fp8g::LoraArgs a = {};
+    a.tokens = (int32_t)tokens, a.n = (int32_t)n, a.k = (int32_t)k, a.rank = (int32_t)rank;
+    a.adapters = (int32_t)adapters, a.segments = (int32_t)segments;
+    return a;
+}
+
 int check_lora_sizes(int64_t tokens, int64_t n, int64_t k, int64_t rank, int64_t adapters, int64_t segments) {
     if (tokens < 0 || n < 0 || k < 0 || rank < 0 || adapters < 0 || segments < 0) return FP8G_ERR_SHAPE;
     if (rank % 8 != 0 || rank > 256 || k % 8 != 0 || tokens >= LIM28 || n >= LIM28 || k >= LIM28 ||
         adapters >= LIM28 || segments > ((int64_t)1 << 20))
         return FP8G_ERR_UNSUPPORTED;
-    return FP8G_OK;
+    return fp8g::lora_add_fits(lora_sizes(tokens, n, k, rank, adapters, segments)) ? FP8G_OK : FP8G_ERR_UNSUPPORTED;
 }
 
 bool dims_ok(int64_t dk, int64_t dv) {
     return (dk == 64 && dv == 64) || (dk == 128 && dv == 128) || (dk == 192 && dv == 128);
+}
+
+bool rows_fit(int64_t tokens, int64_t heads, int64_t dk, int64_t dv) {
+    fp8g::Kv4RowsArgs a = {};
+    a.side[0].dim = (int32_t)dk, a.side[1].dim = (int32_t)dv;
+    a.tokens = (int32_t)tokens, a.heads = (int32_t)heads, a.page_size = 16;
+    return fp8g::kv4_rows_fit(a);
 }
 
 // The cache's arrays, as ranges; a status below 0: go on.
@@ -80,6 +94,18 @@ int check_cache(const void* kc, const void* ks, const void* vc, const void* vs, 
     return -1;
 }
 
+// a window that reaches behind every key is none
+int32_t window_of(int64_t window) { return (int32_t)(window < LIM28 * 4 ? window : 0); }
+
+fp8g::Kv4AttnArgs attn_sizes(int64_t queries, int64_t q_heads, int64_t kv_heads, int64_t dk, int64_t dv, int64_t batch,
+                             int64_t max_pages, int64_t page_size, int64_t window) {
+    fp8g::Kv4AttnArgs a = {};
+    a.queries = (int32_t)queries, a.q_heads = (int32_t)q_heads, a.kv_heads = (int32_t)kv_heads;
+    a.dk = (int32_t)dk, a.dv = (int32_t)dv, a.batch = (int32_t)batch, a.max_pages = (int32_t)max_pages;
+    a.page_size = (int32_t)page_size, a.window = window_of(window);
+    return a;
+}
+
 int check_attn_sizes(int64_t queries, int64_t q_heads, int64_t kv_heads, int64_t dk, int64_t dv, int64_t batch,
                      int64_t max_pages, int64_t page_size, int64_t window) {
     if (queries < 0 || q_heads < 0 || kv_heads < 0 || dk < 0 || dv < 0 || batch < 0 || max_pages < 0 ||
@@ -92,7 +118,8 @@ int check_attn_sizes(int64_t queries, int64_t q_heads, int64_t kv_heads, int64_t
     if (keys < 0 || keys > ((int64_t)1 << 30) || page_size > ((int64_t)1 << 30) || rows < 0 || rows >= LIM31 ||
         queries >= LIM31 || blocks < 0 || blocks >= LIM28)
         return FP8G_ERR_UNSUPPORTED;
-    return FP8G_OK;
+    return fp8g::kv4_attention_fits(attn_sizes(queries, q_heads, kv_heads, dk, dv, batch, max_pages, page_size, window))
+               ? FP8G_OK : FP8G_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -101,10 +128,7 @@ extern "C" {
 
 int64_t lora_add_workspace(int64_t tokens, int64_t n, int64_t k, int64_t rank, int64_t adapters, int64_t segments) {
     if (check_lora_sizes(tokens, n, k, rank, adapters, segments) != FP8G_OK) return -1;
-    fp8g::LoraArgs a = {};
-    a.tokens = (int32_t)tokens, a.n = (int32_t)n, a.k = (int32_t)k, a.rank = (int32_t)rank;
-    a.adapters = (int32_t)adapters, a.segments = (int32_t)segments;
-    return fp8g::lora_add_bytes(a);
+    return fp8g::lora_add_bytes(lora_sizes(tokens, n, k, rank, adapters, segments));
 }
 
 int lora_add(const void* base, const void* x, const void* A, const void* B, const float* scale,
@@ -158,6 +182,10 @@ int qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_strid
     if ((q_heads > 0 && (q_stride < q_row || q_out_stride < q_row)) ||
         (k_heads > 0 && (k_stride < k_row || k_out_stride < k_row)) || (axes > 1 && !axis))
         return FP8G_ERR_SHAPE;
+    fp8g::QkArgs sizes = {};
+    sizes.tokens = (int32_t)tokens, sizes.q_heads = (int32_t)q_heads, sizes.k_heads = (int32_t)k_heads;
+    sizes.head_dim = (int32_t)head_dim;
+    if (!fp8g::qk_norm_rope_fits(sizes, dtype == FP8G_OUT_F32)) return FP8G_ERR_UNSUPPORTED;
     if ((q_heads > 0 && (q_stride % to || q_out_stride % to)) || (k_heads > 0 && (k_stride % to || k_out_stride % to)))
         return FP8G_ERR_UNSUPPORTED;
     if ((q_heads > 0 && (mul3(tokens, q_stride, esz) < 0 || mul3(tokens, q_out_stride, esz) < 0)) ||
@@ -194,6 +222,7 @@ int kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
     if (!dims_ok(dk, dv) || page_size % 16 != 0 || page_size > ((int64_t)1 << 30) || heads > 65536 || tokens >= LIM31)
         return FP8G_ERR_UNSUPPORTED;
     if (tokens == 0 || heads == 0) return FP8G_OK;
+    if (!rows_fit(tokens, heads, dk, dv)) return FP8G_ERR_UNSUPPORTED;
     const int64_t esz = in_dtype == FP8G_IN_BF16 ? 2 : 4, to = 16 / esz;
     if (k_stride < heads * dk || v_stride < heads * dv) return FP8G_ERR_SHAPE;
     if (k_stride % to || v_stride % to || mul3(tokens, k_stride, esz) < 0 || mul3(tokens, v_stride, esz) < 0)
@@ -229,6 +258,7 @@ int kv4_gather(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v
     if (!dims_ok(dk, dv) || page_size % 16 != 0 || page_size > ((int64_t)1 << 30) || heads > 65536 || tokens >= LIM31)
         return FP8G_ERR_UNSUPPORTED;
     if (tokens == 0 || heads == 0) return FP8G_OK;
+    if (!rows_fit(tokens, heads, dk, dv)) return FP8G_ERR_UNSUPPORTED;
     const int64_t esz = out_dtype == FP8G_OUT_F32 ? 4 : 2;
     const int64_t kb = mul3(tokens, heads, dk * esz), vb = mul3(tokens, heads, dv * esz);
     if (kb < 0 || vb < 0) return FP8G_ERR_UNSUPPORTED;
@@ -253,11 +283,7 @@ int kv4_gather(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v
 int64_t kv4_attention_workspace(int64_t queries, int64_t q_heads, int64_t kv_heads, int64_t dk, int64_t dv,
                                 int64_t batch, int64_t max_pages, int64_t page_size, int64_t window) {
     if (check_attn_sizes(queries, q_heads, kv_heads, dk, dv, batch, max_pages, page_size, window) != FP8G_OK) return -1;
-    fp8g::Kv4AttnArgs a = {};
-    a.queries = (int32_t)queries, a.q_heads = (int32_t)q_heads, a.kv_heads = (int32_t)kv_heads;
-    a.dk = (int32_t)dk, a.dv = (int32_t)dv, a.batch = (int32_t)batch, a.max_pages = (int32_t)max_pages;
-    a.page_size = (int32_t)page_size, a.window = (int32_t)(window < LIM28 * 4 ? window : 0);
-    return fp8g::kv4_attention_bytes(a);
+    return fp8g::kv4_attention_bytes(attn_sizes(queries, q_heads, kv_heads, dk, dv, batch, max_pages, page_size, window));
 }
 
 int kv4_attention(const void* q, int64_t q_stride, int64_t queries, int64_t q_heads, const uint8_t* k_codes,
@@ -279,12 +305,11 @@ int kv4_attention(const void* q, int64_t q_stride, int64_t queries, int64_t q_he
     Cache c;
     st = check_cache(k_codes, k_scales, v_codes, v_scales, pages, page_size, kv_heads, dk, dv, c);
     if (st >= 0) return st;
-    // a window that reaches behind every key is none
     const fp8g::Kv4AttnArgs a = {q, k_codes, k_scales, v_codes, v_scales, page_table, q_start, kv_len, out, lse,
                                  static_cast<float*>(workspace), q_stride, (int32_t)queries, (int32_t)q_heads,
                                  (int32_t)kv_heads, (int32_t)dk, (int32_t)dv, (int32_t)pages, (int32_t)page_size,
                                  (int32_t)batch, (int32_t)max_pages, causal != 0,
-                                 (int32_t)(window < LIM28 * 4 ? window : 0), scale};
+                                 window_of(window), scale};
     const int64_t need = fp8g::kv4_attention_bytes(a);
     if (workspace_bytes < need) return FP8G_ERR_UNSUPPORTED;
     if (need > 0 && !workspace) return FP8G_ERR_NULL;

@@ -1033,7 +1033,7 @@ static AttnPlan attn_plan(const Kv4AttnArgs& a) {
     constexpr int64_t full = 512, longest_splits = 16, room = 64 << 20;
     const int64_t steps = (keys + ATTN_CHUNK - 1) / ATTN_CHUNK;
     int64_t fill = blocks >= full ? 1 : full / blocks;
-    const int64_t most = ((int64_t)1 << 30) / ((int64_t)p.ids * a.kv_heads);   // keeps the grid's size an int
+    const int64_t most = most_blocks(wide ? 64 * ATTN_WIDE_WAVES : ATTN_THREADS) / ((int64_t)p.ids * a.kv_heads);
     if (fill > most) fill = most < 1 ? 1 : most;
     if (steps > 0) {
         const int64_t each = (steps + fill - 1) / fill;
@@ -1052,6 +1052,11 @@ static AttnPlan attn_plan(const Kv4AttnArgs& a) {
     p.by_fill = fast_div((uint32_t)fill);
     p.by_splits = fast_div((uint32_t)splits);
     return p;
+}
+
+bool kv4_attention_fits(const Kv4AttnArgs& a) {
+    if (a.queries == 0 || a.batch == 0 || a.q_heads == 0) return true;
+    return (int64_t)attn_plan(a).ids * a.kv_heads <= most_blocks(attn_wide(a) ? 64 * ATTN_WIDE_WAVES : ATTN_THREADS);
 }
 
 int64_t kv4_attention_bytes(const Kv4AttnArgs& a) {

@@ -203,7 +203,7 @@ __global__ __launch_bounds__(KV_THREADS) void kv4_gather_kernel(Kv4RowsArgs a, R
 
 // Few tokens: one a tile.  Many: 16, cut into parts of two full batches of every
 // thread or so.
-static RowsPlan rows_plan(const Kv4RowsArgs& a, unsigned* blocks) {
+static RowsPlan rows_plan(const Kv4RowsArgs& a, int64_t* blocks) {
     RowsPlan p;
     p.tokens_log2 = a.tokens >= 1024 ? 4 : 0;
     p.k_all = (a.heads * (a.side[0].dim >> 3)) << p.tokens_log2;
@@ -217,27 +217,33 @@ static RowsPlan rows_plan(const Kv4RowsArgs& a, unsigned* blocks) {
     p.v_chunks = fast_div(a.side[1].dim >> 3);
     p.page = fast_div(a.page_size);
     p.wide = a.slot_end > ((int64_t)1 << 31);
-    *blocks = (unsigned)((((int64_t)a.tokens - 1) >> p.tokens_log2) + 1) * p.parts;
+    *blocks = ((((int64_t)a.tokens - 1) >> p.tokens_log2) + 1) * p.parts;
     return p;
 }
 
+bool kv4_rows_fit(const Kv4RowsArgs& a) {
+    int64_t blocks;
+    rows_plan(a, &blocks);
+    return blocks <= most_blocks(KV_THREADS);
+}
+
 hipError_t launch_kv4_append(const Kv4RowsArgs& a, int bf16, hipStream_t stream) {
-    unsigned blocks;
+    int64_t blocks;
     const RowsPlan p = rows_plan(a, &blocks);
     if (bf16)
-        kv4_append_kernel<true><<<dim3(blocks), dim3(KV_THREADS), 0, stream>>>(a, p);
+        kv4_append_kernel<true><<<dim3((unsigned)blocks), dim3(KV_THREADS), 0, stream>>>(a, p);
     else
-        kv4_append_kernel<false><<<dim3(blocks), dim3(KV_THREADS), 0, stream>>>(a, p);
+        kv4_append_kernel<false><<<dim3((unsigned)blocks), dim3(KV_THREADS), 0, stream>>>(a, p);
     return hipGetLastError();
 }
 
 hipError_t launch_kv4_gather(const Kv4RowsArgs& a, int f32, hipStream_t stream) {
-    unsigned blocks;
+    int64_t blocks;
     const RowsPlan p = rows_plan(a, &blocks);
     if (f32)
-        kv4_gather_kernel<true><<<dim3(blocks), dim3(KV_THREADS), 0, stream>>>(a, p);
+        kv4_gather_kernel<true><<<dim3((unsigned)blocks), dim3(KV_THREADS), 0, stream>>>(a, p);
     else
-        kv4_gather_kernel<false><<<dim3(blocks), dim3(KV_THREADS), 0, stream>>>(a, p);
+        kv4_gather_kernel<false><<<dim3((unsigned)blocks), dim3(KV_THREADS), 0, stream>>>(a, p);
     return hipGetLastError();
 }
 

@@ -7,6 +7,11 @@
 
 namespace fp8g {
 
+// A launch has fewer than 2^32 threads along a dimension; the runtime refuses
+// others.  <operator>_fits: whether the launches of these sizes are so (pointers
+// unread), asked before anything is queued.
+inline int64_t most_blocks(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
+
 struct QkArgs {
     const void *q, *k;
     void *q_out, *k_out;
@@ -16,6 +21,7 @@ struct QkArgs {
     int32_t tokens, q_heads, k_heads, head_dim, rotary_dim, axes, max_position, interleaved;
     float eps;
 };
+bool qk_norm_rope_fits(const QkArgs& a, int f32);
 hipError_t launch_qk_norm_rope(const QkArgs& a, int f32, hipStream_t stream);
 
 // One side (keys or values) of the MXFP4 cache.
@@ -33,6 +39,7 @@ struct Kv4RowsArgs {
     int64_t slot_end;         // pages * page_size
     int32_t tokens, heads, page_size;
 };
+bool kv4_rows_fit(const Kv4RowsArgs& a);
 hipError_t launch_kv4_append(const Kv4RowsArgs& a, int bf16, hipStream_t stream);
 hipError_t launch_kv4_gather(const Kv4RowsArgs& a, int f32, hipStream_t stream);
 
@@ -48,6 +55,7 @@ struct Kv4AttnArgs {
 };
 // bytes of workspace for these sizes (pointers and lengths on the device unread)
 int64_t kv4_attention_bytes(const Kv4AttnArgs& a);
+bool kv4_attention_fits(const Kv4AttnArgs& a);
 hipError_t launch_kv4_attention(const Kv4AttnArgs& a, hipStream_t stream);
 
 struct LoraArgs {
@@ -59,6 +67,7 @@ struct LoraArgs {
     int32_t tokens, n, k, rank, adapters, segments;
 };
 int64_t lora_add_bytes(const LoraArgs& a);
+bool lora_add_fits(const LoraArgs& a);
 hipError_t launch_lora_add(const LoraArgs& a, int f32, hipStream_t stream);
 
 }  // namespace fp8g

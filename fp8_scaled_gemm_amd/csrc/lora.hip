@@ -602,6 +602,8 @@ static LoraPlan lora_plan(const LoraArgs& a) {
     int most = (a.k + 255) / 256;
     most = most > max_splits ? max_splits : most;
     splits = splits > most ? most : splits;
+    const int64_t room = most_blocks(LORA_THREADS) / (((int64_t)lora_ids(a, p.tiles) + 7) / 8 * 8 * p.rank_blocks);
+    splits = splits > room ? (int)room : splits;
     splits = splits < 1 ? 1 : splits;             // k may be 0
     p.k_split = ((a.k + splits - 1) / splits + 127) / 128 * 128;
     p.splits = a.k > 0 ? (a.k + p.k_split - 1) / p.k_split : 0;
@@ -613,9 +615,15 @@ int64_t lora_add_bytes(const LoraArgs& a) {
     return (int64_t)lora_plan(a).splits * a.tokens * a.rank * 4;
 }
 
+bool lora_add_fits(const LoraArgs& a) {
+    if (a.tokens == 0 || a.n == 0) return true;
+    const int tiles = lora_wide(a) ? 4 : 1;
+    return ((int64_t)lora_ids(a, tiles) + 7) / 8 * 8 * lora_plan(a).rank_blocks <= most_blocks(LORA_THREADS);
+}
+
 template <int RT>
 static hipError_t shrink(const LoraArgs& a, const LoraPlan& p, hipStream_t stream) {
-    const dim3 grid((unsigned)((lora_ids(a, p.tiles) + 7) / 8 * 8 * p.splits * p.rank_blocks)), block(LORA_THREADS);
+    const dim3 grid((unsigned)(((int64_t)lora_ids(a, p.tiles) + 7) / 8 * 8 * p.splits * p.rank_blocks)), block(LORA_THREADS);
     if (p.tiles == 1) {
         lora_shrink_kernel<RT><<<grid, block, 0, stream>>>(a, p.splits, p.k_split, p.rank_blocks);
     } else {
@@ -636,17 +644,19 @@ static hipError_t expand(const LoraArgs& a, const LoraPlan& p, hipStream_t strea
     if (col_blocks < 1) col_blocks = 1;
     const int most = (a.n + unit - 1) / unit;
     col_blocks = col_blocks > most ? most : col_blocks;
+    const int ids = lora_ids(a, tiles);
+    const int64_t room = most_blocks(LORA_THREADS) / (((int64_t)ids + 7) / 8 * 8);      // more segments than tokens
+    col_blocks = col_blocks > room ? (int)room : col_blocks;
     const int cols = ((a.n + col_blocks - 1) / col_blocks + unit - 1) / unit * unit;
     col_blocks = (a.n + cols - 1) / cols;
-    const int ids = lora_ids(a, tiles);
     const dim3 block(LORA_THREADS);
     const int pieces = F32 ? 3 : 2;
     if (wide) {
         const unsigned lds = 64 * (pieces * ((a.rank + 63) / 64 * 64) + 8) * 2;
-        lora_expand_wide_kernel<F32><<<dim3((unsigned)((ids + 7) / 8 * 8 * col_blocks)), block, lds, stream>>>(a, p.splits, col_blocks, cols);
+        lora_expand_wide_kernel<F32><<<dim3((unsigned)(((int64_t)ids + 7) / 8 * 8 * col_blocks)), block, lds, stream>>>(a, p.splits, col_blocks, cols);
     } else {
         const unsigned lds = 16 * ((pieces * a.rank + 31) / 32 * 32 + 8) * 2;
-        lora_expand_kernel<F32><<<dim3((unsigned)(ids * col_blocks)), block, lds, stream>>>(a, p.splits, col_blocks, cols);
+        lora_expand_kernel<F32><<<dim3((unsigned)((int64_t)ids * col_blocks)), block, lds, stream>>>(a, p.splits, col_blocks, cols);
     }
     return hipGetLastError();
 }

@@ -182,9 +182,14 @@ __global__ __launch_bounds__(QK_THREADS) void qk_norm_rope_kernel(QkArgs a, QkPl
     }
 }
 
-template <bool F32, int L>
-static hipError_t launch_l(const QkArgs& a, hipStream_t stream) {
-    constexpr int SLOTS = QK_THREADS / L;
+// lanes of a row: a power of two, 16 bytes a lane
+static int qk_lanes(const QkArgs& a, int f32) {
+    const int bytes = a.head_dim * (f32 ? 4 : 2);
+    return bytes <= 128 ? 8 : bytes <= 256 ? 16 : bytes <= 512 ? 32 : 64;
+}
+
+static QkPlan qk_plan(const QkArgs& a, int lanes, int64_t* blocks) {
+    const int SLOTS = QK_THREADS / lanes;
     const int rows = a.q_heads + a.k_heads;
     QkPlan p;
     p.part = rows, p.row_blocks = 1;
@@ -202,7 +207,20 @@ static hipError_t launch_l(const QkArgs& a, hipStream_t stream) {
     }
     const int most = QK_LDS / (a.head_dim * 16);
     if (p.tokens > most) p.tokens = most;
-    const int64_t grid = ((int64_t)a.tokens + p.tokens - 1) / p.tokens * p.row_blocks;
+    *blocks = ((int64_t)a.tokens + p.tokens - 1) / p.tokens * p.row_blocks;
+    return p;
+}
+
+bool qk_norm_rope_fits(const QkArgs& a, int f32) {
+    int64_t blocks;
+    qk_plan(a, qk_lanes(a, f32), &blocks);
+    return blocks <= most_blocks(QK_THREADS);
+}
+
+template <bool F32, int L>
+static hipError_t launch_l(const QkArgs& a, hipStream_t stream) {
+    int64_t grid;
+    const QkPlan p = qk_plan(a, L, &grid);
     const unsigned lds = p.tokens * a.head_dim * 16;
     if (a.interleaved)
         qk_norm_rope_kernel<F32, L, true><<<dim3((unsigned)grid), dim3(QK_THREADS), lds, stream>>>(a, p);
@@ -212,15 +230,15 @@ static hipError_t launch_l(const QkArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_qk_norm_rope(const QkArgs& a, int f32, hipStream_t stream) {
-    const int bytes = a.head_dim * (f32 ? 4 : 2);
+    const int lanes = qk_lanes(a, f32);
     if (f32) {
-        if (bytes <= 128) return launch_l<true, 8>(a, stream);
-        if (bytes <= 256) return launch_l<true, 16>(a, stream);
-        if (bytes <= 512) return launch_l<true, 32>(a, stream);
+        if (lanes == 8) return launch_l<true, 8>(a, stream);
+        if (lanes == 16) return launch_l<true, 16>(a, stream);
+        if (lanes == 32) return launch_l<true, 32>(a, stream);
         return launch_l<true, 64>(a, stream);
     }
-    if (bytes <= 128) return launch_l<false, 8>(a, stream);
-    if (bytes <= 256) return launch_l<false, 16>(a, stream);
+    if (lanes == 8) return launch_l<false, 8>(a, stream);
+    if (lanes == 16) return launch_l<false, 16>(a, stream);
     return launch_l<false, 32>(a, stream);
 }
 

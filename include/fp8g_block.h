@@ -20,6 +20,9 @@
  * Index and statistics arrays (int32, int64, and the fp32 arrays scale, weight,
  * cos_sin, lse) need the alignment of their element only; all others 16 bytes.
  *
+ * A launch has fewer than 2^32 threads.  Sizes that would need more
+ * (hundreds of millions of rows) are ERR_UNSUPPORTED, too.
+ *
  * Workspaces belong to the caller: <call>_workspace gives the bytes that the
  * same sizes need (0: none; the pointer may then be NULL).  Contents are
  * undefined before and after the call; calls that may overlap need their own.
