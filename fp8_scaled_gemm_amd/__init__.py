@@ -29,6 +29,7 @@ The attention block's operators (``include/fp8g_block.h``, module ``block``):
     kv4_cache(pages, heads, page_size, dk, dv)                         -> KV4Cache
     kv4_append(cache, k, v, slots), kv4_gather(cache, slots)           -> (k, v)
     kv4_attention(q, cache, page_table, q_start, kv_len)               -> out
+    lora_add_workspace(...), kv4_attention_workspace(...)              -> bytes
 
 E4M3 tensors are ``torch.float8_e4m3fn`` (OCP, the gfx950 format) and E5M2
 tensors ``torch.float8_e5m2``, or either as raw ``torch.uint8`` codes; the
@@ -43,7 +44,8 @@ __all__ = ["load", "fp8_quantize_rowwise", "fp8_quantize_ex", "mxfp8_quantize", 
            "fp8_gemm_scaled_noalloc", "mxfp8_gemm",
            "fp8_gemm_scaled_ex", "mxfp8_gemm_ex", "concat_mla_k", "fp8g_roof_mfma", "fp8g_roof_stream",
            "status_string",
-           "lora_add", "qk_norm_rope", "KV4Cache", "kv4_cache", "kv4_append", "kv4_gather", "kv4_attention",
+           "lora_add", "lora_add_workspace", "qk_norm_rope", "KV4Cache", "kv4_cache", "kv4_append", "kv4_gather",
+           "kv4_attention", "kv4_attention_workspace",
            "Fp8gError", "LIB_PATH", "HEADER_PATH", "OUT_BF16", "OUT_F32", "FMT_E4M3", "FMT_E5M2"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -419,5 +421,5 @@ def fp8g_roof_stream(src, dst, write_ratio, nontemporal_stores=0):
     return dst
 
 
-from .block import (KV4Cache, kv4_append, kv4_attention, kv4_cache, kv4_gather, lora_add,  # noqa: E402
-                    qk_norm_rope)
+from .block import (KV4Cache, kv4_append, kv4_attention, kv4_attention_workspace, kv4_cache,  # noqa: E402
+                    kv4_gather, lora_add, lora_add_workspace, qk_norm_rope)

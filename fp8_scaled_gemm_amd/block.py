@@ -11,9 +11,12 @@ import collections
 
 import torch
 
-from . import _check, load
+from . import Fp8gError, _check, load
 
-__all__ = ["lora_add", "qk_norm_rope", "KV4Cache", "kv4_cache", "kv4_append", "kv4_gather", "kv4_attention"]
+__all__ = ["lora_add", "lora_add_workspace", "qk_norm_rope", "KV4Cache", "kv4_cache", "kv4_append", "kv4_gather",
+           "kv4_attention", "kv4_attention_workspace"]
+
+_UNSUPPORTED = 6      # FP8G_ERR_UNSUPPORTED
 
 _native = None
 
@@ -36,6 +39,18 @@ def _done(result, where):
     if type(result) is int:
         _check(result, where)
     return result
+
+
+def _bytes(need, where):
+    """A workspace's size, or the refusal of its sizes as an error."""
+    if need < 0:
+        raise Fp8gError(_UNSUPPORTED, where)
+    return need
+
+
+def lora_add_workspace(tokens, n, k, rank, adapters, segments):
+    """Bytes of workspace that lora_add needs for these sizes (0: none)."""
+    return _bytes(load().lora_add_workspace(tokens, n, k, rank, adapters, segments), "lora_add_workspace")
 
 
 def lora_add(base, x, A, B, scale, seg_start, seg_adapter, out=None, workspace=None):
@@ -97,6 +112,13 @@ def kv4_gather(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16):
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("dtype must be bfloat16 or float32, got %s" % dtype)
     return _done(_block().kv4_gather(*cache, slots, k_out, v_out, dtype is torch.float32), "kv4_gather")
+
+
+def kv4_attention_workspace(queries, q_heads, kv_heads, dk, dv, batch, max_pages, page_size, window=0):
+    """Bytes of workspace that kv4_attention needs for these sizes (0: none; at
+    most 69 MB, whatever max_pages is)."""
+    return _bytes(load().kv4_attention_workspace(queries, q_heads, kv_heads, dk, dv, batch, max_pages, page_size, window),
+                  "kv4_attention_workspace")
 
 
 def kv4_attention(q, cache, page_table, q_start, kv_len, scale=None, causal=True, window=0, out=None, lse=None,

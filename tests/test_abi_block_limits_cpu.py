@@ -55,3 +55,15 @@ def test_launches_of_2_to_the_32_threads_are_refused(lib):
     assert lib.lora_add_workspace((1 << 28) - 1, 8, 8, 256, 1, 1) == -1
     assert lib.lora_add(p[0], p[1], p[2], p[3], p[4], p[5], p[6], (1 << 28) - 1, 8, 8, 256, 1, 1, 0, p[7], p[8], 1 << 50,
                         None) == UNSUPPORTED
+
+
+def test_workspace_sizes_from_python(lib):
+    assert fp8g.lora_add_workspace(8, 64, 64, 16, 2, 3) == lib.lora_add_workspace(8, 64, 64, 16, 2, 3) > 0
+    assert fp8g.lora_add_workspace(0, 64, 64, 16, 2, 3) == 0
+    assert fp8g.kv4_attention_workspace(4, 8, 2, 128, 128, 3, 40, 16) == \
+        lib.kv4_attention_workspace(4, 8, 2, 128, 128, 3, 40, 16, 0) > 0
+    for refused in (lambda: fp8g.lora_add_workspace(8, 64, 64, 12, 2, 3),
+                    lambda: fp8g.kv4_attention_workspace(4, 8, 3, 128, 128, 3, 40, 16)):
+        with pytest.raises(fp8g.Fp8gError) as e:
+            refused()
+        assert e.value.status == UNSUPPORTED

@@ -4,6 +4,8 @@ import numpy as np
 import pytest
 import torch
 
+import test_gpu_block_attention as attention
+import test_gpu_block_rows as rows
 from block_util import rng
 from gpu_util import say
 
@@ -26,3 +28,38 @@ def test_many_more_segments_than_tokens(gpu_lib):
     # as in test_gpu_block_rows.py
     tol = 2.0 ** -24 * want.abs() * 1.01 + 2.0 ** -22 * low + (k + 3 * rank + 8) * 2.0 ** -24 * full + 2.0 ** -23 * base.abs()
     assert ((got.double() - want).abs() <= tol).all()
+
+
+def guarded(need):
+    """A workspace of exactly `need` bytes inside a larger allocation, and a check that the rest is untouched."""
+    room = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+
+    def check():
+        assert (room[:4096] == 0xA5).all() and (room[4096 + need:] == 0xA5).all()
+    return room[4096:4096 + need], check
+
+
+@pytest.mark.parametrize("T,rank", [(40, 16), (600, 64)])
+def test_own_workspace_of_the_adapters(gpu_lib, T, rank):
+    ref, args = rows.lora_case(11, T, 200, 520, rank, 3, [0, 20, T], [2, 1], torch.bfloat16)
+    workspace, check = guarded(gpu_lib.lora_add_workspace(T, 200, 520, rank, 3, 2))
+    got = gpu_lib.lora_add(*args, workspace=workspace)
+    check()
+    rows.lora_check(got, ref, 520, rank, torch.bfloat16)
+    assert torch.equal(got, gpu_lib.lora_add(*args))
+    with pytest.raises(gpu_lib.Fp8gError):
+        gpu_lib.lora_add(*args, workspace=workspace[:-1])
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1, 1], [900, 5, 2000]), ([100, 37], [500, 1200])])
+def test_own_workspace_of_attention(gpu_lib, q_lens, kv_lens):
+    args = attention._setup(gpu_lib, q_lens, kv_lens)
+    need = gpu_lib.kv4_attention_workspace(sum(q_lens), 8, 2, 128, 128, len(kv_lens), args[2].shape[1], 16)
+    assert need > 0
+    workspace, check = guarded(need)
+    out, lse = gpu_lib.kv4_attention(*args, return_lse=True, workspace=workspace)
+    check()
+    want, want_lse = gpu_lib.kv4_attention(*args, return_lse=True)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    with pytest.raises(gpu_lib.Fp8gError):
+        gpu_lib.kv4_attention(*args, workspace=workspace[:-1])
