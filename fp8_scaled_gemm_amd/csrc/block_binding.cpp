@@ -84,7 +84,11 @@ float real(PyObject* o) {
     if (v == -1.0 && PyErr_Occurred()) throw TypeErr("a number is required");
     return (float)v;
 }
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw TypeErr("a truth value is required");     // the object's own error stays set
+    return v == 1;
+}
 
 struct Call {
     int device;

@@ -63,3 +63,24 @@ def test_own_workspace_of_attention(gpu_lib, q_lens, kv_lens):
     assert torch.equal(out, want) and torch.equal(lse, want_lse)
     with pytest.raises(gpu_lib.Fp8gError):
         gpu_lib.kv4_attention(*args, workspace=workspace[:-1])
+
+
+class NoTruth:
+    def __bool__(self):
+        raise ZeroDivisionError
+
+
+def test_flags_without_a_truth_value(gpu_lib):
+    """An argument's own error comes back, and nothing has been written."""
+    args = attention._setup(gpu_lib, [1, 2], [40, 30])
+    out = torch.full((3, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    for flag in ("causal", "return_lse"):
+        with pytest.raises(ZeroDivisionError):
+            gpu_lib.kv4_attention(*args, out=out, **{flag: NoTruth()})
+    q = torch.ones(3, 2, 64, device="cuda")
+    q_out = torch.full_like(q, 7.0)
+    with pytest.raises(ZeroDivisionError):
+        gpu_lib.qk_norm_rope(q, q, None, None, torch.zeros(3, dtype=torch.int32, device="cuda"),
+                             torch.zeros(4, 64, device="cuda"), interleaved=NoTruth(), q_out=q_out)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and (q_out == 7.0).all()
