@@ -84,3 +84,25 @@ def test_flags_without_a_truth_value(gpu_lib):
                              torch.zeros(4, 64, device="cuda"), interleaved=NoTruth(), q_out=q_out)
     torch.cuda.synchronize()
     assert (out == 7.0).all() and (q_out == 7.0).all()
+
+
+def test_host_tensors_are_refused(gpu_lib):
+    """Every tensor of every operator, one at a time."""
+    _, lora = rows.lora_case(7, 8, 64, 64, 16, 2, [0, 8], [1], torch.bfloat16)
+    cache = gpu_lib.kv4_cache(4, 2, 16, 128, 128)
+    row = torch.zeros(3, 2, 128, device="cuda", dtype=torch.bfloat16)
+    slots = torch.arange(3, device="cuda")
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")   # noqa: E731
+    weight, angle = torch.ones(128, device="cuda"), torch.zeros(4, 128, device="cuda")
+    calls = [(gpu_lib.lora_add, lora),
+             (gpu_lib.qk_norm_rope, [row, row, weight, weight, ints(0, 1, 2), angle]),
+             (lambda *a: gpu_lib.kv4_append(gpu_lib.KV4Cache(*a[:4]), *a[4:]), [*cache, row, row, slots]),
+             (lambda *a: gpu_lib.kv4_gather(gpu_lib.KV4Cache(*a[:4]), *a[4:]), [*cache, slots]),
+             (lambda *a: gpu_lib.kv4_attention(a[0], gpu_lib.KV4Cache(*a[1:5]), *a[5:]),
+              [row, *cache, torch.zeros(1, 2, dtype=torch.int32, device="cuda"), ints(0, 3), ints(5)])]
+    for call, args in calls:
+        call(*args)
+        for i, arg in enumerate(args):
+            with pytest.raises(ValueError):
+                call(*args[:i], arg.cpu(), *args[i + 1:])
+    torch.cuda.synchronize()
