@@ -533,15 +533,18 @@ __device__ __forceinline__ int lds_at(int m, int c) {
     return m * CHUNKS + (c ^ (((m >> 1) ^ ((m >> 4) & 1)) & 7));
 }
 
-template <int DK, int DV, int WAVES, bool SPLIT>
-__global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4AttnArgs a, AttnPlan p) {
-    constexpr int THREADS = 64 * WAVES, ROWS = 32 * WAVES, ROWS_LOG2 = WAVES == 8 ? 8 : 7;
+constexpr int WIDE_WAVES = 8, WIDE_THREADS = 64 * WIDE_WAVES;
+constexpr int WIDE_ROWS_LOG2 = 8, WIDE_ROWS = 1 << WIDE_ROWS_LOG2;
+
+template <int DK, int DV, bool SPLIT>
+__global__ __launch_bounds__(WIDE_THREADS, 2) void kv4_attention_wide_kernel(Kv4AttnArgs a, AttnPlan p) {
+    constexpr int THREADS = WIDE_THREADS;
     constexpr int KC = DK / 8, KK = DK / 16, DT = DV / 32;
     // keys: 8 bytes of codes (16 dims) a unit, 8 or 4 of them (a part of 128 or 64
     // dims) side by side; values: 4 dims of 4 keys a unit
     constexpr int KN = DK == 192 ? 2 : 1;
     constexpr int VU = ATTN_STEP / 4 * (DV / 4);
-    static_assert(WAVES == 8 && VU <= THREADS, "one unit of values a thread, and a wave's units in one run of 16 keys");
+    static_assert(VU <= THREADS && WIDE_ROWS == 32 * WIDE_WAVES, "one unit of values a thread, and a wave's units in one run of 16 keys");
     // the halves as arrays of their own, chosen at compile time: the compiler then
     // knows that writes to one do not meet reads of the other, and moves them
     __shared__ v4u s_k0[ATTN_STEP * KC], s_k1[ATTN_STEP * KC], s_v0[DV * 8], s_v1[DV * 8];
@@ -556,7 +559,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     const int blocks = p.ids * a.kv_heads, split = blockIdx.x / blocks, rest = blockIdx.x - split * blocks;
     const int h = rest % a.kv_heads, id = p.ids - 1 - rest / a.kv_heads;
     AttnBlock b;
-    if (!attn_block<ROWS_LOG2>(a, group, id, b)) return;
+    if (!attn_block<WIDE_ROWS_LOG2>(a, group, id, b)) return;
 
     const int first = b.kv - b.queries;
     auto top_of = [&](int q) { return a.causal ? max(0, min(b.kv, first + q + 1)) : b.kv; };
@@ -566,7 +569,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
     const int qi = min(row, b.rows - 1) / group, head = h * group + min(row, b.rows - 1) % group;
     const int hi = real ? top_of(qi) : 0, lo = low_of(qi);
     // keys that some row of the block sees, and that every row sees
-    const int q_first = b.row0 / group, q_last = (min(b.row0 + ROWS, b.rows) - 1) / group;
+    const int q_first = b.row0 / group, q_last = (min(b.row0 + WIDE_ROWS, b.rows) - 1) / group;
     const int all_lo = min(low_of(q_first), b.kv), all_hi = top_of(q_last);
     const int in_lo = low_of(q_last), in_hi = top_of(q_first);
     const AttnPart part = attn_part<SPLIT>(p, split, all_lo, all_hi);
@@ -805,7 +808,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void kv4_attention_wide_kernel(Kv4At
         const int j1 = min(in_hi, end) > begin ? (min(in_hi, end) - begin) / ATTN_STEP : 0;
         auto base_of = [&](int t) { return begin + t * ATTN_STEP; };
         auto edge = [&](int t) { return t < j0 || t >= j1; };
-        const int late = wave >= WAVES / 2;      // the waves one phase behind
+        const int late = wave >= WIDE_WAVES / 2;      // the waves one phase behind
         Keys keys;
         Values values;
         v16f acc[2];
@@ -999,7 +1002,6 @@ __global__ __launch_bounds__(ATTN_THREADS) void kv4_attention_join_kernel(Kv4Att
 // Many rows a sequence on average: blocks of 256 rows, not 16.  8 sequences of
 // 8192 keys, 8 key heads, us with 16 / 256 rows: 48 / 84 at 64 rows a key head,
 // 78 / 109 at 128, 121 / 112 at 160, 115 / 116 at 192.
-constexpr int ATTN_WIDE_WAVES = 8;
 static bool attn_wide(const Kv4AttnArgs& a) {
     return (int64_t)a.queries * (a.q_heads / a.kv_heads) >= 160 * (int64_t)a.batch;
 }
@@ -1008,7 +1010,7 @@ static AttnPlan attn_plan(const Kv4AttnArgs& a) {
     AttnPlan p;
     const int group = a.q_heads / a.kv_heads;
     const bool wide = attn_wide(a);
-    const int rows = wide ? 32 * ATTN_WIDE_WAVES : ATTN_ROWS;
+    const int rows = wide ? WIDE_ROWS : ATTN_ROWS;
     p.ids = (int)((int64_t)a.queries * group / rows) + a.batch;
     p.page = fast_div((uint32_t)a.page_size);
     int64_t keys = (int64_t)a.max_pages * a.page_size;
@@ -1033,7 +1035,7 @@ static AttnPlan attn_plan(const Kv4AttnArgs& a) {
     constexpr int64_t full = 512, longest_splits = 16, room = 64 << 20;
     const int64_t steps = (keys + ATTN_CHUNK - 1) / ATTN_CHUNK;
     int64_t fill = blocks >= full ? 1 : full / blocks;
-    const int64_t most = most_blocks(wide ? 64 * ATTN_WIDE_WAVES : ATTN_THREADS) / ((int64_t)p.ids * a.kv_heads);
+    const int64_t most = most_blocks(wide ? WIDE_THREADS : ATTN_THREADS) / ((int64_t)p.ids * a.kv_heads);
     if (fill > most) fill = most < 1 ? 1 : most;
     if (steps > 0) {
         const int64_t each = (steps + fill - 1) / fill;
@@ -1056,7 +1058,7 @@ static AttnPlan attn_plan(const Kv4AttnArgs& a) {
 
 bool kv4_attention_fits(const Kv4AttnArgs& a) {
     if (a.queries == 0 || a.batch == 0 || a.q_heads == 0) return true;
-    return (int64_t)attn_plan(a).ids * a.kv_heads <= most_blocks(attn_wide(a) ? 64 * ATTN_WIDE_WAVES : ATTN_THREADS);
+    return (int64_t)attn_plan(a).ids * a.kv_heads <= most_blocks(attn_wide(a) ? WIDE_THREADS : ATTN_THREADS);
 }
 
 int64_t kv4_attention_bytes(const Kv4AttnArgs& a) {
@@ -1069,7 +1071,7 @@ template <int DK, int DV, bool SPLIT>
 static hipError_t launch_rows(const Kv4AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)p.ids * a.kv_heads * p.splits));
     if (attn_wide(a))
-        kv4_attention_wide_kernel<DK, DV, ATTN_WIDE_WAVES, SPLIT><<<grid, dim3(64 * ATTN_WIDE_WAVES), 0, stream>>>(a, p);
+        kv4_attention_wide_kernel<DK, DV, SPLIT><<<grid, dim3(WIDE_THREADS), 0, stream>>>(a, p);
     else
         kv4_attention_kernel<DK, DV, SPLIT><<<grid, dim3(ATTN_THREADS), 0, stream>>>(a, p);
     return hipGetLastError();
