@@ -32,12 +32,16 @@
 //   its memory.  While a step is computed from LDS the next one's codes travel
 //   into the registers that it came from.
 // E2M1 with a power-of-two scale is exact in bf16, one convert instruction for
-// two elements; only the softmax weights are rounded (to bf16).
+// two elements; only the softmax weights are rounded (to bf16), as the second
+// product's operand: in two pieces they would double its matrix instructions.
+// Their sum takes them unrounded.  Error against 64 bits, of the size of the result:
+// 0.0019 to 0.0023, of which rounding the result to bf16 makes 0.0017.
 //
 // Measured: 64 sequences of 4165 to 16384 keys, 64 heads over 8 key heads, dims 128:
-// 159 us a call over many calls, 169 as the profiler's median of a dispatch: 4.2 to 4.5
-// TB/s of codes and scales (a 2 GB copy: 4.95).  The loads alone take 147 us, the
-// arithmetic alone 110.  One query of 32 heads on 2048 keys: 5.6 us and 3.2 to join.
+// 159 us a call over many calls, 164 as the profiler's median of a dispatch: 4.4 to 4.5
+// TB/s of codes and scales, where this part reads at up to 6.6.  These loads without the
+// arithmetic took 147 us, the arithmetic alone 110: one step of a wave is in flight.
+// One query of 32 heads on 2048 keys: 5.8 us and 3.0 to join.
 
 #include "device_common.h"
 #include "launch_block.h"
@@ -512,12 +516,12 @@ __global__ __launch_bounds__(ATTN_THREADS, 2) void kv4_attention_kernel(Kv4AttnA
 // barrier between the phases.  Between its matrix instructions a wave has time
 // for what is left: it turns codes of step t + 2 (keys) and t + 1 (values) into
 // the halves of the LDS that both groups have left, and asks for the next ones.
-// Measured: 9664 queries of 32 heads over 3 contexts of up to 8192 keys, dims 128:
-// 738 to 765 us a call over many calls, 805 as the profiler's median of a dispatch: 1.01
-// to 1.10 PFLOP/s (a bf16 library product of 8192 cubed: 1.24).  With the codes turned
+// Measured: 9663 queries of 32 heads over 3 contexts of up to 8192 keys, dims 128:
+// 735 to 776 us a call over many calls, 792 as the profiler's median of a dispatch: 1.02
+// to 1.10 PFLOP/s (a bf16 library product of 8192 cubed: up to 1.43).  With the codes turned
 // in the vector phase too, its 2350 clocks a step stood against 1260 of the matrix
 // phase, and moving them took 68 us of 806 away.  Now counters show the matrix core
-// busy in 51% of the clocks and the vector unit in about 61%.
+// busy in 54% of the clocks and the vector unit in about 65%.
 // The running maximum moves only when a row's maximum has grown by 2^8 or more:
 // weights up to 2^8 lose nothing in bf16 and float32, and the outputs are
 // rarely scaled.
@@ -999,9 +1003,18 @@ __global__ __launch_bounds__(ATTN_THREADS) void kv4_attention_join_kernel(Kv4Att
     if (a.lse && lane == 0) a.lse[row] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
-// Many rows a sequence on average: blocks of 256 rows, not 16.  8 sequences of
-// 8192 keys, 8 key heads, us with 16 / 256 rows: 48 / 84 at 64 rows a key head,
-// 78 / 109 at 128, 121 / 112 at 160, 115 / 116 at 192.
+// Many rows a sequence on average: blocks of 256 rows, not 16.  us with blocks of
+// 16 / 256, four heads a key head:
+//   rows a key head                       64       128       160       192       256       384       512
+//   8 x 8192 keys, 8 key heads, 128    48/ 79    74/105   117/109   113/116   132/149   192/159   251/197
+//   32 x 4096, 4, 128                  56/101    76/107   100/106   115/117   141/167   198/197   260/204
+//   8 x 8192, 16, 192/128              93/220   162/227   201/232   236/239   310/488   457/456   602/508
+//   8 x 8192, 8, 64                    43/ 69    73/ 97    73/ 98    73/100    94/135   134/140   175/179
+//   1 x 32768, 8, 128                  29/ 54    45/ 60    57/ 62    62/ 66    74/107   136/ 87   137/121
+//   3 x 2048, 8, 128                   15/ 19    19/ 24    20/ 27    22/ 28    22/ 42    32/ 44    32/ 46
+// At 160 to 192 rows the larger blocks are between 7% faster and 37% slower, at 256 (one
+// whole block a sequence) 13 to 90% slower, for a reason that was not found, and from
+// 384 on up to a third faster where keys are many.
 static bool attn_wide(const Kv4AttnArgs& a) {
     return (int64_t)a.queries * (a.q_heads / a.kv_heads) >= 160 * (int64_t)a.batch;
 }

@@ -22,9 +22,9 @@
 // for 64-byte and 45 for whole runs.  So shrink, and expand for long segments,
 // load whole 128-byte lines and turn them around in LDS.
 //
-// Measured: 8192 tokens, 7 segments, k 8192, n 2048, rank 64, bf16: shrink 33 us (x
-// read once: 4.0 TB/s), expand 26 us; 64 adapters of rank 16 for 64 tokens, k = n =
-// 4096: 5.1 and 6.5 us, of which reading A and B takes 3 at a large copy's rate.
+// Measured: 8192 tokens, 7 segments, k 8192, n 2048, rank 64, bf16: shrink 34 us (x
+// read once: 3.9 TB/s), expand 26 us; 64 adapters of rank 16 for 64 tokens, k = n =
+// 4096: 5.0 and 6.5 us, of which reading A and B takes 2.7 at a large copy's rate.
 
 #include "device_common.h"
 #include "launch_block.h"
@@ -167,9 +167,9 @@ __global__ __launch_bounds__(LORA_THREADS, 2) void lora_shrink_kernel(LoraArgs a
 // the adapter's tile of a unit of 64 k in LDS, so that it crosses the caches
 // once a block, and turn their own tokens' tiles around in LDS of their own.
 // DEPTH units are in flight in registers.  Blocks of 128 tokens, which read the
-// adapter half as often, came out even: shrink 38.5 instead of 44 us at 8192 x
-// 8192, rank 64, but the more slices of k that fill the chip again cost expand 3,
-// and 37 instead of 34 us in all at 4096 x 4096, rank 32, n 5120.
+// adapter half as often but need more slices of k to fill the chip, took 59 instead of
+// 62 us with expand at 8192 tokens, k 8192, rank 64, n 2048, and 37 instead of 34 at 4096
+// tokens, k 4096, rank 32, n 5120.
 template <int RT>
 __global__ __launch_bounds__(LORA_THREADS, 2) void lora_shrink_wide_kernel(LoraArgs a, int splits, int k_split, int rank_blocks) {
     constexpr int DEPTH = 4;

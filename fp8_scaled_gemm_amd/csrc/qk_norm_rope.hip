@@ -19,8 +19,8 @@
 // row come before its store in the same wave, and a wave holds whole rows, so
 // a row may be written in place.
 //
-// Measured: 8192 tokens x 72 heads x 128 bf16, three axes, 66 us, 4.7 TB/s (a 2 GB
-// copy on the same card: 4.95); 411 us before C and S lay in LDS and rows were in
+// Measured: 8192 tokens x 72 heads x 128 bf16, three axes, 67 us, 4.6 TB/s (copies on
+// this part reach 5.8); 411 us before C and S lay in LDS and rows were in
 // flight while others are worked out.
 
 #include "device_common.h"
