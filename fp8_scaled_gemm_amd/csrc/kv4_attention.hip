@@ -120,8 +120,11 @@ __device__ __forceinline__ AttnPart attn_part(const AttnPlan& p, int split, int 
     const int steps = (max(hi - from, 0) + ATTN_CHUNK - 1) / ATTN_CHUNK;
     int per = (int)divide(steps + p.fill - 1, p.by_fill);
     if (per > ATTN_LONGEST / ATTN_CHUNK) per = max(ATTN_LONGEST / ATTN_CHUNK, (int)divide(steps + p.splits - 1, p.by_splits));
-    const int64_t begin = from + (int64_t)split * per * ATTN_CHUNK;
-    return AttnPart{(int)min(begin, (int64_t)hi), (int)min(begin + per * ATTN_CHUNK, (int64_t)hi)};
+    // in steps, of which there are at most 2^22; known to be the workgroup's, or the
+    // 256-row kernel would keep them in vector registers, of which it has none left
+    const int first = (int)min((int64_t)split * per, (int64_t)steps), last = min(first + per, steps);
+    return AttnPart{__builtin_amdgcn_readfirstlane(from + first * ATTN_CHUNK),
+                    __builtin_amdgcn_readfirstlane(last < steps ? from + last * ATTN_CHUNK : hi)};
 }
 
 // A maximum of -inf alone does not say that a row has seen nothing: maxima drop
@@ -929,16 +932,21 @@ __global__ __launch_bounds__(WIDE_THREADS, 2) void kv4_attention_wide_kernel(Kv4
             part_ml[(target * p.splits + split) * 2 + 1] = l;
         }
     } else {
+        // A row without keys may hold NaN from values that others of its block see.
+        // A select for each value would spill 10 registers at dims 192, this 4.
         const bool none = saw_nothing(m, l);
-        const float inv = 1.0f / l;
-        auto result = [&](float x) { return none ? 0.0f : x * inv; };
+        const float inv = none ? 0.0f : 1.0f / l;
+        if (none) {
+#pragma unroll
+            for (int d = 0; d < DT; d++) o[d] = zero;
+        }
         uint16_t* dst = static_cast<uint16_t*>(a.out) + target * DV + 4 * e;
 #pragma unroll
         for (int d = 0; d < DT; d++)
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<v2u*>(dst + 32 * d + 2 * i) =
-                    v2u{bf16x2_bits(result(o[d][i]), result(o[d][i + 1])), bf16x2_bits(result(o[d][i + 2]), result(o[d][i + 3]))};
+                    v2u{bf16x2_bits(o[d][i] * inv, o[d][i + 1] * inv), bf16x2_bits(o[d][i + 2] * inv, o[d][i + 3] * inv)};
         if (a.lse && e == 0) a.lse[target] = none ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
     }
 }
