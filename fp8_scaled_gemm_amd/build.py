@@ -4,7 +4,7 @@
 
 Compiles every source under csrc/ to an object under _build/ (in parallel;
 the GEMM once per operand-format pair) and links them into one shared library
-next to this file; the binding of the attention block's operators (host code
+next to this file; the binding of the block's operators (host code
 against torch's headers) becomes _block.so beside it.  No fast-math: the quantizer relies on IEEE fp32 division.
 Packed-fp32 ops are disabled (-packed-fp32-ops); the host pass warns that it
 does not know the feature, which is harmless.
@@ -24,10 +24,12 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8g.so")
 SOURCES = ["abi.cpp", "quantize.hip", "mx_quantize.hip", "concat.hip", "roof.hip", "gemm.hip",
-           "abi_block.cpp", "lora.hip", "qk_norm_rope.hip", "kv4_cache.hip", "kv4_attention.hip"]
+           "abi_block.cpp", "lora.hip", "qk_norm_rope.hip", "kv4_cache.hip", "kv4_attention.hip",
+           "abi_ffn.cpp", "norm_quant.hip", "gemm_rows.hip", "moe_route.hip", "moe_combine.hip"]
 # gemm.hip is compiled once per operand-format pair (FP8G_GEMM_FMT = 2 * fmt_a + fmt_b)
 GEMM_PARTS = 4
 BINDING = os.path.join(HERE, "_block.so")
+BINDING_SOURCES = ["block_binding.cpp", "ffn_binding.cpp"]
 ARCH = "gfx950"
 FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -61,16 +63,17 @@ def _binding_cmds(cc):
     """Commands that compile the binding and link it to the library beside it."""
     import torch
     from torch.utils import cpp_extension
-    obj, tmp = os.path.join(OBJDIR, "block_binding.o"), BINDING + ".tmp"
+    tmp = BINDING + ".tmp"
+    objs = [os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o") for src in BINDING_SOURCES]
     include = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(ROCM, "include")] + cpp_extension.include_paths()
     compile_ = [cc, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
                 "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI]
     for path in include:
         compile_ += ["-isystem" if path != INCLUDE else "-I", path]
     torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    link = [cc, "-shared", "-fPIC", "-o", tmp, obj, LIB, "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-ltorch",
+    link = [cc, "-shared", "-fPIC", "-o", tmp] + objs + [LIB, "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-ltorch",
             "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"]
-    return compile_ + ["-c", os.path.join(CSRC, "block_binding.cpp"), "-o", obj], link, tmp
+    return [compile_ + ["-c", os.path.join(CSRC, src), "-o", obj] for src, obj in zip(BINDING_SOURCES, objs)], link, tmp
 
 
 def _run(cmd, verbose):
@@ -87,7 +90,7 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     cmds = [[cc] + FLAGS + extra + ["-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj]
             for src, extra, obj in units]
     binding, link_binding, binding_tmp = _binding_cmds(cc)
-    cmds.append(binding)
+    cmds += binding
     jobs = jobs or max(1, min(len(cmds), os.cpu_count() or 1, 16))
     with ThreadPoolExecutor(max_workers=jobs) as pool:
         results = list(pool.map(lambda c: _run(c, verbose), cmds))

@@ -6,45 +6,12 @@
 
 #include <stdint.h>
 
+#include "args.h"
 #include "launch_block.h"
 
 namespace {
 
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-bool aligned16(const void* p) { return aligned(p, 16); }
-
-// a * b * c, or -1 past 2^60
-int64_t mul3(int64_t a, int64_t b, int64_t c) {
-    const int64_t lim = (int64_t)1 << 60;
-    if (a == 0 || b == 0 || c == 0) return 0;
-    if (a > lim / b) return -1;
-    const int64_t ab = a * b;
-    if (ab > lim / c) return -1;
-    return ab * c;
-}
-
-// `count` runs of `width` bytes, `stride` bytes apart
-struct Rows {
-    uintptr_t at;
-    uint64_t count, width, stride;
-};
-Rows rows_of(const void* p, int64_t count, int64_t width, int64_t stride) {
-    return Rows{reinterpret_cast<uintptr_t>(p), (uint64_t)count, (uint64_t)width, (uint64_t)stride};
-}
-Rows bytes_of(const void* p, int64_t bytes) { return rows_of(p, 1, bytes, bytes); }
-
-bool overlaps(const Rows& a, const Rows& b) {
-    if (!a.count || !b.count || !a.width || !b.width) return false;
-    const uintptr_t a_end = a.at + (a.count - 1) * a.stride + a.width, b_end = b.at + (b.count - 1) * b.stride + b.width;
-    if (a_end <= b.at || b_end <= a.at) return false;
-    if (a.count > 1 && b.count > 1 && a.stride == b.stride) {
-        // side by side in the same rows (q and k of one projection): their
-        // places modulo the stride decide
-        const uint64_t off = a.at < b.at ? (b.at - a.at) % a.stride : (a.stride - (a.at - b.at) % a.stride) % a.stride;
-        return !(off >= a.width && off + b.width <= a.stride);
-    }
-    return true;
-}
+using namespace fp8g;
 
 bool valid_type(int t) { return t == 0 || t == 1; }
 int hip_status(hipError_t e) { return e == hipSuccess ? FP8G_OK : FP8G_ERR_HIP; }

@@ -1,0 +1,248 @@
+// Fused FP8 products for few rows, one product or one for every expert.
+//
+//   z[m, j] = sa[m] sb[j] sum_k A[m, k] B[j, k] + bias[j]      (or block scales)
+//   D[m, n] = act(z[m, n]) (* z[m, N + n] where gated) + residual[m, n]
+//
+// With few rows the weights' bytes are the bound, so nothing stands between
+// them and the matrix core: a wave loads a 16 x 128-byte piece of B straight
+// into the operand registers (lane L holds chunks L/16 and 4 + L/16, 16 bytes
+// each, of row L % 16; rows of 128 bytes are whole lines), and A's pieces, which
+// all workgroups share and the L2 holds, the same way.
+//
+// The eight waves of a workgroup split K: wave w takes the 128-byte steps w, w +
+// 8, ..., so that together they read 1 KB of each row in turn, and every wave has
+// the loads of `AHEAD` steps in flight.  Their sums meet in LDS, added in the
+// order of the waves, and a thread finishes four neighbouring columns of a row.
+//
+// The instruction is V_MFMA_SCALE_F32_16X16X128_F8F6F4 with B's rows as its
+// first operand, so a lane's four results are four neighbouring columns n of one
+// row m.  A lane's first 16 operand bytes are elements 16 g .. 16 g + 15 of the
+// 128 (g = lane / 16), its second 64 + 16 g ..; lane group g brings the scale of
+// the 32-element block g.
+
+#include <type_traits>
+
+#include "epilogue.h"
+#include "launch_ffn.h"
+
+namespace fp8g {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+typedef unsigned int v2u __attribute__((ext_vector_type(2)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+
+constexpr int RW_WAVES = 8;
+constexpr int RW_THREADS = 64 * RW_WAVES;
+constexpr uint32_t RW_OOB = 0x80000000u;      // past any panel (panels are < 2^31 bytes)
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rw_panel(const void* p, int64_t bytes) {
+    // loads at or past the end return 0
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+}
+
+struct RowsArgs {
+    FusedArgs f;
+    Act act;
+};
+
+// NB blocks of 16 of B's rows (gated: NB / 2 of the gate, then NB / 2 of the up
+// projection), MB blocks of 16 rows of A.
+template <bool MX, bool GATED, int NB, int MB, int AHEAD>
+__global__ __launch_bounds__(RW_THREADS, 4) void gemm_rows_kernel(RowsArgs args) {
+    const FusedArgs& a = args.f;
+    constexpr int NO = GATED ? NB / 2 : NB;              // blocks of output columns
+    __shared__ v4f red[RW_WAVES][NB * MB][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, g = lane >> 4;
+    const int N = (int)a.n, K = (int)a.k, nblk = K / 32;
+    const int n0 = (int)blockIdx.x * NO * 16;            // first output column
+    const int64_t nrows = GATED ? 2 * (int64_t)N : N;    // B's rows
+    const uint8_t* B = a.B;
+    int64_t s0 = (int64_t)blockIdx.y * (16 * MB), s1 = a.m, step = (int64_t)gridDim.y * (16 * MB);
+    int64_t b_row = 0;                                    // this product's first row of scale_b and bias
+    if (a.expert_start) {
+        const int e = blockIdx.y, S = (int)a.m;
+        s0 = min(max(a.expert_start[e], 0), S);
+        s1 = min(max(a.expert_start[e + 1], (int)s0), S);
+        step = 16 * MB;
+        b_row = e * nrows;
+        B += b_row * K;
+    }
+    const int steps = (K + 127) / 128;
+
+    // B: panel of the output columns' rows, one for the gate and one for the up projection
+    const int cols = min(NO * 16, N - n0);
+    __amdgpu_buffer_rsrc_t rsB[GATED ? 2 : 1], rsEB[GATED ? 2 : 1];
+#pragma unroll
+    for (int h = 0; h < (GATED ? 2 : 1); h++) {
+        const int64_t first = n0 + (int64_t)h * N;
+        rsB[h] = rw_panel(B + first * K, (int64_t)cols * K);
+        if constexpr (MX)
+            rsEB[h] = rw_panel(static_cast<const uint8_t*>(a.scale_b) + (b_row + first) * nblk, (int64_t)cols * nblk);
+    }
+    uint32_t vb[NO], veb[NO];
+#pragma unroll
+    for (int i = 0; i < NO; i++) {
+        vb[i] = (uint32_t)(16 * i + l16) * (uint32_t)K + 16u * g;
+        veb[i] = (uint32_t)(16 * i + l16) * (uint32_t)nblk + g;
+    }
+
+    for (; s0 < s1; s0 += step) {
+        const int count = (int)min((int64_t)(16 * MB), s1 - s0);
+        // A: this chunk's rows, or with `rows` all of A
+        const bool gather = a.rows != nullptr;
+        const __amdgpu_buffer_rsrc_t rsA = gather ? rw_panel(a.A, a.a_rows * K) : rw_panel(a.A + s0 * K, (int64_t)count * K);
+        __amdgpu_buffer_rsrc_t rsEA;
+        if constexpr (MX) {
+            const uint8_t* ea = static_cast<const uint8_t*>(a.scale_a);
+            rsEA = gather ? rw_panel(ea, a.a_rows * nblk) : rw_panel(ea + s0 * nblk, (int64_t)count * nblk);
+        }
+        uint32_t va[MB], vea[MB];
+#pragma unroll
+        for (int j = 0; j < MB; j++) {
+            int r = min(16 * j + l16, count - 1);         // rows past the end: the last one again, not stored
+            if (gather) r = min(max(a.rows[s0 + r], 0), (int)a.a_rows - 1);
+            va[j] = (uint32_t)r * (uint32_t)K + 16u * g;
+            vea[j] = (uint32_t)r * (uint32_t)nblk + g;
+        }
+
+        struct Frag {
+            v8i b[NB], a[MB];
+            uint32_t eb[NB], ea[MB];
+        };
+        auto load16 = [&](__amdgpu_buffer_rsrc_t rs, uint32_t off, int st) __attribute__((always_inline)) -> v8i {
+            const int kc = 128 * st + 16 * g;             // bytes past K read 0
+            const uint32_t so = 128u * (uint32_t)st;
+            const v4u x = __builtin_amdgcn_raw_buffer_load_b128(rs, kc < K ? off : RW_OOB, so, 0);
+            const v4u y = __builtin_amdgcn_raw_buffer_load_b128(rs, kc + 64 < K ? off + 64u : RW_OOB, so, 0);
+            return (v8i){(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
+        };
+        auto load = [&](int st, Frag& f) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < NB; i++) f.b[i] = load16(rsB[i / NO], vb[i % NO], st);
+#pragma unroll
+            for (int j = 0; j < MB; j++) f.a[j] = load16(rsA, va[j], st);
+            if constexpr (MX) {
+                const bool in = 4 * st + g < nblk;
+#pragma unroll
+                for (int i = 0; i < NB; i++)
+                    f.eb[i] = __builtin_amdgcn_raw_buffer_load_b8(rsEB[i / NO], in ? veb[i % NO] : RW_OOB, 4u * st, 0);
+#pragma unroll
+                for (int j = 0; j < MB; j++)
+                    f.ea[j] = __builtin_amdgcn_raw_buffer_load_b8(rsEA, in ? vea[j] : RW_OOB, 4u * st, 0);
+            }
+        };
+        v4f acc[NB][MB];
+#pragma unroll
+        for (int i = 0; i < NB; i++)
+#pragma unroll
+            for (int j = 0; j < MB; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+
+        // steps past the last one load and add zeros
+        Frag f[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; u++) load(wave + RW_WAVES * u, f[u]);
+        for (int st = wave; st < steps; st += RW_WAVES * AHEAD) {
+#pragma unroll
+            for (int u = 0; u < AHEAD; u++) {
+#pragma unroll
+                for (int i = 0; i < NB; i++)
+#pragma unroll
+                    for (int j = 0; j < MB; j++) {
+                        if constexpr (MX)
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f[u].b[i], f[u].a[j], acc[i][j], 0, 0, 0,
+                                                                                         (int)f[u].eb[i], 0, (int)f[u].ea[j]);
+                        else
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f[u].b[i], f[u].a[j], acc[i][j], 0, 0, 0,
+                                                                                         127, 0, 127);
+                    }
+                load(st + RW_WAVES * (u + AHEAD), f[u]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NB; i++)
+#pragma unroll
+            for (int j = 0; j < MB; j++) red[wave][i * MB + j][lane] = acc[i][j];
+        __syncthreads();
+
+        // a thread: output columns n .. n + 3 of row m
+        for (int u = threadIdx.x; u < NO * MB * 64; u += RW_THREADS) {
+            const int block = u >> 6, i = block / MB, j = block % MB, ln = u & 63;
+            const int mr = 16 * j + (ln & 15), nc = 16 * i + 4 * (ln >> 4);
+            if (mr >= count || nc >= cols) continue;
+            const int n = n0 + nc, left = min(4, cols - nc);
+            const int64_t slot = s0 + mr;
+            float z[GATED ? 2 : 1][4];
+#pragma unroll
+            for (int h = 0; h < (GATED ? 2 : 1); h++) {
+                v4f t = red[0][(h * NO + i) * MB + j][ln];
+#pragma unroll
+                for (int w = 1; w < RW_WAVES; w++) t += red[w][(h * NO + i) * MB + j][ln];
+                float sm = 1.0f;
+                if constexpr (!MX) {
+                    int64_t r = slot;
+                    if (gather) r = min(max(a.rows[slot], 0), (int)a.a_rows - 1);
+                    sm = static_cast<const float*>(a.scale_a)[r];
+                }
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    const int64_t row = b_row + (int64_t)h * N + n + min(c, left - 1);
+                    float v = t[c];
+                    if constexpr (!MX) v = v * sm * static_cast<const float*>(a.scale_b)[row];
+                    if (a.bias) v += a.bias[row];
+                    z[h][c] = v;
+                }
+            }
+            float v[4];
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                v[c] = args.act.on ? activate(z[0][c], args.act.c1, args.act.c3) : z[0][c];
+                if constexpr (GATED) v[c] *= z[1][c];
+            }
+            const int64_t at = slot * N + n;
+            if (a.f32) {
+                float* D = static_cast<float*>(a.D);
+                const float* res = static_cast<const float*>(a.residual);
+                for (int c = 0; c < left; c++) D[at + c] = res ? v[c] + res[at + c] : v[c];
+            } else {
+                uint16_t* D = static_cast<uint16_t*>(a.D);
+                const uint16_t* res = static_cast<const uint16_t*>(a.residual);
+                for (int c = 0; c < left; c++) {
+                    const float r = res ? __builtin_bit_cast(float, (uint32_t)res[at + c] << 16) : 0.0f;
+                    D[at + c] = (uint16_t)bf16x2_bits(res ? v[c] + r : v[c], 0.0f);
+                }
+            }
+        }
+        __syncthreads();       // the sums are read before the next chunk's are written
+    }
+}
+
+template <bool MX, bool GATED, int MB>
+static hipError_t launch_rows(const FusedArgs& f, hipStream_t stream) {
+    constexpr int NB = 2, NO = GATED ? 1 : 2, AHEAD = MB == 1 ? 4 : 2;
+    const int64_t gx = (f.n + 16 * NO - 1) / (16 * NO);
+    int64_t gy = f.expert_start ? f.experts : (f.m + 16 * MB - 1) / (16 * MB);
+    if (gy > 65535) gy = 65535;
+    RowsArgs args{f, act_of(f.act)};
+    gemm_rows_kernel<MX, GATED, NB, MB, AHEAD><<<dim3((unsigned)gx, (unsigned)gy), dim3(RW_THREADS), 0, stream>>>(args);
+    return hipGetLastError();
+}
+
+int64_t moe_gemm_bytes(const FusedArgs&) { return 0; }
+
+hipError_t launch_gemm_fused(const FusedArgs& f, hipStream_t stream) {
+    const int64_t rows = f.expert_start ? (f.m + f.experts - 1) / f.experts : f.m;   // of a product, on average
+    const int mb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    auto go = [&](auto mx, auto gated) {
+        constexpr bool X = decltype(mx)::value, G = decltype(gated)::value;
+        return mb == 1 ? launch_rows<X, G, 1>(f, stream) : mb == 2 ? launch_rows<X, G, 2>(f, stream) : launch_rows<X, G, 4>(f, stream);
+    };
+    using T = std::true_type;
+    using F = std::false_type;
+    if (f.mx) return f.gated ? go(T{}, T{}) : go(T{}, F{});
+    return f.gated ? go(F{}, T{}) : go(F{}, F{});
+}
+
+}  // namespace fp8g

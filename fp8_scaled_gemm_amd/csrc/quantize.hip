@@ -33,10 +33,9 @@
 // the smallest normal fp32 (where 1/s may overflow) use the IEEE division.
 // This file is built without fast-math.
 
-#include <type_traits>
-
 #include "device_common.h"
 #include "launch.h"
+#include "row_div.h"
 
 namespace fp8g {
 
@@ -45,73 +44,11 @@ typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 
 constexpr int QROWS_PER_BLOCK = 4;          // per-wave kernel: 4 waves of 64 lanes, one row each
-constexpr float FLT_MIN_NORMAL = 1.17549435e-38f;
-
-// ---- output formats: the largest finite magnitude (the divisor of amax) and
-// the saturating round-to-nearest-even cast of four values into one dword
-struct OutE4M3 {
-    static constexpr float MAX = 448.0f;
-    __device__ __forceinline__ static uint32_t pack4(float a, float b, float c, float d) {
-        return e4m3_pack4(a, b, c, d);
-    }
-};
-
-struct OutE5M2 {
-    static constexpr float MAX = 57344.0f;
-    __device__ __forceinline__ static uint32_t pack4(float a, float b, float c, float d) {
-        return e5m2_pack4(a, b, c, d);
-    }
-};
 
 template <class O>
 __device__ __forceinline__ uint8_t cast_one(float a) {
     return (uint8_t)(O::pack4(a, 0.0f, 0.0f, 0.0f) & 0xFFu);
 }
-
-// Per-row (per-tensor) divisor: the scale, its correctly rounded reciprocal, the path.
-struct RowDiv {
-    float s, y;
-    bool zero;    // s == 0: signed zeros
-    bool ieee;    // s below the smallest normal: plain IEEE division
-};
-
-// amax is the same in every lane; readfirstlane makes that visible to the
-// compiler, so the path is chosen once with a scalar branch.
-template <class O>
-__device__ __forceinline__ RowDiv row_div(float amax) {
-    amax = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, amax)));
-    RowDiv d;
-    d.s = amax / O::MAX;
-    d.y = 1.0f / d.s;
-    d.zero = (d.s == 0.0f);
-    d.ieee = (d.s < FLT_MIN_NORMAL);
-    return d;
-}
-
-// PATH 0: Markstein quotient; 1: IEEE division; 2: signed zero (s == 0)
-template <int PATH>
-__device__ __forceinline__ float quot(float x, const RowDiv& d) {
-    if constexpr (PATH == 2) {
-        return x * 0.0f;
-    } else if constexpr (PATH == 1) {
-        return x / d.s;
-    } else {
-        const float q0 = x * d.y;
-        const float e = __builtin_fmaf(-q0, d.s, x);
-        // x = -0 gives e = +0 and q0 + e y = +0; the quotient has x's sign (s > 0)
-        return __builtin_copysignf(__builtin_fmaf(e, d.y, q0), x);
-    }
-}
-
-// f(path_tag) with the path as a compile-time constant
-template <typename F>
-__device__ __forceinline__ void by_path(const RowDiv& d, F&& f) {
-    if (d.zero) f(std::integral_constant<int, 2>{});
-    else if (d.ieee) f(std::integral_constant<int, 1>{});
-    else f(std::integral_constant<int, 0>{});
-}
-
-__device__ __forceinline__ float amax2(float a, float b) { return __builtin_fmaxf(__builtin_fabsf(a), __builtin_fabsf(b)); }
 
 // ---- input vectors: 16 bytes of input = EPL elements -> EPL bytes of codes.
 struct InF32 {
