@@ -25,9 +25,11 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfp8g.so")
 SOURCES = ["abi.cpp", "quantize.hip", "mx_quantize.hip", "concat.hip", "roof.hip", "gemm.hip",
            "abi_block.cpp", "lora.hip", "qk_norm_rope.hip", "kv4_cache.hip", "kv4_attention.hip",
-           "abi_ffn.cpp", "norm_quant.hip", "gemm_rows.hip", "moe_route.hip", "moe_combine.hip"]
+           "abi_ffn.cpp", "norm_quant.hip", "gemm_rows.hip", "gemm_fused.hip", "moe_route.hip", "moe_combine.hip"]
 # gemm.hip is compiled once per operand-format pair (FP8G_GEMM_FMT = 2 * fmt_a + fmt_b)
 GEMM_PARTS = 4
+# and gemm_fused.hip once per mode and kind (FP8G_FUSED_PART = 4 * gated + 2 * mx + moe)
+FUSED_PARTS = 8
 BINDING = os.path.join(HERE, "_block.so")
 BINDING_SOURCES = ["block_binding.cpp", "ffn_binding.cpp"]
 ARCH = "gfx950"
@@ -54,9 +56,13 @@ def _units():
         if src == "gemm.hip":
             for p in range(GEMM_PARTS):
                 out.append((src, ["-DFP8G_GEMM_FMT=%d" % p], os.path.join(OBJDIR, "%s_%d.o" % (stem, p))))
+        elif src == "gemm_fused.hip":
+            for p in range(FUSED_PARTS):
+                out.append((src, ["-DFP8G_FUSED_PART=%d" % p], os.path.join(OBJDIR, "%s_%d.o" % (stem, p))))
         else:
             out.append((src, [], os.path.join(OBJDIR, stem + ".o")))
-    return out
+    # the objects that take longest first
+    return sorted(out, key=lambda u: not u[0].startswith("gemm"))
 
 
 def _binding_cmds(cc):

@@ -230,9 +230,7 @@ static hipError_t launch_rows(const FusedArgs& f, hipStream_t stream) {
     return hipGetLastError();
 }
 
-int64_t moe_gemm_bytes(const FusedArgs&) { return 0; }
-
-hipError_t launch_gemm_fused(const FusedArgs& f, hipStream_t stream) {
+hipError_t launch_gemm_rows(const FusedArgs& f, hipStream_t stream) {
     const int64_t rows = f.expert_start ? (f.m + f.experts - 1) / f.experts : f.m;   // of a product, on average
     const int mb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     auto go = [&](auto mx, auto gated) {

@@ -33,6 +33,18 @@ struct FusedArgs {
 };
 int64_t moe_gemm_bytes(const FusedArgs& a);
 hipError_t launch_gemm_fused(const FusedArgs& a, hipStream_t stream);
+hipError_t launch_gemm_rows(const FusedArgs& a, hipStream_t stream);      // few rows, no workspace
+
+// A launch of the tile kernel; for the experts' products with its plan (gemm_tile.h).
+struct TileLaunch {
+    int tile, dev, cus;
+    int64_t tile_rows;                   // of all experts, at most
+    const int32_t* plan;
+    const uint32_t* row_at;
+    const void* scale_a;
+};
+// The tile that the scaled product of these sizes takes (gemm.hip), without K splits.
+int gemm_tile_of(int64_t m, int64_t n, int64_t k, int mx, int cus);
 
 struct RouteArgs {
     const void* logits;
