@@ -40,7 +40,7 @@ The feed-forward half's operators (``include/fp8g_ffn.h``, module ``ffn``):
     fp8_moe_gemm(A, B, scale_a, scale_b, expert_start, rows)           -> D
     mxfp8_moe_gemm(...)                                                -> D
     moe_combine(y, slots, weights, residual)                           -> out
-    moe_route_workspace(...), moe_gemm_workspace(...)                  -> bytes
+    gemm_fused_workspace(...), moe_route_workspace(...), moe_gemm_workspace(...)  -> bytes
 
 E4M3 tensors are ``torch.float8_e4m3fn`` (OCP, the gfx950 format) and E5M2
 tensors ``torch.float8_e5m2``, or either as raw ``torch.uint8`` codes; the
@@ -57,7 +57,7 @@ __all__ = ["load", "fp8_quantize_rowwise", "fp8_quantize_ex", "mxfp8_quantize", 
            "status_string",
            "lora_add", "lora_add_workspace", "qk_norm_rope", "KV4Cache", "kv4_cache", "kv4_append", "kv4_gather",
            "kv4_attention", "kv4_attention_workspace",
-           "NormQuant", "add_rms_norm_quantize", "fp8_gemm_fused", "mxfp8_gemm_fused", "MoeRoute", "moe_route",
+           "NormQuant", "add_rms_norm_quantize", "fp8_gemm_fused", "mxfp8_gemm_fused", "gemm_fused_workspace", "MoeRoute", "moe_route",
            "moe_route_workspace", "fp8_moe_gemm", "mxfp8_moe_gemm", "moe_gemm_workspace", "moe_combine",
            "Fp8gError", "LIB_PATH", "HEADER_PATH", "OUT_BF16", "OUT_F32", "FMT_E4M3", "FMT_E5M2"]
 
@@ -96,8 +96,9 @@ _SIGNATURES = {
     "kv4_attention_workspace": [_I64] * 9,
     "add_rms_norm_quantize": [_VOIDP, _I64, _VOIDP, _I64, ctypes.c_int, _I64, _I64, _VOIDP, ctypes.c_float, ctypes.c_int,
                               ctypes.c_int] + [_VOIDP] * 5,
-    "fp8_gemm_fused": [_I64] * 3 + [_VOIDP] * 5 + [ctypes.c_int] * 2 + [_VOIDP] * 2 + [ctypes.c_int, _VOIDP],
-    "mxfp8_gemm_fused": [_I64] * 3 + [_VOIDP] * 5 + [ctypes.c_int] * 2 + [_VOIDP] * 2 + [ctypes.c_int, _VOIDP],
+    "fp8_gemm_fused": [_I64] * 3 + [_VOIDP] * 5 + [ctypes.c_int] * 2 + [_VOIDP] * 2 + [ctypes.c_int, _VOIDP, _I64, _VOIDP],
+    "mxfp8_gemm_fused": [_I64] * 3 + [_VOIDP] * 5 + [ctypes.c_int] * 2 + [_VOIDP] * 2 + [ctypes.c_int, _VOIDP, _I64, _VOIDP],
+    "gemm_fused_workspace": [_I64] * 3 + [ctypes.c_int] * 2,
     "moe_route": [_VOIDP, ctypes.c_int] + [_I64] * 3 + [_VOIDP, ctypes.c_int] + [_I64] * 3 + [ctypes.c_int, ctypes.c_float]
                  + [_VOIDP] * 6 + [_I64, _VOIDP],
     "moe_route_workspace": [_I64] * 3,
@@ -448,5 +449,5 @@ def fp8g_roof_stream(src, dst, write_ratio, nontemporal_stores=0):
 
 from .block import (KV4Cache, kv4_append, kv4_attention, kv4_attention_workspace, kv4_cache,  # noqa: E402
                     kv4_gather, lora_add, lora_add_workspace, qk_norm_rope)
-from .ffn import (MoeRoute, NormQuant, add_rms_norm_quantize, fp8_gemm_fused, fp8_moe_gemm, moe_combine,  # noqa: E402
-                  moe_gemm_workspace, moe_route, moe_route_workspace, mxfp8_gemm_fused, mxfp8_moe_gemm)
+from .ffn import (MoeRoute, NormQuant, add_rms_norm_quantize, fp8_gemm_fused, fp8_moe_gemm, gemm_fused_workspace,  # noqa: E402
+                  moe_combine, moe_gemm_workspace, moe_route, moe_route_workspace, mxfp8_gemm_fused, mxfp8_moe_gemm)

@@ -28,8 +28,8 @@ SOURCES = ["abi.cpp", "quantize.hip", "mx_quantize.hip", "concat.hip", "roof.hip
            "abi_ffn.cpp", "norm_quant.hip", "gemm_rows.hip", "gemm_fused.hip", "moe_route.hip", "moe_combine.hip"]
 # gemm.hip is compiled once per operand-format pair (FP8G_GEMM_FMT = 2 * fmt_a + fmt_b)
 GEMM_PARTS = 4
-# and gemm_fused.hip once per mode and kind (FP8G_FUSED_PART = 4 * gated + 2 * mx + moe)
-FUSED_PARTS = 8
+# and gemm_fused.hip once per mode and kind (FP8G_FUSED_PART = 4 * gated + 2 * mx + moe, or 8 + mx)
+FUSED_PARTS = 10
 BINDING = os.path.join(HERE, "_block.so")
 BINDING_SOURCES = ["block_binding.cpp", "ffn_binding.cpp"]
 ARCH = "gfx950"

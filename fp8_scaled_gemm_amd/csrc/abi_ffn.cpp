@@ -51,8 +51,8 @@ int fused(int64_t m, int64_t n, int64_t k, int64_t experts, const uint8_t* A, in
     if (ab < 0 || bb < 0 || db < 0 || sab < 0 || sbb < 0) return FP8G_ERR_UNSUPPORTED;
     FusedArgs a = {A, B, sa, sb, bias, residual, D, rows, moe ? start : nullptr, ws, m, n, k, a_rows, products, act,
                    gated != 0, mx, out_dtype == FP8G_OUT_F32};
-    const int64_t need = moe ? moe_gemm_bytes(a) : 0;
-    if (moe && ws_bytes < need) return FP8G_ERR_UNSUPPORTED;
+    const int64_t need = moe ? moe_gemm_bytes(a) : gemm_fused_bytes(a);
+    if (ws_bytes < need) return FP8G_ERR_UNSUPPORTED;
     if ((ab > 0 && !A) || (bb > 0 && !B) || (sab > 0 && !sa) || (sbb > 0 && !sb) || !D || (moe && !start) ||
         (need > 0 && !ws))
         return FP8G_ERR_NULL;
@@ -66,7 +66,7 @@ int fused(int64_t m, int64_t n, int64_t k, int64_t experts, const uint8_t* A, in
     const Rows d = bytes_of(D, db), w = bytes_of(ws, need), r = bytes_of(residual, residual ? db : 0);
     for (const Rows& x : in)
         if (overlaps(d, x) || overlaps(w, x)) return FP8G_ERR_OVERLAP;
-    if ((residual != D && overlaps(d, r)) || overlaps(d, w)) return FP8G_ERR_OVERLAP;
+    if ((residual != D && overlaps(d, r)) || overlaps(d, w) || overlaps(w, r)) return FP8G_ERR_OVERLAP;
     return hip_status(launch_gemm_fused(a, stream));
 }
 
@@ -123,16 +123,23 @@ int add_rms_norm_quantize(const void* x, int64_t x_stride, const void* residual,
 
 int fp8_gemm_fused(int64_t m, int64_t n, int64_t k, const uint8_t* A, const uint8_t* B, const float* scale_a,
                    const float* scale_b, const float* bias, int act, int gated, const void* residual, void* D,
-                   int out_dtype, hipStream_t stream) {
+                   int out_dtype, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     return fused(m, n, k, 1, A, m, nullptr, nullptr, B, scale_a, scale_b, 0, bias, act, gated, residual, D, out_dtype,
-                 nullptr, 0, false, stream);
+                 workspace, workspace_bytes, false, stream);
 }
 
 int mxfp8_gemm_fused(int64_t m, int64_t n, int64_t k, const uint8_t* A, const uint8_t* B, const uint8_t* scale_a,
                      const uint8_t* scale_b, const float* bias, int act, int gated, const void* residual, void* D,
-                     int out_dtype, hipStream_t stream) {
+                     int out_dtype, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     return fused(m, n, k, 1, A, m, nullptr, nullptr, B, scale_a, scale_b, 1, bias, act, gated, residual, D, out_dtype,
-                 nullptr, 0, false, stream);
+                 workspace, workspace_bytes, false, stream);
+}
+
+int64_t gemm_fused_workspace(int64_t m, int64_t n, int64_t k, int gated, int mx) {
+    if (check_product(m, n, k, 1, FP8G_ACT_NONE, gated, mx, FP8G_OUT_BF16) != FP8G_OK) return -1;
+    FusedArgs a = {};
+    a.m = m, a.n = n, a.k = k, a.experts = 1, a.gated = gated != 0, a.mx = mx != 0;
+    return m && n ? gemm_fused_bytes(a) : 0;
 }
 
 int64_t moe_gemm_workspace(int64_t slots, int64_t n, int64_t k, int64_t experts, int gathered, int gated, int mx) {

@@ -89,10 +89,10 @@ PyObject* norm_quantize_(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// m, n, k, A, B, scale_a, scale_b, mx, bias, act, gated, residual, D, float32
+// m, n, k, A, B, scale_a, scale_b, mx, bias, act, gated, residual, D, float32, workspace
 PyObject* gemm_fused_(PyObject*, PyObject* const* a, Py_ssize_t count) {
     return guarded([&]() -> PyObject* {
-        arguments(count, 14);
+        arguments(count, 15);
         const int64_t m = integer(a[0]), n = integer(a[1]), k = integer(a[2]);
         const Tensor &A = codes(a[3], "A"), &B = codes(a[4], "B"), &sa = tensor(a[5], "scale_a"), &sb = tensor(a[6], "scale_b");
         const bool mx = truth(a[7]), gated = truth(a[10]), f32 = truth(a[13]);
@@ -119,10 +119,11 @@ PyObject* gemm_fused_(PyObject*, PyObject* const* a, Py_ssize_t count) {
         }
         const Tensor D = output(a[12], "D", dt, {m, n}, c);
         const int out = f32 ? FP8G_OUT_F32 : FP8G_OUT_BF16;
+        const Workspace ws(a[14], gemm_fused_workspace(m, n, k, gated, mx), c);
         const int st = mx ? mxfp8_gemm_fused(m, n, k, bytes_at(A), bytes_at(B), bytes_at(sa), bytes_at(sb), bias, act, gated, res,
-                                             D.data_ptr(), out, c.stream)
+                                             D.data_ptr(), out, ws.ptr, ws.bytes, c.stream)
                           : fp8_gemm_fused(m, n, k, bytes_at(A), bytes_at(B), sa.data_ptr<float>(), sb.data_ptr<float>(), bias,
-                                           act, gated, res, D.data_ptr(), out, c.stream);
+                                           act, gated, res, D.data_ptr(), out, ws.ptr, ws.bytes, c.stream);
         return st ? PyLong_FromLong(st) : THPVariable_Wrap(D);
     });
 }

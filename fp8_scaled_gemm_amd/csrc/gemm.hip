@@ -10,7 +10,6 @@
 
 #include "gemm_tile.h"
 #include "launch.h"
-#include "launch_ffn.h"
 
 namespace fp8g {
 
@@ -331,8 +330,6 @@ static bool fits(int64_t m, int64_t n, int64_t k) {
     const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
     return m < (1LL << 31) && n < (1LL << 31) && k < (1LL << 23) && tiles < (1LL << 31);
 }
-
-int gemm_tile_of(int64_t m, int64_t n, int64_t k, int mx, int cus) { return gemm_schedule(m, n, k, mx != 0, cus).tile; }
 
 hipError_t schedule_gemm(int64_t m, int64_t n, int64_t k, int mx, int cus, int* tile_m, int* tile_n, int* split,
                          int* split_tiles) {

@@ -10,9 +10,11 @@
 // row's own, and puts A's scales (32 or 128 times smaller than A) into the
 // slots' order.
 //
-// Compiled once per mode and kind (FP8G_FUSED_PART = 4 * gated + 2 * MX + MOE).
+// Compiled once per mode and kind (FP8G_FUSED_PART = 4 * gated + 2 * MX + MOE, or
+// 8 + MX for the partial sums of K ranges).
 
 #include <atomic>
+#include <cstdlib>
 #include <type_traits>
 
 #include "gemm_tile.h"
@@ -46,8 +48,9 @@ static hipError_t launch_tile(const FusedArgs& a, const TileLaunch& t, hipStream
         configured.fetch_or(bit, std::memory_order_release);
     }
     constexpr int BM = Geo<TILE>::BM, BNO = EPI == EPI_GATED ? Geo<TILE>::BN / 2 : Geo<TILE>::BN;
-    const int64_t tiles = (MOE ? t.tile_rows : (a.m + BM - 1) / BM) * ((a.n + BNO - 1) / BNO);
-    const TileExtra ex = {a.bias, a.residual, act_of(a.act), t.plan, t.row_at, t.row_at ? (uint32_t)(a.a_rows * a.k) : 0u};
+    const int64_t tiles = (MOE ? t.tile_rows : (a.m + BM - 1) / BM) * ((a.n + BNO - 1) / BNO) * (EPI == EPI_PARTIAL ? t.ranges : 1);
+    const TileExtra ex = {a.bias,  a.residual, act_of(a.act), t.plan, t.row_at, t.row_at ? (uint32_t)(a.a_rows * a.k) : 0u,
+                          t.ranges, t.pitch, t.part_rows};
     kern<<<dim3((unsigned)(tiles < t.cus ? tiles : t.cus)), dim3(NTHREADS), LDS_BYTES, stream>>>(
         (int)a.m, (int)a.n, (int)a.k, a.A, a.B, t.scale_a, a.scale_b, a.D, ex);
     return hipGetLastError();
@@ -57,19 +60,24 @@ template <bool MX, bool MOE, int EPI>
 hipError_t launch_fused_part(const FusedArgs& a, const TileLaunch& t, hipStream_t stream) {
     auto go = [&](auto tile) {
         constexpr int TILE = decltype(tile)::value;
-        if (a.k % BK)
+        if constexpr (EPI == EPI_PARTIAL)
+            return a.k % BK ? launch_tile<MX, true, true, TILE, EPI, MOE>(a, t, stream)
+                            : launch_tile<MX, true, false, TILE, EPI, MOE>(a, t, stream);
+        else if (a.k % BK)
             return a.f32 ? launch_tile<MX, true, true, TILE, EPI, MOE>(a, t, stream)
                          : launch_tile<MX, false, true, TILE, EPI, MOE>(a, t, stream);
-        return a.f32 ? launch_tile<MX, true, false, TILE, EPI, MOE>(a, t, stream)
-                     : launch_tile<MX, false, false, TILE, EPI, MOE>(a, t, stream);
+        else
+            return a.f32 ? launch_tile<MX, true, false, TILE, EPI, MOE>(a, t, stream)
+                         : launch_tile<MX, false, false, TILE, EPI, MOE>(a, t, stream);
     };
     if constexpr (!MX) {
         if (t.tile == TILE_64x128) return go(std::integral_constant<int, TILE_64x128>{});
-        if constexpr (!MOE)
+        if constexpr (EPI != EPI_PARTIAL)
             if (t.tile == 256) return launch_tile<MX, false, false, 256, EPI, MOE>(a, t, stream);
     }
-    if (t.tile == 128) return go(std::integral_constant<int, 128>{});
-    return go(std::integral_constant<int, TILE_256x128>{});
+    if constexpr (EPI != EPI_PARTIAL)
+        if (t.tile == TILE_256x128) return go(std::integral_constant<int, TILE_256x128>{});
+    return go(std::integral_constant<int, 128>{});
 }
 
 #ifndef FP8G_FUSED_PART
@@ -77,7 +85,11 @@ hipError_t launch_fused_part(const FusedArgs& a, const TileLaunch& t, hipStream_
 #endif
 #define FP8G_FUSED(KW, MX, MOE, EPI) \
     KW hipError_t launch_fused_part<MX, MOE, EPI>(const FusedArgs&, const TileLaunch&, hipStream_t);
+#if FP8G_FUSED_PART >= 8
+FP8G_FUSED(template, (FP8G_FUSED_PART == 9), false, EPI_PARTIAL)
+#else
 FP8G_FUSED(template, ((FP8G_FUSED_PART & 2) != 0), ((FP8G_FUSED_PART & 1) != 0), ((FP8G_FUSED_PART & 4) ? EPI_GATED : EPI_LINEAR))
+#endif
 
 #if FP8G_FUSED_PART == 0
 FP8G_FUSED(extern template, false, true, EPI_LINEAR)
@@ -87,6 +99,8 @@ FP8G_FUSED(extern template, false, false, EPI_GATED)
 FP8G_FUSED(extern template, false, true, EPI_GATED)
 FP8G_FUSED(extern template, true, false, EPI_GATED)
 FP8G_FUSED(extern template, true, true, EPI_GATED)
+FP8G_FUSED(extern template, false, false, EPI_PARTIAL)
+FP8G_FUSED(extern template, true, false, EPI_PARTIAL)
 
 template <bool MX, bool MOE>
 static hipError_t launch_fused(const FusedArgs& a, const TileLaunch& t, hipStream_t stream) {
@@ -169,20 +183,188 @@ __global__ __launch_bounds__(PLAN_THREADS) void moe_plan(const int32_t* __restri
     }
 }
 
-// Products of at most this many rows (of an expert: on average) go to gemm_rows.hip.
-constexpr int64_t FEW_ROWS = 64, FEW_ROWS_EXPERT = 32;
+// ---- one product: which kernel, tile and K ranges.
+//
+// Times of a launch in us, fitted to measurements on MI355X (256 CUs; weights
+// from HBM) and used to choose between
+//   the row kernel (gemm_rows.hip), the larger of
+//     4 + B at 5.5 TB/s, again at 8 TB/s for every further 64 rows, + A, read by
+//     every workgroup, at 9.3 TB/s (mode (b): 4.2, 6 and 7), and
+//     4 + the steps of a wave at 0.35 / 0.6 / 1.1 us with 16 / 32 / 64 rows of A
+//     (mode (b): half as much again);
+//   a tile: 4.5 + rounds of workgroups x (fixed + stages x stage), below, the
+//     stage of the small tiles shorter while they fill at most half of the CUs;
+//   64x128 or 128x128 tiles with K in ranges, where the tiles leave CUs idle:
+//     one round of the longest range, and 4 + the partial sums written and
+//     read at 4 TB/s for the kernel that adds them up.
+// Measured, mode (a), 2 x 11008 x 8192 gated: rows 37.7 us at m = 8, 51 at 32, 74
+// at 64 (64x128 tiles 41, 41, 43); 256x256 tiles 360 at 2500, 555 at 4099.  4096 x
+// 14336: rows 14.5 at 8, 35.5 at 64; 64x128 tiles 48 to 54 up to 512 rows, in 4
+// ranges 25 at 128; 128x128 tiles 130, 256x128 ones 104 at 1777.
+struct TileCost {
+    int tile;
+    double fixed, stage, idle_stage;
+};
+constexpr TileCost COST_A[] = {{TILE_64x128, 0.5, 0.38, 0.30}, {128, 0.5, 0.53, 0.43}, {TILE_256x128, 3.4, 0.92, 0.92},
+                               {256, 6.0, 1.27, 1.27}};
+constexpr TileCost COST_B[] = {{128, 0.3, 0.70, 0.58}, {TILE_256x128, 1.5, 1.04, 1.04}};
 
-static bool few_rows(const FusedArgs& a) {
-    return a.expert_start ? a.m <= FEW_ROWS_EXPERT * a.experts : a.m <= FEW_ROWS;
-}
-
-// The experts' tile by the rows an expert has on average.
-static int moe_tile(const FusedArgs& a) {
-    const int64_t rows = a.m / a.experts;
-    if (!a.mx && rows <= 64) return TILE_64x128;
-    return rows <= 128 ? 128 : TILE_256x128;
-}
 static int tile_bm(int tile) { return tile > 1000 ? tile / 1000 : tile; }
+static int tile_bn(int tile) { return tile > 1000 ? tile % 1000 : tile; }
+
+struct FusedPlan {
+    int tile;                    // 0: the row kernel
+    int ranges;                  // of K; 1: not split
+    double us;
+};
+static FusedPlan fused_plan(const FusedArgs& a, int cus) {
+    if (const char* force = getenv("FP8G_FORCE")) return {atoi(force) % 1000000, atoi(force) / 1000000 ? atoi(force) / 1000000 : 1, 0};
+    const int64_t b_rows = a.gated ? 2 * a.n : a.n, nk = (a.k + BK - 1) / BK;
+    const double b_bytes = (double)b_rows * a.k, work = b_bytes + (double)a.m * a.k;
+    const int64_t wgs = (b_rows + 31) / 32, cols = wgs < 512 && !a.gated ? 16 : 32;     // as launch_gemm_rows cuts it
+    const double a_read = (double)((b_rows + cols - 1) / cols) * ((a.m + 15) / 16 * 16) * a.k;
+    const double again = (double)((a.m + 63) / 64 - 1);
+    const double fed = b_bytes / (a.mx ? 4.2e6 : 5.5e6) + again * b_bytes / (a.mx ? 6.0e6 : 8.0e6) + a_read / (a.mx ? 7.0e6 : 9.3e6);
+    const double steps = (double)((nk + 3) / 4) * (a.m <= 16 ? 0.35 : a.m <= 32 ? 0.6 : 1.1) * (a.mx ? 1.5 : 1.0);
+    FusedPlan best = {0, 1, 4.0 + (fed > steps ? fed : steps)};
+    if (a.m <= 16) return best;                       // the tiles are mostly empty
+    const double hbm = 6.0 + work / 5.3e6;
+    auto consider = [&](const TileCost& c) {
+        // 256x256 tiles only where they hold their registers (fp32 output: 256x128 then)
+        if (c.tile == 256 && (a.mx || a.k % BK)) return;
+        const int64_t tiles = ((a.m + tile_bm(c.tile) - 1) / tile_bm(c.tile)) * ((b_rows + tile_bn(c.tile) - 1) / tile_bn(c.tile));
+        const int64_t rounds = (tiles + cus - 1) / cus;
+        const double stage = 2 * tiles <= cus ? c.idle_stage : c.stage;
+        double us = 4.5 + (double)rounds * (c.fixed + stage * (double)nk);
+        if (us < hbm) us = hbm;
+        if (us < best.us) best = {c.tile, 1, us};
+        if (c.tile != TILE_64x128 && c.tile != 128) return;
+        const double part = (double)tiles * tile_bm(c.tile) * tile_bn(c.tile) * 8.0;     // bytes written and read
+        for (int r = 2; r <= 16 && r * tiles <= cus && nk / r >= 4; r *= 2) {
+            // gated: the partial sums hold both projections
+            const double longest = (double)((nk + r - 1) / r + (a.mx ? 3 : 0));
+            us = 4.5 + c.fixed + (2 * r * tiles <= cus ? c.idle_stage : c.stage) * longest;
+            if (us < hbm) us = hbm;
+            us += 4.0 + r * part / 4.0e6;
+            if (us < best.us) best = {c.tile, r, us};
+        }
+    };
+    if (a.mx)
+        for (const TileCost& c : COST_B) consider(c);
+    else
+        for (const TileCost& c : COST_A) consider(c);
+    return best;
+}
+
+constexpr int PLAN_CUS = 256;    // the workspace's size may not hang on a device
+
+struct PartSpace {
+    int64_t rows, pitch, bytes;
+};
+static PartSpace part_space(const FusedArgs& a, const FusedPlan& p) {
+    PartSpace s = {};
+    if (p.ranges < 2) return s;
+    const int bm = tile_bm(p.tile), bn = tile_bn(p.tile);
+    s.rows = (a.m + bm - 1) / bm * bm;
+    s.pitch = ((a.gated ? 2 * a.n : a.n) + bn - 1) / bn * bn;
+    s.bytes = p.ranges * s.rows * s.pitch * 4;
+    return s;
+}
+int64_t gemm_fused_bytes(const FusedArgs& a) { return part_space(a, fused_plan(a, PLAN_CUS)).bytes; }
+
+// The ranges' sums added in order, and the epilogue: a thread takes four columns of a row.
+struct FinishArgs {
+    FusedArgs f;
+    Act act;
+    int64_t pitch, part;         // elements: of a row, of a range
+    int ranges;
+};
+constexpr int FIN_THREADS = 256;
+__global__ __launch_bounds__(FIN_THREADS) void fused_finish(FinishArgs x) {
+    const FusedArgs& a = x.f;
+    const int N = (int)a.n, n = ((int)blockIdx.x * FIN_THREADS + (int)threadIdx.x) * 4;
+    const int64_t m = blockIdx.y;
+    if (n >= N) return;
+    const int left = min(4, N - n);
+    const float* part = static_cast<const float*>(a.workspace) + m * x.pitch;
+    const float sm = a.mx ? 1.0f : static_cast<const float*>(a.scale_a)[m];
+    float z[2][4] = {};
+    for (int h = 0; h <= a.gated; ++h) {
+        const int64_t at = (int64_t)h * N + n;
+        float t[4] = {};
+        for (int r = 0; r < x.ranges; ++r) {
+            const float* p = part + r * x.part + at;
+            // the up projection's columns are aligned only where N is a multiple of four
+            if ((at & 3) == 0) {
+                const v4f v = *reinterpret_cast<const v4f*>(p);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) t[c] = r ? t[c] + v[c] : v[c];
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (c < left) t[c] = r ? t[c] + p[c] : p[c];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c >= left) continue;
+            float v = t[c];
+            if (!a.mx) v = v * sm * static_cast<const float*>(a.scale_b)[at + c];
+            if (a.bias) v += a.bias[at + c];
+            z[h][c] = v;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if (c >= left) continue;
+        float v = x.act.on ? activate(z[0][c], x.act.c1, x.act.c3) : z[0][c];
+        if (a.gated) v *= z[1][c];
+        const int64_t i = m * N + n + c;
+        if (a.f32) {
+            if (a.residual) v += static_cast<const float*>(a.residual)[i];
+            static_cast<float*>(a.D)[i] = v;
+        } else {
+            if (a.residual) v += __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(a.residual)[i] << 16);
+            static_cast<uint16_t*>(a.D)[i] = (uint16_t)bf16x2_bits(v, 0.0f);
+        }
+    }
+}
+
+// ---- the experts' products.  Up to this many rows an expert on average the
+// row kernel reads the weights faster (64 experts of 2 x 1408 x 4096, 6 rows:
+// 131 us against 144 on 64x128 tiles); above, the experts of many rows make it
+// read them again for every 16, and tiles win whatever the spread.
+constexpr int64_t FEW_ROWS_EXPERT = 6;
+static bool few_rows(const FusedArgs& a) { return a.m <= FEW_ROWS_EXPERT * a.experts; }
+
+// The tile of the rest, by the costs above: an expert of c rows has ceil(c / bm)
+// tile rows, on average c / bm + 1/2 but at least one.  256x256 tiles count a
+// tenth more, since ragged experts fill them less evenly, and 128x128 ones in mode
+// (b) 0.8 us a stage.  Measured, mode (a), 64x128 / 128x128 / 256x128 / 256x256 in us: 128 experts of
+// 2 x 1024 x 4096 with 32 rows 222 / 229 / 253 / 230, with 128 rows 375 / 308 / 327
+// / 276, with 512 rows 977 / 723 / 701 / 594; 60 of 2048 x 1408 with 273 rows
+// 127 / 98 / 99 / 105.
+static int moe_tile(const FusedArgs& a) {
+    if (const char* force = getenv("FP8G_FORCE")) if (atoi(force) > 1) return atoi(force);
+    const int64_t b_rows = a.gated ? 2 * a.n : a.n, nk = (a.k + BK - 1) / BK;
+    int best = 0;
+    double best_us = 0.0;
+    auto consider = [&](const TileCost& c) {
+        if (c.tile == 256 && a.k % BK) return;
+        double rows = (double)a.m / (double)a.experts / tile_bm(c.tile) + 0.5;      // of an expert
+        if (rows < 1.0) rows = 1.0;
+        const double tiles = rows * (double)a.experts * (double)((b_rows + tile_bn(c.tile) - 1) / tile_bn(c.tile));
+        const double rounds = (double)((int64_t)(tiles / PLAN_CUS) + 1);
+        const double stage = a.mx && c.tile == 128 ? 0.8 : c.stage;
+        const double us = rounds * (c.fixed + stage * (double)nk) * (c.tile == 256 ? 1.1 : 1.0);
+        if (!best || us < best_us) best = c.tile, best_us = us;
+    };
+    if (a.mx)
+        for (const TileCost& c : COST_B) consider(c);
+    else
+        for (const TileCost& c : COST_A) consider(c);
+    return best;
+}
 
 struct MoeSpace {
     int64_t tile_rows, row_at, scale, bytes;      // byte offsets behind the plan, which comes first
@@ -197,24 +379,46 @@ static MoeSpace moe_space(const FusedArgs& a) {
     return s;
 }
 
-int64_t moe_gemm_bytes(const FusedArgs& a) { return few_rows(a) ? 0 : moe_space(a).bytes; }
+int64_t moe_gemm_bytes(const FusedArgs& a) { return few_rows(a) && !getenv("FP8G_FORCE") ? 0 : moe_space(a).bytes; }
 
-hipError_t launch_gemm_fused(const FusedArgs& a, hipStream_t stream) {
-    if (few_rows(a)) return launch_gemm_rows(a, stream);
+static hipError_t launch_product(const FusedArgs& a, hipStream_t stream) {
+    FusedPlan p = fused_plan(a, PLAN_CUS);
+    if (p.tile <= 1) return launch_gemm_rows(a, stream);
     TileLaunch t = {};
     hipError_t e = hipGetDevice(&t.dev);
     if (e != hipSuccess) return e;
     e = hipDeviceGetAttribute(&t.cus, hipDeviceAttributeMultiprocessorCount, t.dev);
     if (e != hipSuccess) return e;
+    t.tile = p.tile == 256 && a.f32 ? TILE_256x128 : p.tile;
     t.scale_a = a.scale_a;
-    if (!a.expert_start) {
-        // the scaled products' choice, but 256x256 tiles only where they hold their
-        // registers: per-row scales, bf16 output, K in whole stages
-        t.tile = gemm_tile_of(a.m, a.gated ? 2 * a.n : a.n, a.k, a.mx, t.cus);
-        if (t.tile == 256 && (a.mx || a.f32 || a.k % BK)) t.tile = TILE_256x128;
-        return a.mx ? launch_fused<true, false>(a, t, stream) : launch_fused<false, false>(a, t, stream);
-    }
+    const int64_t tiles = ((a.m + tile_bm(p.tile) - 1) / tile_bm(p.tile)) *
+                          (((a.gated ? 2 * a.n : a.n) + tile_bn(p.tile) - 1) / tile_bn(p.tile));
+    if (p.ranges * tiles > t.cus) p.ranges = 1;      // a device of fewer CUs: an item a workgroup would not fit
+    if (p.ranges == 1) return a.mx ? launch_fused<true, false>(a, t, stream) : launch_fused<false, false>(a, t, stream);
+    const PartSpace s = part_space(a, p);
+    FusedArgs g = a;             // the plain product of all of B's rows
+    g.n = a.gated ? 2 * a.n : a.n, g.gated = 0, g.f32 = 1;
+    g.bias = nullptr, g.residual = nullptr, g.D = a.workspace;
+    t.ranges = p.ranges, t.pitch = (int32_t)s.pitch, t.part_rows = (int32_t)s.rows;
+    e = a.mx ? launch_fused_part<true, false, EPI_PARTIAL>(g, t, stream) : launch_fused_part<false, false, EPI_PARTIAL>(g, t, stream);
+    if (e != hipSuccess) return e;
+    const FinishArgs f = {a, act_of(a.act), s.pitch, s.rows * s.pitch, p.ranges};
+    fused_finish<<<dim3((unsigned)((a.n + 4 * FIN_THREADS - 1) / (4 * FIN_THREADS)), (unsigned)a.m), dim3(FIN_THREADS), 0, stream>>>(f);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemm_fused(const FusedArgs& a, hipStream_t stream) {
+    if (!a.expert_start) return launch_product(a, stream);
+    const char* force = getenv("FP8G_FORCE");
+    const int forced = force ? atoi(force) : 0;
+    if (forced ? forced == 1 : few_rows(a)) return launch_gemm_rows(a, stream);
+    TileLaunch t = {};
+    hipError_t e = hipGetDevice(&t.dev);
+    if (e != hipSuccess) return e;
+    e = hipDeviceGetAttribute(&t.cus, hipDeviceAttributeMultiprocessorCount, t.dev);
+    if (e != hipSuccess) return e;
     t.tile = moe_tile(a);
+    t.scale_a = a.scale_a;
     const MoeSpace s = moe_space(a);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     t.tile_rows = s.tile_rows;
@@ -228,6 +432,7 @@ hipError_t launch_gemm_fused(const FusedArgs& a, hipStream_t stream) {
         const_cast<int32_t*>(t.plan), const_cast<uint32_t*>(t.row_at), a.rows ? ws + s.scale : nullptr);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
+    if (t.tile == 256 && a.f32) t.tile = TILE_256x128;      // the same rows a tile
     return a.mx ? launch_fused<true, true>(a, t, stream) : launch_fused<false, true>(a, t, stream);
 }
 #endif  // FP8G_FUSED_PART == 0

@@ -32,7 +32,11 @@ typedef unsigned int v4u __attribute__((ext_vector_type(4)));
 typedef unsigned int v2u __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-constexpr int RW_WAVES = 8;
+#ifdef SWEEP
+constexpr int RW_WAVES = SWEEP_W;
+#else
+constexpr int RW_WAVES = 4;
+#endif
 constexpr int RW_THREADS = 64 * RW_WAVES;
 constexpr uint32_t RW_OOB = 0x80000000u;      // past any panel (panels are < 2^31 bytes)
 
@@ -46,19 +50,24 @@ struct RowsArgs {
     Act act;
 };
 
-// NB blocks of 16 of B's rows (gated: NB / 2 of the gate, then NB / 2 of the up
-// projection), MB blocks of 16 rows of A.
-template <bool MX, bool GATED, int NB, int MB, int AHEAD>
-__global__ __launch_bounds__(RW_THREADS, 4) void gemm_rows_kernel(RowsArgs args) {
+// B's rows of a workgroup: NB blocks of 16; gated: the first half of them the
+// gate's, the others the up projection's.  MB: blocks of 16 rows of A.  AHEAD:
+// steps in flight.  WPE: waves of a SIMD that the registers are to allow.
+template <bool MX, bool GATED, int NB, int MB, int AHEAD, int WPE>
+__global__ __launch_bounds__(RW_THREADS, WPE) void gemm_rows_kernel(RowsArgs args) {
     const FusedArgs& a = args.f;
-    constexpr int NO = GATED ? NB / 2 : NB;              // blocks of output columns
+    constexpr int H = GATED ? 2 : 1;                      // projections
+    constexpr int NO = NB / H;                            // blocks of one
+    constexpr int COLS = 16 * NO;                         // output columns
+    constexpr int UNITS = COLS / 4 * 16 * MB;             // threads that finish: four columns of a row each
+    static_assert(NB % H == 0 && UNITS <= RW_THREADS, "one unit a thread");
     __shared__ v4f red[RW_WAVES][NB * MB][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, g = lane >> 4;
     const int N = (int)a.n, K = (int)a.k, nblk = K / 32;
-    const int n0 = (int)blockIdx.x * NO * 16;            // first output column
-    const int64_t nrows = GATED ? 2 * (int64_t)N : N;    // B's rows
+    const int n0 = (int)blockIdx.x * COLS;                // first output column
+    const int64_t b_rows = GATED ? 2 * (int64_t)N : N;    // B's rows of a product
     const uint8_t* B = a.B;
     int64_t s0 = (int64_t)blockIdx.y * (16 * MB), s1 = a.m, step = (int64_t)gridDim.y * (16 * MB);
     int64_t b_row = 0;                                    // this product's first row of scale_b and bias
@@ -66,17 +75,18 @@ __global__ __launch_bounds__(RW_THREADS, 4) void gemm_rows_kernel(RowsArgs args)
         const int e = blockIdx.y, S = (int)a.m;
         s0 = min(max(a.expert_start[e], 0), S);
         s1 = min(max(a.expert_start[e + 1], (int)s0), S);
+        if (s0 == s1) return;
         step = 16 * MB;
-        b_row = e * nrows;
+        b_row = e * b_rows;
         B += b_row * K;
     }
     const int steps = (K + 127) / 128;
+    const bool gather = a.rows != nullptr;
 
-    // B: panel of the output columns' rows, one for the gate and one for the up projection
-    const int cols = min(NO * 16, N - n0);
-    __amdgpu_buffer_rsrc_t rsB[GATED ? 2 : 1], rsEB[GATED ? 2 : 1];
+    const int cols = min(COLS, N - n0);
+    __amdgpu_buffer_rsrc_t rsB[H], rsEB[H];
 #pragma unroll
-    for (int h = 0; h < (GATED ? 2 : 1); h++) {
+    for (int h = 0; h < H; h++) {
         const int64_t first = n0 + (int64_t)h * N;
         rsB[h] = rw_panel(B + first * K, (int64_t)cols * K);
         if constexpr (MX)
@@ -92,7 +102,6 @@ __global__ __launch_bounds__(RW_THREADS, 4) void gemm_rows_kernel(RowsArgs args)
     for (; s0 < s1; s0 += step) {
         const int count = (int)min((int64_t)(16 * MB), s1 - s0);
         // A: this chunk's rows, or with `rows` all of A
-        const bool gather = a.rows != nullptr;
         const __amdgpu_buffer_rsrc_t rsA = gather ? rw_panel(a.A, a.a_rows * K) : rw_panel(a.A + s0 * K, (int64_t)count * K);
         __amdgpu_buffer_rsrc_t rsEA;
         if constexpr (MX) {
@@ -140,10 +149,14 @@ __global__ __launch_bounds__(RW_THREADS, 4) void gemm_rows_kernel(RowsArgs args)
 #pragma unroll
             for (int j = 0; j < MB; j++) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
 
-        // steps past the last one load and add zeros
+        // Steps past the last one load and add zeros.  The barriers keep each step's
+        // loads behind the step before: reordered, the loop waited for all of them.
         Frag f[AHEAD];
 #pragma unroll
-        for (int u = 0; u < AHEAD; u++) load(wave + RW_WAVES * u, f[u]);
+        for (int u = 0; u < AHEAD; u++) {
+            load(wave + RW_WAVES * u, f[u]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
         for (int st = wave; st < steps; st += RW_WAVES * AHEAD) {
 #pragma unroll
             for (int u = 0; u < AHEAD; u++) {
@@ -158,42 +171,49 @@ __global__ __launch_bounds__(RW_THREADS, 4) void gemm_rows_kernel(RowsArgs args)
                             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f[u].b[i], f[u].a[j], acc[i][j], 0, 0, 0,
                                                                                          127, 0, 127);
                     }
+                __builtin_amdgcn_sched_barrier(0);
                 load(st + RW_WAVES * (u + AHEAD), f[u]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-#pragma unroll
-        for (int i = 0; i < NB; i++)
-#pragma unroll
-            for (int j = 0; j < MB; j++) red[wave][i * MB + j][lane] = acc[i][j];
-        __syncthreads();
 
-        // a thread: output columns n .. n + 3 of row m
-        for (int u = threadIdx.x; u < NO * MB * 64; u += RW_THREADS) {
-            const int block = u >> 6, i = block / MB, j = block % MB, ln = u & 63;
-            const int mr = 16 * j + (ln & 15), nc = 16 * i + 4 * (ln >> 4);
-            if (mr >= count || nc >= cols) continue;
-            const int n = n0 + nc, left = min(4, cols - nc);
-            const int64_t slot = s0 + mr;
-            float z[GATED ? 2 : 1][4];
+        // a thread's unit: output columns n .. n + 3 of row mr; its scales and bias are
+        // asked for before the sums meet
+        const int i = wave / MB, j = wave % MB, mr = 16 * j + l16, nc = 16 * i + 4 * g;
+        const bool mine = wave < NO * MB && mr < count && nc < cols;
+        const int n = n0 + nc, left = min(4, cols - nc);
+        const int64_t slot = s0 + mr;
+        float sm = 1.0f, sn[H][4], bs[H][4];
+        if (mine) {
+            if constexpr (!MX) {
+                int64_t r = slot;
+                if (gather) r = min(max(a.rows[slot], 0), (int)a.a_rows - 1);
+                sm = static_cast<const float*>(a.scale_a)[r];
+            }
 #pragma unroll
-            for (int h = 0; h < (GATED ? 2 : 1); h++) {
-                v4f t = red[0][(h * NO + i) * MB + j][ln];
-#pragma unroll
-                for (int w = 1; w < RW_WAVES; w++) t += red[w][(h * NO + i) * MB + j][ln];
-                float sm = 1.0f;
-                if constexpr (!MX) {
-                    int64_t r = slot;
-                    if (gather) r = min(max(a.rows[slot], 0), (int)a.a_rows - 1);
-                    sm = static_cast<const float*>(a.scale_a)[r];
-                }
+            for (int h = 0; h < H; h++)
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
                     const int64_t row = b_row + (int64_t)h * N + n + min(c, left - 1);
-                    float v = t[c];
-                    if constexpr (!MX) v = v * sm * static_cast<const float*>(a.scale_b)[row];
-                    if (a.bias) v += a.bias[row];
-                    z[h][c] = v;
+                    sn[h][c] = MX ? 1.0f : static_cast<const float*>(a.scale_b)[row];
+                    bs[h][c] = a.bias ? a.bias[row] : 0.0f;
                 }
+        }
+#pragma unroll
+        for (int x = 0; x < NB; x++)
+#pragma unroll
+            for (int y = 0; y < MB; y++) red[wave][x * MB + y][lane] = acc[x][y];
+        __syncthreads();
+        if (mine) {
+            float z[H][4];
+#pragma unroll
+            for (int h = 0; h < H; h++) {
+                const int from = (h * NO + i) * MB + j;
+                v4f t = red[0][from][lane];
+#pragma unroll
+                for (int w = 1; w < RW_WAVES; w++) t += red[w][from][lane];
+#pragma unroll
+                for (int c = 0; c < 4; c++) z[h][c] = (MX ? t[c] : t[c] * sm * sn[h][c]) + bs[h][c];
             }
             float v[4];
 #pragma unroll
@@ -219,28 +239,43 @@ __global__ __launch_bounds__(RW_THREADS, 4) void gemm_rows_kernel(RowsArgs args)
     }
 }
 
-template <bool MX, bool GATED, int MB>
-static hipError_t launch_rows(const FusedArgs& f, hipStream_t stream) {
-    constexpr int NB = 2, NO = GATED ? 1 : 2, AHEAD = MB == 1 ? 4 : 2;
-    const int64_t gx = (f.n + 16 * NO - 1) / (16 * NO);
+template <bool MX, bool GATED, int NB, int MB, int AHEAD, int WPE>
+static hipError_t launch_one_rows(const FusedArgs& f, hipStream_t stream) {
+    constexpr int COLS = GATED ? 8 * NB : 16 * NB;
+    const int64_t gx = (f.n + COLS - 1) / COLS;
     int64_t gy = f.expert_start ? f.experts : (f.m + 16 * MB - 1) / (16 * MB);
     if (gy > 65535) gy = 65535;
     RowsArgs args{f, act_of(f.act)};
-    gemm_rows_kernel<MX, GATED, NB, MB, AHEAD><<<dim3((unsigned)gx, (unsigned)gy), dim3(RW_THREADS), 0, stream>>>(args);
+    gemm_rows_kernel<MX, GATED, NB, MB, AHEAD, WPE><<<dim3((unsigned)gx, (unsigned)gy), dim3(RW_THREADS), 0, stream>>>(args);
     return hipGetLastError();
 }
 
-hipError_t launch_gemm_rows(const FusedArgs& f, hipStream_t stream) {
-    const int64_t rows = f.expert_start ? (f.m + f.experts - 1) / f.experts : f.m;   // of a product, on average
-    const int mb = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    auto go = [&](auto mx, auto gated) {
-        constexpr bool X = decltype(mx)::value, G = decltype(gated)::value;
-        return mb == 1 ? launch_rows<X, G, 1>(f, stream) : mb == 2 ? launch_rows<X, G, 2>(f, stream) : launch_rows<X, G, 4>(f, stream);
-    };
-    using T = std::true_type;
-    using F = std::false_type;
-    if (f.mx) return f.gated ? go(T{}, T{}) : go(T{}, F{});
-    return f.gated ? go(F{}, T{}) : go(F{}, F{});
+#ifdef SWEEP
+extern "C" hipError_t sweep(const FusedArgs* f, int mb, hipStream_t stream) {
+    return f->mx ? launch_one_rows<true, SWEEP_G, SWEEP_NB, SWEEP_MB, SWEEP_AHEAD, SWEEP_WPE>(*f, stream)
+                 : launch_one_rows<false, SWEEP_G, SWEEP_NB, SWEEP_MB, SWEEP_AHEAD, SWEEP_WPE>(*f, stream);
 }
+#else
+template <bool MX, bool GATED>
+static hipError_t launch_rows(const FusedArgs& f, hipStream_t stream) {
+    const int64_t rows = f.expert_start ? (f.m + f.experts - 1) / f.experts : f.m;   // of a product, on average
+    if constexpr (GATED) {
+        if (rows <= 16) return launch_one_rows<MX, true, 2, 1, 2, 4>(f, stream);
+        if (rows <= 32) return launch_one_rows<MX, true, 2, 2, 2, 2>(f, stream);
+        return launch_one_rows<MX, true, 2, 4, 2, 2>(f, stream);
+    } else {
+        if (rows > 32) return launch_one_rows<MX, false, 1, 4, 2, 2>(f, stream);
+        if (rows > 16) return launch_one_rows<MX, false, 1, 2, 4, 2>(f, stream);
+        const int64_t blocks = (f.n + 31) / 32 * (f.expert_start ? f.experts : 1);
+        if (blocks < 512) return launch_one_rows<MX, false, 1, 1, 4, 4>(f, stream);
+        return launch_one_rows<MX, false, 2, 1, 2, 4>(f, stream);
+    }
+}
+
+hipError_t launch_gemm_rows(const FusedArgs& f, hipStream_t stream) {
+    if (f.mx) return f.gated ? launch_rows<true, true>(f, stream) : launch_rows<true, false>(f, stream);
+    return f.gated ? launch_rows<false, true>(f, stream) : launch_rows<false, false>(f, stream);
+}
+#endif
 
 }  // namespace fp8g

@@ -252,7 +252,7 @@ __device__ __forceinline__ TileCoord tile_coord(int t, int tiles_m, int tiles_n)
 // ---------------------------------------------------------------- kernel
 
 // What a fused product (EPI > 0) and the experts' products (MOE) take beside the operands.
-constexpr int EPI_NONE = 0, EPI_LINEAR = 1, EPI_GATED = 2;
+constexpr int EPI_NONE = 0, EPI_LINEAR = 1, EPI_GATED = 2, EPI_PARTIAL = 3;
 struct TileExtra {
     const float* bias;          // [B's rows], or NULL
     const void* residual;       // as D, or NULL
@@ -263,6 +263,8 @@ struct TileExtra {
     const int32_t* plan;
     const uint32_t* row_at;
     uint32_t a_bytes;           // of all of A, where its rows are gathered
+    // EPI_PARTIAL: K ranges, and the partial sums' row pitch (elements) and size (rows)
+    int32_t ranges, pitch, part_rows;
 };
 
 // Words that no kernel of the launch writes, through the scalar cache.
@@ -279,6 +281,8 @@ __device__ __forceinline__ const_words const_at(const void* p) { return (const_w
 // the gated pair (EPI_GATED: B has 2 N rows, and a tile takes BN / 2 output
 // columns, so that a wave's first blocks of B's rows hold the gate and its last
 // ones the up projection of the same columns, which thus meet in one lane).
+// EPI_PARTIAL: K in ex.ranges ranges, one work item each and at most one item a
+// workgroup; D takes their unscaled sums, one after the other, in whole tiles.
 // MOE: B, its scales and the bias by expert, tile rows from a plan on the device.
 template <bool MX, bool OUT_F32, bool KTAIL, int FA, int FB, int TILE, bool SPLIT, int EPI, bool MOE>
 __device__ __forceinline__ void gemm_tiles(
@@ -288,7 +292,8 @@ __device__ __forceinline__ void gemm_tiles(
     int* __restrict__ cnt, const TileExtra& ex) {
     static_assert(!SPLIT || (!MX && !KTAIL && TILE == 128), "K splits: mode (a), whole stages, 128x128 tiles");
     static_assert(!SPLIT || EPI == EPI_NONE, "no K splits of fused products");
-    constexpr bool GATED = EPI == EPI_GATED;
+    constexpr bool GATED = EPI == EPI_GATED, PARTIAL = EPI == EPI_PARTIAL;
+    static_assert(!PARTIAL || (OUT_F32 && Ring<MX, KTAIL, TILE>::OWN_STAGE), "partial sums: fp32, staging of their own");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     using GEO = Geo<TILE>;
     constexpr int BM = GEO::BM, BN = GEO::BN, WTM = GEO::WTM, WTN = GEO::WTN, NBM = GEO::NBM, NBN = GEO::NBN;
@@ -303,7 +308,7 @@ __device__ __forceinline__ void gemm_tiles(
     const int l32 = lane & 31, lhi = lane >> 5;
 
     const int tiles_m = MOE ? const_at(ex.plan)[0] : (M + BM - 1) / BM, tiles_n = (N + BNO - 1) / BNO;
-    const int total = tiles_m * tiles_n;
+    const int tiles = tiles_m * tiles_n, total = PARTIAL ? tiles * ex.ranges : tiles;
     const int nk = (K + BK - 1) / BK;            // stages per tile
     const int nblk = K / 32;                     // MX scale bytes per row
 
@@ -328,7 +333,15 @@ __device__ __forceinline__ void gemm_tiles(
     }
     const int my_tiles = my_whole + (my_split >= 0 ? 1 : 0);          // work items
     const int nks = SPLIT ? nk / split : nk;                           // stages of a split item
-    const int NS = my_whole * nk + (my_split >= 0 ? nks : 0);          // stages in this workgroup's stream
+    // item t of EPI_PARTIAL: tile t % tiles, K range t / tiles; in mode (b) a range
+    // starts at a whole scale group
+    auto range_start = [&](int r) __attribute__((always_inline)) {
+        const int at = (int)((int64_t)nk * r / ex.ranges);
+        return MX && r < ex.ranges ? at & ~3 : at;
+    };
+    // stages in this workgroup's stream
+    const int NS = PARTIAL ? (my_whole ? range_start((run0 + slot) / tiles + 1) - range_start((run0 + slot) / tiles) : 0)
+                           : my_whole * nk + (my_split >= 0 ? nks : 0);
     // item j: its tile, first stage (kb) and stages (ns)
     struct Item {
         TileCoord tc;
@@ -336,7 +349,12 @@ __device__ __forceinline__ void gemm_tiles(
     };
     auto item_of = [&](int j) __attribute__((always_inline)) -> Item {
         Item it;
-        if (!SPLIT || j < my_whole) {
+        if constexpr (PARTIAL) {
+            const int t = run0 + slot + j * wx, r = t / tiles;
+            it.tc = tile_coord(t - r * tiles, tiles_m, tiles_n);
+            it.kb = range_start(r);
+            it.ns = range_start(r + 1) - it.kb;
+        } else if (!SPLIT || j < my_whole) {
             it.tc = tile_coord(run0 + slot + j * wx, tiles_m, tiles_n);
             it.kb = 0;
             it.ns = nk;
@@ -488,6 +506,7 @@ __device__ __forceinline__ void gemm_tiles(
     // load q (0 .. SC_LOADS-1) of group gi (of the tile of rsEA, rsEB) into buffer ub
     auto sc_load = [&](int q, int gi, int ub) __attribute__((always_inline)) {
         if constexpr (R::SCALES) {
+            if constexpr (PARTIAL) gi += item_of(0).kb / R::SC_GROUP;
             if constexpr (R::SC_A == R::SC_B) {
                 constexpr int PER_OP = SC_LOADS / 2;
                 const int o = q / PER_OP, p = wave + 4 * (q % PER_OP);
@@ -580,7 +599,8 @@ __device__ __forceinline__ void gemm_tiles(
                 const __amdgpu_buffer_rsrc_t pb = panel(eb_e + (int64_t)p.n0 * nblk, cols * (uint32_t)nblk);
                 __amdgpu_buffer_rsrc_t pu = pb;
                 if constexpr (GATED) pu = panel(eb_e + (int64_t)(N + p.n0) * nblk, cols * (uint32_t)nblk);
-                const int kb = 4 * s + 2 * h + lhi;   // this lane half's block
+                // this lane half's block
+                const int kb = 4 * s + 2 * h + lhi + (PARTIAL ? 4 * item_of(0).kb : 0);
                 const bool in = kb < nblk;
                 const uint32_t kc = (uint32_t)min(kb, nblk - 1);
 #pragma unroll
@@ -1128,6 +1148,42 @@ __device__ __forceinline__ void gemm_tiles(
             }
         });
     };
+    // ---- partial sums (EPI_PARTIAL): the item's accumulators as they are, whole
+    // tiles of rows of ex.pitch elements, through LDS as in epilogue_staged_f32
+    auto partial_staged = [&](int j, v16f (&acc)[NBN][NBM]) __attribute__((always_inline)) {
+        const int t = run0 + slot + j * wx, range = t / tiles;
+        const TileCoord tc = tile_of(j);
+        const uint32_t pitch = (uint32_t)ex.pitch;
+        const __amdgpu_buffer_rsrc_t rsD = panel(
+            reinterpret_cast<uint8_t*>(Dv) + (((int64_t)range * ex.part_rows + tc.tm * BM) * pitch + tc.tn * BN) * 4,
+            ((uint32_t)(BM - 1) * pitch + BN) * 4u);
+        const int lane_e = fresh_lane();
+        const int l32e = lane_e & 31, lhie = lane_e >> 5;
+        uint8_t* st = smem + R::STAGE_AREA + wave * 4096;
+        const uint32_t wkey = (uint32_t)((l32e >> 1) & 7);
+        const uint32_t rc = (uint32_t)(lane_e & 7);
+        const int rr = lane_e >> 3;
+        const uint32_t rd_off = (uint32_t)(rr * 128) + ((rc ^ (uint32_t)((rr >> 1) & 3)) << 4);
+#pragma unroll
+        for (int i = 0; i < NBN; ++i)
+#pragma unroll
+            for (int jb = 0; jb < NBM; ++jb) {
+#pragma unroll
+                for (int gq = 0; gq < 4; ++gq) {
+                    const uint32_t pc = (uint32_t)(2 * gq + lhie) ^ wkey;
+                    *reinterpret_cast<v4f*>(st + l32e * 128 + pc * 16) =
+                        (v4f){acc[i][jb][4 * gq], acc[i][jb][4 * gq + 1], acc[i][jb][4 * gq + 2], acc[i][jb][4 * gq + 3]};
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const v4u d = *reinterpret_cast<const v4u*>(st + k * 1024 + (rd_off ^ (uint32_t)(64 * (k & 1))));
+                    const uint32_t mr = (uint32_t)(wm * WTM + jb * 32 + 8 * k + rr);   // row inside the tile
+                    const uint32_t col = (uint32_t)(wn * WTN + 32 * i) + 4u * rc;
+                    __builtin_amdgcn_raw_buffer_store_b128(d, rsD, (mr * pitch + col) * 4u, 0, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    };
     // Staged epilogues: bf16 for N % 8 == 0; fp32 in mode (a) for N % 32 == 0,
     // rows of whole 128-byte lines (at N = 22012, rows straddling lines, staged
     // fp32 ran 4% slower than from registers; mode (b) with fp32 output staged
@@ -1348,7 +1404,7 @@ __device__ __forceinline__ void gemm_tiles(
             // next tile's first step; load the tile's scales into it for the
             // epilogue (before this step's item loads, so that waiting for all
             // but those leaves the scales landed)
-            if constexpr (!MX && LAST) {
+            if constexpr (!MX && LAST && !PARTIAL) {
                 tile_scales_to_lds(j, R::OWN_STAGE ? (uint32_t)R::STAGE_AREA : slot_off(slot_add(rslot, 1)));
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -1425,7 +1481,7 @@ __device__ __forceinline__ void gemm_tiles(
         for (int i = 0; i < NBN; ++i)
 #pragma unroll
             for (int jb = 0; jb < NBM; ++jb) acc[i][jb] = (v16f){};
-        const int nsj = SPLIT ? item_of(j).ns : nk;   // stages of this work item
+        const int nsj = SPLIT || PARTIAL ? item_of(j).ns : nk;   // stages of this work item
         for (int s = 0; s < nsj - 1; ++s) {
             kstep(acc, j, s, Step0{}, NotLast{}, fa0, fb0, fa1, fb1);
             kstep(acc, j, s, Step1{}, NotLast{}, fa1, fb1, fa0, fb0);
@@ -1440,7 +1496,9 @@ __device__ __forceinline__ void gemm_tiles(
             // up the tile has no epilogue and nothing after it
             if (j == my_whole && !split_reduce(acc, stage_off)) break;
         }
-        if (staged) {
+        if constexpr (PARTIAL) {
+            partial_staged(j, acc);
+        } else if (staged) {
             if constexpr (!MX) wait_vmcnt<LI_LAST>();   // the tile's scales (only the last item's loads may be in flight)
             __syncthreads();
             epilogue_staged_any(j, acc, stage_off);

@@ -31,6 +31,7 @@ struct FusedArgs {
     int64_t m, n, k, a_rows, experts;    // m: rows of D; n: columns of D
     int32_t act, gated, mx, f32;
 };
+int64_t gemm_fused_bytes(const FusedArgs& a);
 int64_t moe_gemm_bytes(const FusedArgs& a);
 hipError_t launch_gemm_fused(const FusedArgs& a, hipStream_t stream);
 hipError_t launch_gemm_rows(const FusedArgs& a, hipStream_t stream);      // few rows, no workspace
@@ -42,10 +43,8 @@ struct TileLaunch {
     const int32_t* plan;
     const uint32_t* row_at;
     const void* scale_a;
+    int32_t ranges, pitch, part_rows;    // K ranges' partial sums
 };
-// The tile that the scaled product of these sizes takes (gemm.hip), without K splits.
-int gemm_tile_of(int64_t m, int64_t n, int64_t k, int mx, int cus);
-
 struct RouteArgs {
     const void* logits;
     const float* bias;

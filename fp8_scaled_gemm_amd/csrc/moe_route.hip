@@ -3,282 +3,460 @@
 //   p = softmax or sigmoid of the logits, choice = p + bias; groups by the sum
 //   of their largest choices; the top_k of the kept groups' experts
 //
-// A wave scores a token: lane L holds the experts L, L + 64, ...  Scores and sums
-// are fp64, so that two experts change places only where their choices agree to
-// 2^-50 or so: an fp32 choice would hang on the order of a sum and on the
-// exponential at hand.  Each of the top_k rounds takes the wave's largest
-// choice, and among equals the lowest expert.
+// A wave scores a token: lane L holds the experts L VPL .. L VPL + VPL - 1, and
+// each of the top_k rounds takes the wave's largest choice, among equals the
+// lowest expert.  Choices are defined in fp64, so that the ids do not hang on
+// the rounding of an exponential or a sum.  They are looked at in fp32 first: the
+// logits themselves are exact there, and where a choice is p + bias, or groups
+// are compared, every decision of the token is checked to be wider than the fp32
+// error (RT_MARGIN); a token with a closer one (about one in a thousand) is gone
+// through again in fp64.  Weights always come from fp64.
 //
-// The rows are sorted by counting, stably and without order-dependent atomics:
-// a workgroup counts the experts of its run of tokens (integer additions in
-// LDS); the counts are summed over the workgroups, expert by expert; and each
-// workgroup then places its tokens' rows behind those of the workgroups before
-// it, a row's rank within the run being the number of rows of the same expert
-// ahead of it.
+// Bound by the vector instructions of a token (some 400, most of them in the
+// rounds), not by its bytes; a run of 64 tokens has 16 waves, four on a SIMD.
+//
+// The rows are sorted by counting, stably and with no result that hangs on an
+// order: a run of at most 64 tokens sets bit t of its experts' 64-bit masks in
+// LDS for its token t, so a mask's bits are the run's rows of the expert, in
+// order, and a row's rank is the number of bits below its own.  The runs' counts
+// are summed expert by expert, and each run places its rows behind those of the
+// runs before it.  Up to RT_SMALL tokens one workgroup does all of it in one launch.
 
 #include "launch_ffn.h"
 #include "rows16.h"
 
 namespace fp8g {
 
-constexpr int RT_THREADS = 256, RT_WAVES = RT_THREADS / 64;
+constexpr int RT_WAVES = 16, RT_THREADS = 64 * RT_WAVES;
+constexpr int RT_PLACE = 256;            // threads that place a run's rows
 constexpr int RT_MAX_EXPERTS = 1024;
-constexpr int RT_ENTRIES = 512;          // routed rows of a workgroup's run, at most
+constexpr int RT_RUN = 64;               // tokens of a run, at most: bits of a mask
+constexpr int RT_SMALL = 64;
+// fp32 choices: p from the hardware's exponential and reciprocal (one ulp each, the
+// argument's rounding times an exponent of at most 88 p) and a sum of 1024
+// terms is within 2^-20 of p's range [0, 1]; the bias adds half an ulp of the
+// choice, a group's sum twice all of that.
+constexpr float RT_MARGIN = 1.0f / (1 << 18);
 
-struct RoutePlan {
-    int chunk, blocks;                   // tokens of a run, runs
-};
-static RoutePlan route_plan(const RouteArgs& a) {
-    RoutePlan p;
-    p.chunk = RT_WAVES;
-    while (p.chunk < 64 && (int64_t)p.chunk * 256 < a.tokens && 2 * p.chunk * a.top_k <= RT_ENTRIES) p.chunk *= 2;
-    p.blocks = (a.tokens + p.chunk - 1) / p.chunk;
-    return p;
+// All lanes' combination, in every lane: over rows of 16, then over the four rows.
+template <int CTRL>
+__device__ __forceinline__ float dpp_from(float v, float other) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, other), __builtin_bit_cast(int, v),
+                                                                 CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_from(double v, double other) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v), o = __builtin_bit_cast(uint64_t, other);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)o, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)(o >> 32), (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ float lane63(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+__device__ __forceinline__ double lane63(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+template <class R, class F>
+__device__ __forceinline__ R over_wave(R v, R neutral, F f) {
+    v = f(v, dpp_from<0x111>(v, neutral));      // row_shr:1, 2, 4, 8
+    v = f(v, dpp_from<0x112>(v, neutral));
+    v = f(v, dpp_from<0x114>(v, neutral));
+    v = f(v, dpp_from<0x118>(v, neutral));
+    v = f(v, dpp_from<0x142>(v, neutral));      // row_bcast:15, 31
+    v = f(v, dpp_from<0x143>(v, neutral));
+    return lane63(v);
+}
+__device__ __forceinline__ float larger(float u, float v) { return __builtin_fmaxf(u, v); }
+__device__ __forceinline__ double larger(double u, double v) { return __builtin_fmax(u, v); }
+template <class R>
+__device__ __forceinline__ R wave_most(R v) {
+    return over_wave(v, -(R)__builtin_inff(), [](R a, R b) { return larger(a, b); });
+}
+template <class R>
+__device__ __forceinline__ R wave_total(R v) {
+    return over_wave(v, (R)0, [](R a, R b) { return a + b; });
 }
 
-__device__ __forceinline__ double wave_max_f64(double v) {
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ double exp_of(double x) { return exp(x); }
+__device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
+
+// The token's experts: in lane j < top_k the j-th, or -1.  False: two of them, or
+// two groups, are too close for R = float to tell.
+template <class R, int VPL>
+__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL], int& id) {
+    const int lane = threadIdx.x & 63, E = a.experts;
+    const R NEG = -(R)__builtin_inff();
+    const bool exact = sizeof(R) == 8;
+    R p[VPL], key[VPL];                                   // NEG: not available
+    const bool scored = a.bias != nullptr || a.groups > 1;
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v = __builtin_fmax(v, __shfl_xor(v, off, 64));
-    return v;
+    for (int i = 0; i < VPL; i++) {
+        key[i] = x[i] > -__builtin_inff() ? (R)x[i] + (R)0 : NEG;      // NaN: not there; -0 as +0
+        p[i] = (R)0;
+    }
+    if (scored) {
+        if (a.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < VPL; i++) p[i] = inverse((R)1 + exp_of(-key[i]));
+        } else {
+            R most = NEG, sum = (R)0;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) most = larger(most, key[i]);
+            most = wave_most(most);
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                // the largest itself without a difference, which is NaN between infinities
+                p[i] = key[i] == NEG ? (R)0 : key[i] == most ? (R)1 : exp_of(key[i] - most);
+                sum += p[i];
+            }
+            sum = wave_total(sum);
+            const R part = sum > (R)0 ? (R)1 / sum : (R)0;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) p[i] = exact ? (sum > (R)0 ? p[i] / sum : (R)0) : p[i] * part;
+        }
+    }
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < VPL; i++) {
+            const int e = lane * VPL + i;
+            const R c = e < E ? p[i] + (R)a.bias[e] : NEG;
+            key[i] = key[i] > NEG && c > NEG ? c : NEG;   // a bias of -inf or NaN: not there
+        }
+    }
+    bool clear = true;                                    // every decision so far is wider than the error
+    if (a.groups > 1) {
+        const int width = E / a.groups, lanes = width / VPL;
+        R mine = NEG;                                     // lane q: group q's value
+        if (width % VPL == 0 && (lanes & (lanes - 1)) == 0) {
+            // a group is `lanes` neighbouring lanes: all groups at once
+            R top = NEG, second = NEG;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                const R v = key[i] > NEG ? (a.bias ? key[i] : p[i]) : NEG;
+                second = larger(second, v < top ? v : top);
+                top = larger(top, v);
+            }
+            for (int off = 1; off < lanes; off <<= 1) {
+                const R t = __shfl_xor(top, off, 64), u = __shfl_xor(second, off, 64);
+                second = larger(larger(second, u), t < top ? t : top);
+                top = larger(top, t);
+            }
+            const R value = a.group_top == 2 ? top + second : top;
+            mine = __shfl(value, lane * lanes & 63, 64);
+            if (lane >= a.groups) mine = NEG;
+        } else {
+            for (int q = 0; q < a.groups; q++) {
+                R top = NEG, v[VPL];
+#pragma unroll
+                for (int i = 0; i < VPL; i++) {
+                    const int e = lane * VPL + i;
+                    v[i] = key[i] > NEG && e / width == q ? (a.bias ? key[i] : p[i]) : NEG;
+                    top = larger(top, v[i]);
+                }
+                const R best = wave_most(top);
+                R value = best;
+                if (a.group_top == 2) {
+                    // one of the largest taken out: the lowest lane's first
+                    const uint64_t b = __ballot(top == best);
+                    bool gone = lane != __builtin_ctzll(b);
+                    R second = NEG;
+#pragma unroll
+                    for (int i = 0; i < VPL; i++) {
+                        const bool out = !gone && v[i] == best;
+                        second = larger(second, out ? NEG : v[i]);
+                        gone = gone || out;
+                    }
+                    value = best + wave_most(second);
+                }
+                if (lane == q) mine = value;
+            }
+        }
+        int rank = 0;
+        for (int q = 0; q < a.groups; q++) {
+            const R other = __shfl(mine, q, 64);
+            rank += other > mine || (other == mine && q < lane) ? 1 : 0;
+        }
+        const bool in = lane < a.groups && rank < a.top_groups;
+        const uint64_t kept = __ballot(in);
+        if (!exact && a.top_groups < a.groups) {
+            const R last = -wave_most(in ? -mine : NEG), next = wave_most(lane < a.groups && !in ? mine : NEG);
+            // groups without enough experts (NEG) are behind all others for sure
+            clear = next == NEG || last - next > (R)RT_MARGIN * ((R)1 + larger(last, -last));
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; i++) {
+            const int e = lane * VPL + i;
+            if (e >= E || !((kept >> (e / width)) & 1)) key[i] = NEG;
+        }
+    }
+    id = -1;
+    R before = (R)__builtin_inff();
+    const int rounds = !exact && a.bias ? a.top_k + 1 : a.top_k;       // one more: the gap behind the last
+    for (int j = 0; j < rounds; j++) {
+        R own = key[0];
+#pragma unroll
+        for (int i = 1; i < VPL; i++) own = larger(own, key[i]);
+        const R top = wave_most(own);
+        if (!(top > NEG)) break;
+        if (!exact && a.bias) {
+            clear = clear && before - top > (R)RT_MARGIN * ((R)1 + larger(top, -top));
+            before = top;
+        }
+        const int from = __builtin_ctzll(__ballot(own == top));
+        int at = 0;
+        bool gone = lane != from;
+#pragma unroll
+        for (int i = 0; i < VPL; i++) {
+            const bool out = !gone && key[i] == top;
+            if (out) key[i] = NEG, at = i;
+            gone = gone || out;
+        }
+        at = __builtin_amdgcn_readlane(at, from);
+        if (lane == j && j < a.top_k) id = from * VPL + at;
+    }
+    return clear;
 }
-__device__ __forceinline__ double wave_sum_f64(double v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-    return v;
+
+template <bool F32>
+__device__ __forceinline__ float logit_at(const RouteArgs& a, int64_t i) {
+    if constexpr (F32) return static_cast<const float*>(a.logits)[i];
+    else return __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(a.logits)[i] << 16);
 }
 
 // The token's experts and weights: in lane j < top_k the j-th.
 template <bool F32, int VPL>
 __device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int& id, float& weight) {
     const int lane = threadIdx.x & 63, E = a.experts;
-    const double NEG = -__builtin_inf();
-    double p[VPL], key[VPL];
-    bool there[VPL];
-    double most = NEG;
+    float x[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; i++) {
-        const int e = lane + 64 * i;
-        float x = -__builtin_inff();
-        if (e < E) {
-            if constexpr (F32) x = static_cast<const float*>(a.logits)[t * E + e];
-            else x = __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(a.logits)[t * E + e] << 16);
-        }
-        there[i] = x > -__builtin_inff();                 // NaN: not there
-        key[i] = there[i] ? (double)x + 0.0 : NEG;        // -0 as +0
-        most = __builtin_fmax(most, key[i]);
+        const int e = lane * VPL + i;
+        x[i] = e < E ? logit_at<F32>(a, t * E + e) : -__builtin_inff();
     }
+    if (!choose<float, VPL>(a, x, id)) choose<double, VPL>(a, x, id);
+    // weights: lane j's own logit
+    const double NEG = -__builtin_inf();
+    const double own = id >= 0 ? (double)logit_at<F32>(a, t * E + id) : NEG;
+    double share;
     if (a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < VPL; i++) p[i] = there[i] ? 1.0 / (1.0 + exp(-key[i])) : 0.0;
+        share = id >= 0 ? 1.0 / (1.0 + exp(-own)) : 0.0;
     } else {
-        most = wave_max_f64(most);
-        double sum = 0.0;
+        double most = own;
+        if (!a.renormalize) {
 #pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            // the largest itself without a difference, which is NaN between infinities
-            p[i] = there[i] ? (key[i] == most ? 1.0 : exp(key[i] - most)) : 0.0;
-            sum += p[i];
+            for (int i = 0; i < VPL; i++) most = larger(most, x[i] > -__builtin_inff() ? (double)x[i] : NEG);
         }
-        sum = wave_sum_f64(sum);
+        most = wave_most(most);
+        share = id < 0 ? 0.0 : own == most ? 1.0 : exp(own - most);
+        if (!a.renormalize) {
+            double sum = 0.0;
 #pragma unroll
-        for (int i = 0; i < VPL; i++) p[i] = sum > 0.0 ? p[i] / sum : 0.0;
-    }
-    if (a.bias) {
-#pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            const int e = lane + 64 * i;
-            if (there[i]) key[i] = p[i] + (double)a.bias[e];
-            there[i] = there[i] && key[i] > NEG;          // a bias of -inf or NaN: not there
+            for (int i = 0; i < VPL; i++)
+                if (x[i] > -__builtin_inff()) sum += (double)x[i] == most ? 1.0 : exp((double)x[i] - most);
+            sum = wave_total(sum);
+            share = sum > 0.0 ? share / sum : 0.0;
         }
-    }
-    if (a.groups > 1) {
-        const int width = E / a.groups;
-        double mine = NEG;                                // lane q: group q's value
-        for (int q = 0; q < a.groups; q++) {
-            double top = NEG, v[VPL];
-#pragma unroll
-            for (int i = 0; i < VPL; i++) {
-                const int e = lane + 64 * i;
-                v[i] = there[i] && e / width == q ? (a.bias ? key[i] : p[i]) : NEG;
-                top = __builtin_fmax(top, v[i]);
-            }
-            top = wave_max_f64(top);
-            double value = top;
-            if (a.group_top == 2) {
-                bool gone = false;                        // one of the largest taken out
-                double second = NEG;
-#pragma unroll
-                for (int i = 0; i < VPL; i++) {
-                    const uint64_t b = __ballot(v[i] == top);
-                    if (!gone && b) {
-                        if (lane == __builtin_ctzll(b)) v[i] = NEG;
-                        gone = true;
-                    }
-                    second = __builtin_fmax(second, v[i]);
-                }
-                value = top + wave_max_f64(second);
-            }
-            if (lane == q) mine = value;
-        }
-        int rank = 0;
-        for (int q = 0; q < a.groups; q++) {
-            const double other = __shfl(mine, q, 64);
-            rank += other > mine || (other == mine && q < lane) ? 1 : 0;
-        }
-        const uint64_t kept = __ballot(lane < a.groups && rank < a.top_groups);
-#pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            const int e = lane + 64 * i;
-            there[i] = there[i] && ((kept >> (e / width)) & 1);
-        }
-    }
-    id = -1;
-    double share = 0.0;
-    for (int j = 0; j < a.top_k; j++) {
-        double top = NEG;
-#pragma unroll
-        for (int i = 0; i < VPL; i++) top = __builtin_fmax(top, there[i] ? key[i] : NEG);
-        top = wave_max_f64(top);
-        bool found = false;
-#pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            const uint64_t b = __ballot(there[i] && key[i] == top);
-            if (!found && b) {
-                const int from = __builtin_ctzll(b);
-                const double w = __shfl(p[i], from, 64);
-                if (lane == j) id = from + 64 * i, share = w;
-                if (lane == from) there[i] = false;
-                found = true;
-            }
-        }
-        if (!found) break;
     }
     if (a.renormalize) {
-        const double sum = wave_sum_f64(share);
+        const double sum = wave_total(share);
         share = sum > 0.0 ? share / sum : 0.0;
     }
     weight = (float)(share * (double)a.scale);
 }
 
+// Bit t of the masks of the token's experts, and its results.
+__device__ __forceinline__ void note(const RouteArgs& a, int64_t token, int t, int id, float weight, unsigned long long* mask) {
+    const int lane = threadIdx.x & 63;
+    if (lane < a.top_k) {
+        a.ids[token * a.top_k + lane] = id;
+        a.weights[token * a.top_k + lane] = weight;
+        if (id >= 0) atomicOr(&mask[id], 1ull << t);
+    }
+}
+
+// Sums over the threads before, of `threads` threads; part: one word a thread.
+template <int THREADS>
+__device__ __forceinline__ int before_threads(int own, int* part, int& total) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    int sum = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(sum, off, 64);
+        if (lane >= off) sum += v;
+    }
+    if (lane == 63) part[wave] = sum;
+    __syncthreads();
+    int ahead = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; w++) {
+        if (w < wave) ahead += part[w];
+        total += part[w];
+    }
+    return ahead + sum - own;
+}
+
+// A run's row i (of token i / top_k) to its slot; base: the experts' first slots for this run.
+__device__ __forceinline__ void place(const RouteArgs& a, int64_t first, int i, int id, const int* base,
+                                      const unsigned long long* mask, int total) {
+    int slot = -1;
+    if (id >= 0) {
+        const int t = i / a.top_k;
+        slot = base[id] + __popcll(mask[id] & ((1ull << t) - 1));
+        a.rows[slot] = (int)((first + i) / a.top_k);
+    }
+    a.slots[first + i] = slot;
+    if (first + i >= total) a.rows[first + i] = -1;       // behind the last expert's
+}
+
 // Experts and weights of a run of tokens, and how many rows each expert gets of it.
 template <bool F32, int VPL>
-__global__ __launch_bounds__(RT_THREADS) void route_tokens(RouteArgs a, int chunk) {
-    __shared__ int count[RT_MAX_EXPERTS];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int e = tid; e < a.experts; e += RT_THREADS) count[e] = 0;
+__global__ __launch_bounds__(RT_THREADS) void route_tokens(RouteArgs a, int run) {
+    __shared__ unsigned long long mask[RT_MAX_EXPERTS];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    for (int e = tid; e < a.experts; e += RT_THREADS) mask[e] = 0;
     __syncthreads();
-    const int64_t first = (int64_t)blockIdx.x * chunk;
-    for (int u = wave; u < chunk && first + u < a.tokens; u += RT_WAVES) {
-        const int64_t t = first + u;
+    const int64_t first = (int64_t)blockIdx.x * run;
+    for (int u = wave; u < run && first + u < a.tokens; u += RT_WAVES) {
         int id;
         float w;
-        route_token<F32, VPL>(a, t, id, w);
-        if (lane < a.top_k) {
-            a.ids[t * a.top_k + lane] = id;
-            a.weights[t * a.top_k + lane] = w;
-            if (id >= 0) atomicAdd(&count[id], 1);
-        }
+        route_token<F32, VPL>(a, first + u, id, w);
+        note(a, first + u, u, id, w, mask);
     }
     __syncthreads();
-    for (int e = tid; e < a.experts; e += RT_THREADS) a.workspace[(int64_t)blockIdx.x * a.experts + e] = count[e];
+    for (int e = tid; e < a.experts; e += RT_THREADS) a.workspace[(int64_t)blockIdx.x * a.experts + e] = __popcll(mask[e]);
 }
 
 // Counts of each run -> rows of the runs before it, expert by expert, and the totals.
-__global__ __launch_bounds__(RT_THREADS) void route_counts(RouteArgs a, int blocks) {
-    const int lane = threadIdx.x & 63, e = (int)blockIdx.x * RT_WAVES + (threadIdx.x >> 6);
+__global__ __launch_bounds__(RT_PLACE) void route_counts(RouteArgs a, int runs) {
+    const int lane = threadIdx.x & 63, e = (int)blockIdx.x * (RT_PLACE / 64) + (threadIdx.x >> 6);
     if (e >= a.experts) return;
     int before = 0;
-    for (int b0 = 0; b0 < blocks; b0 += 64) {
+    for (int b0 = 0; b0 < runs; b0 += 64) {
         const int b = b0 + lane;
-        const int own = b < blocks ? a.workspace[(int64_t)b * a.experts + e] : 0;
+        const int own = b < runs ? a.workspace[(int64_t)b * a.experts + e] : 0;
         int sum = own;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
             const int v = __shfl_up(sum, off, 64);
             if (lane >= off) sum += v;
         }
-        if (b < blocks) a.workspace[(int64_t)b * a.experts + e] = before + sum - own;
+        if (b < runs) a.workspace[(int64_t)b * a.experts + e] = before + sum - own;
         before += __shfl(sum, 63, 64);
     }
-    if (lane == 0) a.workspace[(int64_t)blocks * a.experts + e] = before;
+    if (lane == 0) a.workspace[(int64_t)runs * a.experts + e] = before;
 }
 
 // A run's rows to their slots.
-__global__ __launch_bounds__(RT_THREADS) void route_place(RouteArgs a, int chunk, int blocks) {
-    __shared__ int base[RT_MAX_EXPERTS + 1];              // an expert's first slot, then this run's
-    __shared__ int part[RT_THREADS];
-    __shared__ int ids[RT_ENTRIES];
+__global__ __launch_bounds__(RT_PLACE) void route_place(RouteArgs a, int run, int runs) {
+    __shared__ int base[RT_MAX_EXPERTS];                  // an expert's first slot for this run
+    __shared__ int part[RT_PLACE / 64];
+    __shared__ unsigned long long mask[RT_MAX_EXPERTS];
     const int tid = threadIdx.x, E = a.experts;
-    constexpr int PER = RT_MAX_EXPERTS / RT_THREADS;
+    constexpr int PER = RT_MAX_EXPERTS / RT_PLACE;
     int own[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; i++) {
         const int e = tid * PER + i;
-        own[i] = e < E ? a.workspace[(int64_t)blocks * E + e] : 0;
+        own[i] = e < E ? a.workspace[(int64_t)runs * E + e] : 0;
         sum += own[i];
+        if (e < E) mask[e] = 0;
     }
-    part[tid] = sum;
-    __syncthreads();
-    for (int off = 1; off < RT_THREADS; off <<= 1) {
-        const int v = tid >= off ? part[tid - off] : 0;
-        __syncthreads();
-        part[tid] += v;
-        __syncthreads();
-    }
-    int at = part[tid] - sum;
+    int total;
+    int at = before_threads<RT_PLACE>(sum, part, total);
 #pragma unroll
     for (int i = 0; i < PER; i++) {
         const int e = tid * PER + i;
         if (e < E) {
-            base[e] = at;
+            base[e] = at + a.workspace[(int64_t)blockIdx.x * E + e];
             if (blockIdx.x == 0) a.expert_start[e] = at;
         }
         at += own[i];
     }
-    const int total = part[RT_THREADS - 1];
     if (blockIdx.x == 0 && tid == 0) a.expert_start[E] = total;
-    if (blocks == 0) return;                              // no token at all
-    const int64_t first = (int64_t)blockIdx.x * chunk * a.top_k;
-    const int entries = (int)min((int64_t)chunk * a.top_k, (int64_t)a.tokens * a.top_k - first);
-    for (int i = tid; i < entries; i += RT_THREADS) ids[i] = a.ids[first + i];
     __syncthreads();
-    for (int e = tid; e < E; e += RT_THREADS) base[e] += a.workspace[(int64_t)blockIdx.x * E + e];
-    __syncthreads();
-    for (int i = tid; i < entries; i += RT_THREADS) {
-        const int id = ids[i];
-        int slot = -1;
-        if (id >= 0) {
-            int rank = 0;
-            for (int j = 0; j < i; j++) rank += ids[j] == id ? 1 : 0;
-            slot = base[id] + rank;
-            a.rows[slot] = (int)((first + i) / a.top_k);
-        }
-        a.slots[first + i] = slot;
-        if (first + i >= total) a.rows[first + i] = -1;   // behind the last expert's
+    const int64_t first = (int64_t)blockIdx.x * run * a.top_k;
+    const int entries = (int)min((int64_t)run * a.top_k, (int64_t)a.tokens * a.top_k - first);
+    for (int i = tid; i < entries; i += RT_PLACE) {
+        const int id = a.ids[first + i];
+        if (id >= 0) atomicOr(&mask[id], 1ull << (i / a.top_k));
     }
+    __syncthreads();
+    for (int i = tid; i < entries; i += RT_PLACE) place(a, first, i, a.ids[first + i], base, mask, total);
 }
 
-int64_t moe_route_bytes(const RouteArgs& a) { return ((int64_t)route_plan(a).blocks + 1) * a.experts * 4; }
+// Up to 64 tokens: everything in one workgroup.
+template <bool F32, int VPL>
+__global__ __launch_bounds__(RT_THREADS) void route_small(RouteArgs a) {
+    __shared__ int base[RT_MAX_EXPERTS];
+    __shared__ int part[RT_WAVES];
+    __shared__ unsigned long long mask[RT_MAX_EXPERTS];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), E = a.experts;
+    for (int e = tid; e < E; e += RT_THREADS) mask[e] = 0;
+    __syncthreads();
+    for (int u = wave; u < a.tokens; u += RT_WAVES) {
+        int id;
+        float w;
+        route_token<F32, VPL>(a, u, id, w);
+        note(a, u, u, id, w, mask);
+    }
+    __syncthreads();
+    static_assert(RT_MAX_EXPERTS <= RT_THREADS, "a thread an expert");
+    int total;
+    const int at = before_threads<RT_THREADS>(tid < E ? __popcll(mask[tid]) : 0, part, total);
+    if (tid < E) base[tid] = a.expert_start[tid] = at;
+    if (tid == 0) a.expert_start[E] = total;
+    __syncthreads();
+    const int entries = a.tokens * a.top_k;
+    // ids from this workgroup's own stores (ordered by the barriers)
+    for (int i = tid; i < entries; i += RT_THREADS) place(a, 0, i, a.ids[i], base, mask, total);
+}
+
+struct RoutePlan {
+    int run, runs;                       // tokens of a run; runs (0: one workgroup for all)
+};
+static RoutePlan route_plan(const RouteArgs& a) {
+    if (a.tokens <= RT_SMALL) return {RT_RUN, 0};
+    int run = RT_WAVES;                  // a token a wave, until the card is full of runs
+    while (run < RT_RUN && (int64_t)run * 256 < a.tokens) run *= 2;
+    return {run, (a.tokens + run - 1) / run};
+}
+
+int64_t moe_route_bytes(const RouteArgs& a) {
+    const RoutePlan p = route_plan(a);
+    return p.runs ? ((int64_t)p.runs + 1) * a.experts * 4 : 0;
+}
+
+template <bool F32, int VPL>
+static hipError_t queue_route(const RouteArgs& a, hipStream_t stream) {
+    const RoutePlan p = route_plan(a);
+    if (p.runs == 0) {
+        route_small<F32, VPL><<<dim3(1), dim3(RT_THREADS), 0, stream>>>(a);
+        return hipGetLastError();
+    }
+    route_tokens<F32, VPL><<<dim3((unsigned)p.runs), dim3(RT_THREADS), 0, stream>>>(a, p.run);
+    route_counts<<<dim3((unsigned)((a.experts + RT_PLACE / 64 - 1) / (RT_PLACE / 64))), dim3(RT_PLACE), 0, stream>>>(a, p.runs);
+    route_place<<<dim3((unsigned)p.runs), dim3(RT_PLACE), 0, stream>>>(a, p.run, p.runs);
+    return hipGetLastError();
+}
 
 template <bool F32>
-static void queue_tokens(const RouteArgs& a, const RoutePlan& p, hipStream_t stream) {
-    const dim3 grid((unsigned)p.blocks), threads(RT_THREADS);
-    if (a.experts <= 64) route_tokens<F32, 1><<<grid, threads, 0, stream>>>(a, p.chunk);
-    else if (a.experts <= 128) route_tokens<F32, 2><<<grid, threads, 0, stream>>>(a, p.chunk);
-    else if (a.experts <= 256) route_tokens<F32, 4><<<grid, threads, 0, stream>>>(a, p.chunk);
-    else if (a.experts <= 512) route_tokens<F32, 8><<<grid, threads, 0, stream>>>(a, p.chunk);
-    else route_tokens<F32, 16><<<grid, threads, 0, stream>>>(a, p.chunk);
+static hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
+    if (a.experts <= 64) return queue_route<F32, 1>(a, stream);
+    if (a.experts <= 128) return queue_route<F32, 2>(a, stream);
+    if (a.experts <= 256) return queue_route<F32, 4>(a, stream);
+    if (a.experts <= 512) return queue_route<F32, 8>(a, stream);
+    return queue_route<F32, 16>(a, stream);
 }
 
 hipError_t launch_moe_route(const RouteArgs& a, int f32, hipStream_t stream) {
-    const RoutePlan p = route_plan(a);
-    if (p.blocks > 0) {
-        if (f32) queue_tokens<true>(a, p, stream);
-        else queue_tokens<false>(a, p, stream);
-    }
-    route_counts<<<dim3((unsigned)((a.experts + RT_WAVES - 1) / RT_WAVES)), dim3(RT_THREADS), 0, stream>>>(a, p.blocks);
-    route_place<<<dim3((unsigned)(p.blocks ? p.blocks : 1)), dim3(RT_THREADS), 0, stream>>>(a, p.chunk, p.blocks);
-    return hipGetLastError();
+    return f32 ? launch_route<true>(a, stream) : launch_route<false>(a, stream);
 }
 
 }  // namespace fp8g

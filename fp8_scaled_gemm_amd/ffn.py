@@ -14,7 +14,7 @@ import torch
 from . import FMT_E4M3, load
 from .block import _block, _bytes, _done
 
-__all__ = ["NormQuant", "add_rms_norm_quantize", "fp8_gemm_fused", "mxfp8_gemm_fused", "MoeRoute", "moe_route",
+__all__ = ["NormQuant", "add_rms_norm_quantize", "fp8_gemm_fused", "mxfp8_gemm_fused", "gemm_fused_workspace", "MoeRoute", "moe_route",
            "moe_route_workspace", "fp8_moe_gemm", "mxfp8_moe_gemm", "moe_gemm_workspace", "moe_combine"]
 
 _ACTS = {None: 0, "none": 0, "silu": 1, "gelu_tanh": 2}
@@ -58,24 +58,30 @@ def add_rms_norm_quantize(x, weight=None, residual=None, eps=1e-6, mx=False, fmt
 
 
 def fp8_gemm_fused(m, n, k, A, B, scale_a, scale_b, bias=None, act=None, gated=False, residual=None, D=None,
-                   out_dtype=None):
+                   out_dtype=None, workspace=None):
     """D [m, n] = act(z) + residual with z = scale_a * scale_b * (A [m, k] @ B [n, k]^T) + bias (E4M3 operands);
     gated: B [2 n, k] holds the gate and then the up projection, and D =
     act(z_gate) * z_up + residual.
 
     act: None, "silu" or "gelu_tanh"; bias float32 [n or 2 n]; residual of D's
-    type, bfloat16 or float32, and may be D itself.
+    type, bfloat16 or float32, and may be D itself.  workspace: a device tensor
+    to use instead of a fresh one (gemm_fused_workspace gives its bytes).
     """
     return _done(_block().gemm_fused(m, n, k, A, B, scale_a, scale_b, False, bias, _choice(_ACTS, act, "act"), gated, residual,
-                                     D, _is_f32(D, out_dtype)), "fp8_gemm_fused")
+                                     D, _is_f32(D, out_dtype), workspace), "fp8_gemm_fused")
 
 
 def mxfp8_gemm_fused(m, n, k, A, B, scale_a, scale_b, bias=None, act=None, gated=False, residual=None, D=None,
-                     out_dtype=None):
+                     out_dtype=None, workspace=None):
     """fp8_gemm_fused with a UE8M0 code (uint8) for every 32 elements of k in
     scale_a [m, k / 32] and scale_b [n or 2 n, k / 32]."""
     return _done(_block().gemm_fused(m, n, k, A, B, scale_a, scale_b, True, bias, _choice(_ACTS, act, "act"), gated, residual,
-                                     D, _is_f32(D, out_dtype)), "mxfp8_gemm_fused")
+                                     D, _is_f32(D, out_dtype), workspace), "mxfp8_gemm_fused")
+
+
+def gemm_fused_workspace(m, n, k, gated=False, mx=False):
+    """Bytes of workspace that fp8_gemm_fused (mx: mxfp8_gemm_fused) needs for these sizes."""
+    return _bytes(load().gemm_fused_workspace(m, n, k, gated, mx), "gemm_fused_workspace")
 
 
 class MoeRoute(collections.namedtuple("MoeRoute", "ids weights expert_start rows slots")):

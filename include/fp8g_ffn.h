@@ -109,18 +109,25 @@ int add_rms_norm_quantize(const void* x, int64_t x_stride, const void* residual,
  * act      fp8g_act_t
  * residual device, [m, n] of out_dtype, or NULL; may be D itself
  * D        device, [m, n] of out_dtype (fp8g_out_t), written
+ * workspace  device, for the partial sums of products whose K is split (few
+ *          tiles and a long K); at most 64 MB
  * m == 0 or n == 0: no-op.  k == 0: the product is 0.
  * Limits and contract as fp8_gemm_scaled / mxfp8_gemm, with n or 2 n rows of B
- * below 2^22 (bf16 output) / 2^21 (fp32).
+ * below 2^22 (bf16 output) / 2^21 (fp32); a workspace smaller than
+ * gemm_fused_workspace is ERR_UNSUPPORTED.
  * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_DTYPE (out_dtype, act),
  * ERR_OVERLAP, ERR_UNSUPPORTED, ERR_HIP.
  */
 int fp8_gemm_fused(int64_t m, int64_t n, int64_t k, const uint8_t* A, const uint8_t* B, const float* scale_a,
                    const float* scale_b, const float* bias, int act, int gated, const void* residual, void* D,
-                   int out_dtype, hipStream_t stream);
+                   int out_dtype, void* workspace, int64_t workspace_bytes, hipStream_t stream);
 int mxfp8_gemm_fused(int64_t m, int64_t n, int64_t k, const uint8_t* A, const uint8_t* B, const uint8_t* scale_a,
                      const uint8_t* scale_b, const float* bias, int act, int gated, const void* residual, void* D,
-                     int out_dtype, hipStream_t stream);
+                     int out_dtype, void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace the fused products need (mx: of mxfp8_gemm_fused); -1 for
+ * sizes they refuse. */
+int64_t gemm_fused_workspace(int64_t m, int64_t n, int64_t k, int gated, int mx);
 
 /*
  * moe_route -- the experts of every token.

@@ -30,7 +30,7 @@ def lib():
 def test_exports_every_header_function(lib):
     text = open(os.path.join(os.path.dirname(fp8g.HEADER_PATH), "fp8g_ffn.h")).read()
     names = re.findall(r"^(?:int|int64_t)\s+(\w+)\s*\(", text, flags=re.M)
-    assert set(names) == {"add_rms_norm_quantize", "fp8_gemm_fused", "mxfp8_gemm_fused", "moe_route", "moe_route_workspace",
+    assert set(names) == {"add_rms_norm_quantize", "fp8_gemm_fused", "mxfp8_gemm_fused", "gemm_fused_workspace", "moe_route", "moe_route_workspace",
                           "fp8_moe_gemm", "mxfp8_moe_gemm", "moe_gemm_workspace", "moe_combine"}
     for name in names:
         assert hasattr(lib, name)
@@ -61,9 +61,10 @@ def test_norm_refusals(lib):
     assert norm(lib, q=P(4)) == OVERLAP and norm(lib, scale=P(5)) == OVERLAP and norm(lib, total=P(2)) == OVERLAP
 
 
-def gemm(lib, mx=False, m=4, n=64, k=256, A=P(0), B=P(1), sa=P(2), sb=P(3), bias=P(4), act=1, gated=1, res=P(5), D=P(6), out=0):
+def gemm(lib, mx=False, m=4, n=64, k=256, A=P(0), B=P(1), sa=P(2), sb=P(3), bias=P(4), act=1, gated=1, res=P(5), D=P(6), out=0,
+         ws=P(9), size=1 << 40):
     call = lib.mxfp8_gemm_fused if mx else lib.fp8_gemm_fused
-    return call(m, n, k, A, B, sa, sb, bias, act, gated, res, D, out, None)
+    return call(m, n, k, A, B, sa, sb, bias, act, gated, res, D, out, ws, size, None)
 
 
 def moe(lib, mx=False, S=8, n=64, k=256, E=4, A=P(0), Ra=5, rows=P(7), start=P(8), B=P(1), sa=P(2), sb=P(3), bias=P(4), act=1,
@@ -91,6 +92,12 @@ def test_product_refusals(lib, mx):
             assert call(lib, mx, D=P(i)) == OVERLAP, i
     assert gemm(lib, mx, k=264) == (SHAPE if mx else UNSUPPORTED) and moe(lib, mx, k=264) == (SHAPE if mx else UNSUPPORTED)
     assert gemm(lib, mx, res=P(5, 4)) == ALIGN and gemm(lib, mx, D=P(5, 16)) == OVERLAP
+    need = lib.gemm_fused_workspace(256, 1024, 8192, 1, mx)          # few tiles, a long K: split
+    split = {"m": 256, "n": 1024, "k": 8192}
+    assert need > 0 and gemm(lib, mx, size=need - 1, **split) == UNSUPPORTED and gemm(lib, mx, ws=None, **split) == NULL
+    for i in (0, 1, 2, 3, 4, 5, 6):
+        assert gemm(lib, mx, ws=P(i), **split) == OVERLAP
+    assert lib.gemm_fused_workspace(64, 1024, 8200, 1, mx) == -1 and lib.gemm_fused_workspace(0, 1024, 8192, 1, mx) == 0
     assert moe(lib, mx, E=-1) == SHAPE and moe(lib, mx, Ra=-1) == SHAPE and moe(lib, mx, Ra=0) == SHAPE
     assert moe(lib, mx, rows=None) == SHAPE                        # 5 rows of A for 8 slots
     assert moe(lib, mx, E=1025) == UNSUPPORTED and moe(lib, mx, S=1 << 28) == UNSUPPORTED
@@ -109,7 +116,7 @@ def test_product_refusals(lib, mx):
     assert lib.moe_gemm_workspace(0, 64, 256, 4, 1, 0, mx) == 0
 
 
-def route(lib, x=P(0), dtype=0, T=7, E=64, k=4, bias=P(1), score=0, groups=8, top=3, each=2, ids=P(2), w=P(3), start=P(4),
+def route(lib, x=P(0), dtype=0, T=70, E=64, k=4, bias=P(1), score=0, groups=8, top=3, each=2, ids=P(2), w=P(3), start=P(4),
           rows=P(5), slots=P(6), ws=P(7), size=1 << 40):
     return lib.moe_route(x, dtype, T, E, k, bias, score, groups, top, each, 1, 1.0, ids, w, start, rows, slots, ws, size, None)
 
@@ -129,8 +136,9 @@ def test_route_refusals(lib):
         for j in range(8):
             if i != j:
                 assert route(lib, **{name: P(j)}) == OVERLAP, (name, j)
-    need = lib.moe_route_workspace(7, 64, 4)
-    assert need >= 0 and (need == 0 or route(lib, size=need - 1) == UNSUPPORTED)
+    need = lib.moe_route_workspace(70, 64, 4)
+    assert need > 0 and route(lib, size=need - 1) == UNSUPPORTED
+    assert lib.moe_route_workspace(64, 64, 4) == 0                  # one workgroup does it all
     assert lib.moe_route_workspace(7, 64, 65) == -1 and lib.moe_route_workspace(7, 1025, 2) == -1
 
 
