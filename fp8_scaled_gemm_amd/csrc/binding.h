@@ -92,6 +92,15 @@ struct Call {
     }
 };
 
+// A dense tensor of `shape` at byte `at` of a block of bytes that several outputs
+// share: one allocation for all of them.
+Tensor part(const Tensor& block, int64_t at, Sizes shape, at::ScalarType t) {
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(block.storage()), block.key_set(), c10::scalarTypeToTypeMeta(t));
+    impl->set_storage_offset(block.storage_offset() + at / (int64_t)c10::elementSize(t));
+    impl->set_sizes_contiguous(shape);
+    return Tensor(std::move(impl));
+}
+
 // The caller's workspace, or one from torch's allocator for this call: freed
 // behind the call, its memory is handed out again in stream order.
 struct Workspace {

@@ -141,8 +141,12 @@ PyObject* moe_route_(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(x, "logits", dt, {T, E}, c.device);
         const float* bias = floats(a[2], "bias", {E}, c);
         if (k < 1 || k > E) throw std::invalid_argument("top_k must be between 1 and the number of experts");
-        const Tensor ids = c.make({T, k}, at::kInt), w = c.make({T, k}, at::kFloat), start = c.make({E + 1}, at::kInt);
-        const Tensor rows = c.make({T * k}, at::kInt), slots = c.make({T, k}, at::kInt);
+        // one allocation for the five: a decode step calls this once a layer
+        const int64_t each = (4 * T * k + 15) / 16 * 16;
+        const Tensor all = c.make({4 * each + 4 * (E + 1)}, at::kByte);
+        const Tensor ids = part(all, 0, {T, k}, at::kInt), w = part(all, each, {T, k}, at::kFloat);
+        const Tensor rows = part(all, 2 * each, {T * k}, at::kInt), slots = part(all, 3 * each, {T, k}, at::kInt);
+        const Tensor start = part(all, 4 * each, {E + 1}, at::kInt);
         const Workspace ws(a[9], moe_route_workspace(T, E, k), c);
         const int st = moe_route(x.data_ptr(), code, T, E, k, bias, (int)integer(a[3]), integer(a[4]), integer(a[5]),
                                  integer(a[6]), truth(a[7]), real(a[8]), ids.data_ptr<int32_t>(), w.data_ptr<float>(),
@@ -151,9 +155,9 @@ PyObject* moe_route_(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (st) return PyLong_FromLong(st);
         PyObject* r = PyTuple_New(5);
         if (!r) return nullptr;
-        const Tensor* all[] = {&ids, &w, &start, &rows, &slots};
+        const Tensor* out[] = {&ids, &w, &start, &rows, &slots};
         for (int i = 0; i < 5; i++) {
-            PyObject* o = THPVariable_Wrap(*all[i]);
+            PyObject* o = THPVariable_Wrap(*out[i]);
             if (!o) {
                 Py_DECREF(r);
                 return nullptr;

@@ -14,7 +14,6 @@
 // 8 + MX for the partial sums of K ranges).
 
 #include <atomic>
-#include <cstdlib>
 #include <type_traits>
 
 #include "gemm_tile.h"
@@ -115,10 +114,10 @@ __global__ __launch_bounds__(PLAN_THREADS) void moe_plan(const int32_t* __restri
                                                          const void* __restrict__ sa, int experts, int slots, int a_rows,
                                                          int k, int mx, int bm, int32_t* __restrict__ plan,
                                                          uint32_t* __restrict__ row_at, void* __restrict__ scale) {
-    __shared__ int sum[PLAN_THREADS];
+    __shared__ int sum[PLAN_THREADS / 64];
     __shared__ int mine[3];
     constexpr int PER = PLAN_EXPERTS / PLAN_THREADS;
-    const int tid = threadIdx.x, t = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, t = blockIdx.x;
     int first[PER], count[PER], tiles = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -130,18 +129,23 @@ __global__ __launch_bounds__(PLAN_THREADS) void moe_plan(const int32_t* __restri
         }
         tiles += (count[i] + bm - 1) / bm;
     }
-    sum[tid] = tiles;
-    __syncthreads();
-    for (int off = 1; off < PLAN_THREADS; off <<= 1) {
-        const int v = tid >= off ? sum[tid - off] : 0;
-        __syncthreads();
-        sum[tid] += v;
-        __syncthreads();
+    int upto = tiles;                                     // with this thread's
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(upto, off, 64);
+        if (lane >= off) upto += v;
     }
-    const int total = sum[PLAN_THREADS - 1];
+    if (lane == 63) sum[wave] = upto;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < PLAN_THREADS / 64; ++w) {
+        if (w < wave) upto += sum[w];
+        total += sum[w];
+    }
     if (t == 0 && tid == 0) plan[0] = total;
     if (t >= total) return;
-    int at = sum[tid] - tiles;
+    int at = upto - tiles;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int n = (count[i] + bm - 1) / bm;
@@ -189,9 +193,9 @@ __global__ __launch_bounds__(PLAN_THREADS) void moe_plan(const int32_t* __restri
 // from HBM) and used to choose between
 //   the row kernel (gemm_rows.hip), the larger of
 //     4 + B at 5.5 TB/s, again at 8 TB/s for every further 64 rows, + A, read by
-//     every workgroup, at 9.3 TB/s (mode (b): 4.2, 6 and 7), and
+//     every workgroup, at 9.3 TB/s, and
 //     4 + the steps of a wave at 0.35 / 0.6 / 1.1 us with 16 / 32 / 64 rows of A
-//     (mode (b): half as much again);
+//     (mode (b): a tenth more of all of it);
 //   a tile: 4.5 + rounds of workgroups x (fixed + stages x stage), below, the
 //     stage of the small tiles shorter while they fill at most half of the CUs;
 //   64x128 or 128x128 tiles with K in ranges, where the tiles leave CUs idle:
@@ -218,15 +222,14 @@ struct FusedPlan {
     double us;
 };
 static FusedPlan fused_plan(const FusedArgs& a, int cus) {
-    if (const char* force = getenv("FP8G_FORCE")) return {atoi(force) % 1000000, atoi(force) / 1000000 ? atoi(force) / 1000000 : 1, 0};
     const int64_t b_rows = a.gated ? 2 * a.n : a.n, nk = (a.k + BK - 1) / BK;
     const double b_bytes = (double)b_rows * a.k, work = b_bytes + (double)a.m * a.k;
     const int64_t wgs = (b_rows + 31) / 32, cols = wgs < 512 && !a.gated ? 16 : 32;     // as launch_gemm_rows cuts it
     const double a_read = (double)((b_rows + cols - 1) / cols) * ((a.m + 15) / 16 * 16) * a.k;
     const double again = (double)((a.m + 63) / 64 - 1);
-    const double fed = b_bytes / (a.mx ? 4.2e6 : 5.5e6) + again * b_bytes / (a.mx ? 6.0e6 : 8.0e6) + a_read / (a.mx ? 7.0e6 : 9.3e6);
-    const double steps = (double)((nk + 3) / 4) * (a.m <= 16 ? 0.35 : a.m <= 32 ? 0.6 : 1.1) * (a.mx ? 1.5 : 1.0);
-    FusedPlan best = {0, 1, 4.0 + (fed > steps ? fed : steps)};
+    const double fed = b_bytes / 5.5e6 + again * b_bytes / 8.0e6 + a_read / 9.3e6;
+    const double steps = (double)((nk + 3) / 4) * (a.m <= 16 ? 0.35 : a.m <= 32 ? 0.6 : 1.1);
+    FusedPlan best = {0, 1, 4.0 + (fed > steps ? fed : steps) * (a.mx ? 1.1 : 1.0)};
     if (a.m <= 16) return best;                       // the tiles are mostly empty
     const double hbm = 6.0 + work / 5.3e6;
     auto consider = [&](const TileCost& c) {
@@ -345,7 +348,6 @@ static bool few_rows(const FusedArgs& a) { return a.m <= FEW_ROWS_EXPERT * a.exp
 // / 276, with 512 rows 977 / 723 / 701 / 594; 60 of 2048 x 1408 with 273 rows
 // 127 / 98 / 99 / 105.
 static int moe_tile(const FusedArgs& a) {
-    if (const char* force = getenv("FP8G_FORCE")) if (atoi(force) > 1) return atoi(force);
     const int64_t b_rows = a.gated ? 2 * a.n : a.n, nk = (a.k + BK - 1) / BK;
     int best = 0;
     double best_us = 0.0;
@@ -379,7 +381,7 @@ static MoeSpace moe_space(const FusedArgs& a) {
     return s;
 }
 
-int64_t moe_gemm_bytes(const FusedArgs& a) { return few_rows(a) && !getenv("FP8G_FORCE") ? 0 : moe_space(a).bytes; }
+int64_t moe_gemm_bytes(const FusedArgs& a) { return few_rows(a) ? 0 : moe_space(a).bytes; }
 
 static hipError_t launch_product(const FusedArgs& a, hipStream_t stream) {
     FusedPlan p = fused_plan(a, PLAN_CUS);
@@ -409,9 +411,7 @@ static hipError_t launch_product(const FusedArgs& a, hipStream_t stream) {
 
 hipError_t launch_gemm_fused(const FusedArgs& a, hipStream_t stream) {
     if (!a.expert_start) return launch_product(a, stream);
-    const char* force = getenv("FP8G_FORCE");
-    const int forced = force ? atoi(force) : 0;
-    if (forced ? forced == 1 : few_rows(a)) return launch_gemm_rows(a, stream);
+    if (few_rows(a)) return launch_gemm_rows(a, stream);
     TileLaunch t = {};
     hipError_t e = hipGetDevice(&t.dev);
     if (e != hipSuccess) return e;

@@ -18,7 +18,9 @@
 // first operand, so a lane's four results are four neighbouring columns n of one
 // row m.  A lane's first 16 operand bytes are elements 16 g .. 16 g + 15 of the
 // 128 (g = lane / 16), its second 64 + 16 g ..; lane group g brings the scale of
-// the 32-element block g.
+// the 32-element block g.  Block scales pass through LDS where a workgroup's fit
+// (SC_LDS): fetched by the step they are a load each for a byte a lane, half as
+// many again as the operands' (64 experts of 2 x 1408 x 4096, 6 rows: 168 us so).
 
 #include <type_traits>
 
@@ -50,10 +52,15 @@ struct RowsArgs {
     Act act;
 };
 
+// Bytes between the scale rows in LDS: whole 16 bytes, an odd number of them, so
+// that the 16 rows of a read lie in different banks.
+__host__ __device__ constexpr int scale_pitch(int nblk) { return ((nblk + 15) / 16 | 1) * 16; }
+constexpr int SC_LIMIT = 40 * 1024;       // of a workgroup: four on a CU beside their sums
+
 // B's rows of a workgroup: NB blocks of 16; gated: the first half of them the
 // gate's, the others the up projection's.  MB: blocks of 16 rows of A.  AHEAD:
 // steps in flight.  WPE: waves of a SIMD that the registers are to allow.
-template <bool MX, bool GATED, int NB, int MB, int AHEAD, int WPE>
+template <bool MX, bool SC_LDS, bool GATED, int NB, int MB, int AHEAD, int WPE>
 __global__ __launch_bounds__(RW_THREADS, WPE) void gemm_rows_kernel(RowsArgs args) {
     const FusedArgs& a = args.f;
     constexpr int H = GATED ? 2 : 1;                      // projections
@@ -61,7 +68,9 @@ __global__ __launch_bounds__(RW_THREADS, WPE) void gemm_rows_kernel(RowsArgs arg
     constexpr int COLS = 16 * NO;                         // output columns
     constexpr int UNITS = COLS / 4 * 16 * MB;             // threads that finish: four columns of a row each
     static_assert(NB % H == 0 && UNITS <= RW_THREADS, "one unit a thread");
+    static_assert(MX || !SC_LDS, "block scales");
     __shared__ v4f red[RW_WAVES][NB * MB][64];
+    extern __shared__ __attribute__((aligned(16))) uint8_t scales[];      // SC_LDS: B's rows, then A's
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, g = lane >> 4;
@@ -99,6 +108,30 @@ __global__ __launch_bounds__(RW_THREADS, WPE) void gemm_rows_kernel(RowsArgs arg
         veb[i] = (uint32_t)(16 * i + l16) * (uint32_t)nblk + g;
     }
 
+    // SC_LDS: `rows` rows of nblk scale bytes into LDS from row `at` on; from(r): row
+    // r's, or nullptr
+    const int pitch = scale_pitch(nblk);
+    auto fetch_scales = [&](int at, int rows, auto from) __attribute__((always_inline)) {
+        auto copy = [&](auto unit) __attribute__((always_inline)) {
+            using U = decltype(unit);
+            const int per = nblk / (int)sizeof(U);
+            for (int i = threadIdx.x; i < rows * per; i += RW_THREADS) {
+                const int r = i / per, c = i - r * per;
+                const uint8_t* p = from(r);
+                if (p) reinterpret_cast<U*>(scales + (at + r) * pitch)[c] = reinterpret_cast<const U*>(p)[c];
+            }
+        };
+        if (nblk % 16 == 0) copy(v4u{});
+        else if (nblk % 4 == 0) copy(uint32_t{});
+        else copy(uint8_t{});
+    };
+    if constexpr (SC_LDS) {
+        fetch_scales(0, 16 * NB, [&](int r) {
+            const int h = r / (16 * NO), c = r % (16 * NO);
+            return c < cols ? static_cast<const uint8_t*>(a.scale_b) + (b_row + (int64_t)h * N + n0 + c) * nblk : nullptr;
+        });
+    }
+
     for (; s0 < s1; s0 += step) {
         const int count = (int)min((int64_t)(16 * MB), s1 - s0);
         // A: this chunk's rows, or with `rows` all of A
@@ -115,6 +148,12 @@ __global__ __launch_bounds__(RW_THREADS, WPE) void gemm_rows_kernel(RowsArgs arg
             if (gather) r = min(max(a.rows[s0 + r], 0), (int)a.a_rows - 1);
             va[j] = (uint32_t)r * (uint32_t)K + 16u * g;
             vea[j] = (uint32_t)r * (uint32_t)nblk + g;
+        }
+        if constexpr (SC_LDS) {
+            fetch_scales(16 * NB, count, [&](int r) {
+                const int64_t row = gather ? min(max(a.rows[s0 + r], 0), (int)a.a_rows - 1) : s0 + r;
+                return static_cast<const uint8_t*>(a.scale_a) + row * nblk;
+            });
         }
 
         struct Frag {
@@ -133,7 +172,7 @@ __global__ __launch_bounds__(RW_THREADS, WPE) void gemm_rows_kernel(RowsArgs arg
             for (int i = 0; i < NB; i++) f.b[i] = load16(rsB[i / NO], vb[i % NO], st);
 #pragma unroll
             for (int j = 0; j < MB; j++) f.a[j] = load16(rsA, va[j], st);
-            if constexpr (MX) {
+            if constexpr (MX && !SC_LDS) {
                 const bool in = 4 * st + g < nblk;
 #pragma unroll
                 for (int i = 0; i < NB; i++)
@@ -157,9 +196,18 @@ __global__ __launch_bounds__(RW_THREADS, WPE) void gemm_rows_kernel(RowsArgs arg
             load(wave + RW_WAVES * u, f[u]);
             __builtin_amdgcn_sched_barrier(0);
         }
+        if constexpr (SC_LDS) __syncthreads();
         for (int st = wave; st < steps; st += RW_WAVES * AHEAD) {
 #pragma unroll
             for (int u = 0; u < AHEAD; u++) {
+                if constexpr (SC_LDS) {
+                    // blocks past K: some byte of the row; the codes there are zeros
+                    const int c = min(4 * (st + RW_WAVES * u) + g, nblk - 1);
+#pragma unroll
+                    for (int i = 0; i < NB; i++) f[u].eb[i] = scales[(16 * i + l16) * pitch + c];
+#pragma unroll
+                    for (int j = 0; j < MB; j++) f[u].ea[j] = scales[(16 * NB + min(16 * j + l16, count - 1)) * pitch + c];
+                }
 #pragma unroll
                 for (int i = 0; i < NB; i++)
 #pragma unroll
@@ -246,7 +294,15 @@ static hipError_t launch_one_rows(const FusedArgs& f, hipStream_t stream) {
     int64_t gy = f.expert_start ? f.experts : (f.m + 16 * MB - 1) / (16 * MB);
     if (gy > 65535) gy = 65535;
     RowsArgs args{f, act_of(f.act)};
-    gemm_rows_kernel<MX, GATED, NB, MB, AHEAD, WPE><<<dim3((unsigned)gx, (unsigned)gy), dim3(RW_THREADS), 0, stream>>>(args);
+    const dim3 grid((unsigned)gx, (unsigned)gy), threads(RW_THREADS);
+    if constexpr (MX) {
+        const int64_t lds = (int64_t)scale_pitch((int)(f.k / 32)) * 16 * (NB + MB);
+        if (lds <= SC_LIMIT && f.k > 0) {
+            gemm_rows_kernel<true, true, GATED, NB, MB, AHEAD, WPE><<<grid, threads, (unsigned)lds, stream>>>(args);
+            return hipGetLastError();
+        }
+    }
+    gemm_rows_kernel<MX, false, GATED, NB, MB, AHEAD, WPE><<<grid, threads, 0, stream>>>(args);
     return hipGetLastError();
 }
 
@@ -260,7 +316,7 @@ template <bool MX, bool GATED>
 static hipError_t launch_rows(const FusedArgs& f, hipStream_t stream) {
     const int64_t rows = f.expert_start ? (f.m + f.experts - 1) / f.experts : f.m;   // of a product, on average
     if constexpr (GATED) {
-        if (rows <= 16) return launch_one_rows<MX, true, 2, 1, 2, 4>(f, stream);
+        if (rows <= 16) return launch_one_rows<MX, true, 2, 1, 1, 4>(f, stream);
         if (rows <= 32) return launch_one_rows<MX, true, 2, 2, 2, 2>(f, stream);
         return launch_one_rows<MX, true, 2, 4, 2, 2>(f, stream);
     } else {
@@ -268,7 +324,7 @@ static hipError_t launch_rows(const FusedArgs& f, hipStream_t stream) {
         if (rows > 16) return launch_one_rows<MX, false, 1, 2, 4, 2>(f, stream);
         const int64_t blocks = (f.n + 31) / 32 * (f.expert_start ? f.experts : 1);
         if (blocks < 512) return launch_one_rows<MX, false, 1, 1, 4, 4>(f, stream);
-        return launch_one_rows<MX, false, 2, 1, 2, 4>(f, stream);
+        return launch_one_rows<MX, false, 2, 1, 1, 4>(f, stream);
     }
 }
 

@@ -27,7 +27,9 @@
 
 namespace fp8g {
 
-constexpr int RT_WAVES = 16, RT_THREADS = 64 * RT_WAVES;
+// waves of a run's workgroup: 16, and 8 where a lane holds more experts than 128
+// registers do
+constexpr int rt_waves(int vpl) { return vpl <= 4 ? 16 : 8; }
 constexpr int RT_PLACE = 256;            // threads that place a run's rows
 constexpr int RT_MAX_EXPERTS = 1024;
 constexpr int RT_RUN = 64;               // tokens of a run, at most: bits of a mask
@@ -38,47 +40,66 @@ constexpr int RT_SMALL = 64;
 // choice, a group's sum twice all of that.
 constexpr float RT_MARGIN = 1.0f / (1 << 18);
 
-// All lanes' combination, in every lane: over rows of 16, then over the four rows.
-template <int CTRL>
-__device__ __forceinline__ float dpp_from(float v, float other) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, other), __builtin_bit_cast(int, v),
-                                                                 CTRL, 0xF, 0xF, false));
+// A value that comes from lanes to the left, or `none` where there are none.
+template <int CTRL, bool ZERO>
+__device__ __forceinline__ float dpp_from(float v, float none) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v), CTRL,
+                                                                 0xF, 0xF, ZERO));
 }
-template <int CTRL>
-__device__ __forceinline__ double dpp_from(double v, double other) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v), o = __builtin_bit_cast(uint64_t, other);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)o, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)(o >> 32), (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+template <int CTRL, bool ZERO>
+__device__ __forceinline__ double dpp_from(double v, double none) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v), o = __builtin_bit_cast(uint64_t, none);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)o, (int)(uint32_t)b, CTRL, 0xF, 0xF, ZERO);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)(o >> 32), (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, ZERO);
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
-__device__ __forceinline__ float lane63(float v) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+// a uniform lane's value, as a scalar
+__device__ __forceinline__ float from_lane(float v, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
-__device__ __forceinline__ double lane63(double v) {
+__device__ __forceinline__ double from_lane(double v, int lane) {
     const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-template <class R, class F>
-__device__ __forceinline__ R over_wave(R v, R neutral, F f) {
-    v = f(v, dpp_from<0x111>(v, neutral));      // row_shr:1, 2, 4, 8
-    v = f(v, dpp_from<0x112>(v, neutral));
-    v = f(v, dpp_from<0x114>(v, neutral));
-    v = f(v, dpp_from<0x118>(v, neutral));
-    v = f(v, dpp_from<0x142>(v, neutral));      // row_bcast:15, 31
-    v = f(v, dpp_from<0x143>(v, neutral));
-    return lane63(v);
 }
 __device__ __forceinline__ float larger(float u, float v) { return __builtin_fmaxf(u, v); }
 __device__ __forceinline__ double larger(double u, double v) { return __builtin_fmax(u, v); }
-template <class R>
-__device__ __forceinline__ R wave_most(R v) {
-    return over_wave(v, -(R)__builtin_inff(), [](R a, R b) { return larger(a, b); });
+// Over the wave: over rows of 16 lanes, then over the four rows; the last lane has
+// it all.  A lane without a lane to its left takes itself (largest) or 0 (sum),
+// so that each step is one instruction.
+// (fp32: the six steps written out, as the compiler takes four instructions for
+// one of them; a lane written by the instruction before is read two waits later)
+__device__ __forceinline__ float wave_most(float v) {
+    asm volatile(
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_shr:1 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_shr:2 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_shr:4 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_shr:8 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_bcast:15 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 row_bcast:31 row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 1"
+        : "+v"(v));
+    return from_lane(v, 63);
+}
+__device__ __forceinline__ double wave_most(double v) {
+    v = larger(v, dpp_from<0x111, false>(v, v));      // row_shr:1, 2, 4, 8
+    v = larger(v, dpp_from<0x112, false>(v, v));
+    v = larger(v, dpp_from<0x114, false>(v, v));
+    v = larger(v, dpp_from<0x118, false>(v, v));
+    v = larger(v, dpp_from<0x142, false>(v, v));      // row_bcast:15, 31
+    v = larger(v, dpp_from<0x143, false>(v, v));
+    return from_lane(v, 63);
 }
 template <class R>
 __device__ __forceinline__ R wave_total(R v) {
-    return over_wave(v, (R)0, [](R a, R b) { return a + b; });
+    v += dpp_from<0x111, true>(v, (R)0);
+    v += dpp_from<0x112, true>(v, (R)0);
+    v += dpp_from<0x114, true>(v, (R)0);
+    v += dpp_from<0x118, true>(v, (R)0);
+    v += dpp_from<0x142, true>(v, (R)0);
+    v += dpp_from<0x143, true>(v, (R)0);
+    return from_lane(v, 63);
 }
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
@@ -86,10 +107,31 @@ __device__ __forceinline__ double exp_of(double x) { return exp(x); }
 __device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
 __device__ __forceinline__ double inverse(double x) { return 1.0 / x; }
 
-// The token's experts: in lane j < top_k the j-th, or -1.  False: two of them, or
-// two groups, are too close for R = float to tell.
+// A lane's experts in falling order (VPL <= 4), among equals the lowest first;
+// byte i of `order` is the place of the i-th.
 template <class R, int VPL>
-__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL], int& id) {
+__device__ __forceinline__ void sort_lane(R (&key)[VPL], uint32_t& order) {
+    order = 0x03020100u;
+    auto step = [&](int i, int j) __attribute__((always_inline)) {      // i < j
+        const uint32_t a = (order >> (8 * i)) & 0xFFu, b = (order >> (8 * j)) & 0xFFu;
+        const bool turn = key[j] > key[i] || (key[j] == key[i] && b < a);
+        const R u = key[i], v = key[j];
+        key[i] = turn ? v : u, key[j] = turn ? u : v;
+        const uint32_t both = (a ^ b) << (8 * i) | (a ^ b) << (8 * j);
+        order = turn ? order ^ both : order;
+    };
+    if constexpr (VPL == 2) {
+        step(0, 1);
+    } else if constexpr (VPL == 4) {
+        step(0, 1), step(2, 3), step(0, 2), step(1, 3), step(1, 2);
+    }
+}
+
+// The token's experts: in lane at + j, j < top_k, the j-th; lanes keep what ids
+// holds where there is none.  False: two of them, or two groups, are too close for
+// R = float to tell.  x, bias: the lane's experts (-inf behind the last one).
+template <class R, int VPL>
+__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL], const float (&bias)[VPL], int to, int& ids) {
     const int lane = threadIdx.x & 63, E = a.experts;
     const R NEG = -(R)__builtin_inff();
     const bool exact = sizeof(R) == 8;
@@ -124,8 +166,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
     if (a.bias) {
 #pragma unroll
         for (int i = 0; i < VPL; i++) {
-            const int e = lane * VPL + i;
-            const R c = e < E ? p[i] + (R)a.bias[e] : NEG;
+            const R c = p[i] + (R)bias[i];
             key[i] = key[i] > NEG && c > NEG ? c : NEG;   // a bias of -inf or NaN: not there
         }
     }
@@ -179,7 +220,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
         }
         int rank = 0;
         for (int q = 0; q < a.groups; q++) {
-            const R other = __shfl(mine, q, 64);
+            const R other = from_lane(mine, q);
             rank += other > mine || (other == mine && q < lane) ? 1 : 0;
         }
         const bool in = lane < a.groups && rank < a.top_groups;
@@ -195,30 +236,46 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
             if (e >= E || !((kept >> (e / width)) & 1)) key[i] = NEG;
         }
     }
-    id = -1;
-    R before = (R)__builtin_inff();
     const int rounds = !exact && a.bias ? a.top_k + 1 : a.top_k;       // one more: the gap behind the last
+    R tops = NEG;                                         // lane j: the j-th choice
+    uint32_t order;
+    if constexpr (VPL <= 4) sort_lane<R, VPL>(key, order);
     for (int j = 0; j < rounds; j++) {
         R own = key[0];
+        if constexpr (VPL > 4) {
 #pragma unroll
-        for (int i = 1; i < VPL; i++) own = larger(own, key[i]);
+            for (int i = 1; i < VPL; i++) own = larger(own, key[i]);
+        }
         const R top = wave_most(own);
         if (!(top > NEG)) break;
-        if (!exact && a.bias) {
-            clear = clear && before - top > (R)RT_MARGIN * ((R)1 + larger(top, -top));
-            before = top;
-        }
         const int from = __builtin_ctzll(__ballot(own == top));
         int at = 0;
-        bool gone = lane != from;
+        if constexpr (VPL <= 4) {
+            at = __builtin_amdgcn_readlane((int)order, from) & 0xFF;
+            if (lane == from) {
 #pragma unroll
-        for (int i = 0; i < VPL; i++) {
-            const bool out = !gone && key[i] == top;
-            if (out) key[i] = NEG, at = i;
-            gone = gone || out;
+                for (int i = 0; i + 1 < VPL; i++) key[i] = key[i + 1];
+                key[VPL - 1] = NEG;
+                order >>= 8;
+            }
+        } else {
+            bool gone = lane != from;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                const bool out = !gone && key[i] == top;
+                key[i] = out ? NEG : key[i];
+                at = out ? i : at;
+                gone = gone || out;
+            }
+            at = __builtin_amdgcn_readlane(at, from);
         }
-        at = __builtin_amdgcn_readlane(at, from);
-        if (lane == j && j < a.top_k) id = from * VPL + at;
+        if (j < a.top_k) ids = lane == to + j ? from * VPL + at : ids;
+        if (!exact && a.bias) tops = lane == j ? top : tops;
+    }
+    if (!exact && a.bias) {
+        const R next = __shfl_down(tops, 1, 64);
+        const bool close = next > NEG && !(tops - next > (R)RT_MARGIN * ((R)1 + larger(tops, -tops)));
+        clear = clear && __ballot(lane < a.top_k && close) == 0;
     }
     return clear;
 }
@@ -229,54 +286,91 @@ __device__ __forceinline__ float logit_at(const RouteArgs& a, int64_t i) {
     else return __builtin_bit_cast(float, (uint32_t)static_cast<const uint16_t*>(a.logits)[i] << 16);
 }
 
-// The token's experts and weights: in lane j < top_k the j-th.
+// What a lane reads of a token's row: its VPL experts' logits, all loads at once.
 template <bool F32, int VPL>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int64_t t, int& id, float& weight) {
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int64_t t, float (&x)[VPL]) {
     const int lane = threadIdx.x & 63, E = a.experts;
-    float x[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; i++) {
-        const int e = lane * VPL + i;
-        x[i] = e < E ? logit_at<F32>(a, t * E + e) : -__builtin_inff();
-    }
-    if (!choose<float, VPL>(a, x, id)) choose<double, VPL>(a, x, id);
-    // weights: lane j's own logit
-    const double NEG = -__builtin_inf();
-    const double own = id >= 0 ? (double)logit_at<F32>(a, t * E + id) : NEG;
-    double share;
-    if (a.sigmoid) {
-        share = id >= 0 ? 1.0 / (1.0 + exp(-own)) : 0.0;
-    } else {
-        double most = own;
-        if (!a.renormalize) {
+    for (int i = 0; i < VPL; i++) x[i] = logit_at<F32>(a, t * E + min(lane * VPL + i, E - 1));
+}
+template <int VPL>
+__device__ __forceinline__ void load_bias(const RouteArgs& a, float (&bias)[VPL]) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-            for (int i = 0; i < VPL; i++) most = larger(most, x[i] > -__builtin_inff() ? (double)x[i] : NEG);
-        }
-        most = wave_most(most);
-        share = id < 0 ? 0.0 : own == most ? 1.0 : exp(own - most);
-        if (!a.renormalize) {
-            double sum = 0.0;
-#pragma unroll
-            for (int i = 0; i < VPL; i++)
-                if (x[i] > -__builtin_inff()) sum += (double)x[i] == most ? 1.0 : exp((double)x[i] - most);
-            sum = wave_total(sum);
-            share = sum > 0.0 ? share / sum : 0.0;
-        }
-    }
-    if (a.renormalize) {
-        const double sum = wave_total(share);
-        share = sum > 0.0 ? share / sum : 0.0;
-    }
-    weight = (float)(share * (double)a.scale);
+    for (int i = 0; i < VPL; i++) bias[i] = a.bias ? a.bias[min(lane * VPL + i, a.experts - 1)] : 0.0f;
 }
 
-// Bit t of the masks of the token's experts, and its results.
-__device__ __forceinline__ void note(const RouteArgs& a, int64_t token, int t, int id, float weight, unsigned long long* mask) {
-    const int lane = threadIdx.x & 63;
-    if (lane < a.top_k) {
-        a.ids[token * a.top_k + lane] = id;
-        a.weights[token * a.top_k + lane] = weight;
-        if (id >= 0) atomicOr(&mask[id], 1ull << t);
+// Over aligned groups of `width` lanes (a power of two), in every lane.
+__device__ __forceinline__ double group_most(double v, int width) {
+    for (int off = 1; off < width; off <<= 1) v = larger(v, __shfl_xor(v, off, 64));
+    return v;
+}
+__device__ __forceinline__ double group_total(double v, int width) {
+    for (int off = 1; off < width; off <<= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// Tokens first + wave, first + wave + WAVES, ... below `end` of this workgroup's
+// run.  The next one's logits are on their way while one is worked out.  The
+// weights, in fp64, are worked out for as many tokens at once as fit a wave, a
+// token in `wide` lanes, the power of two that holds top_k.
+template <bool F32, int VPL>
+__device__ __forceinline__ void route_run(const RouteArgs& a, int64_t first, int end, int wide, unsigned long long* mask) {
+    constexpr int WAVES = rt_waves(VPL);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const double NEG = -__builtin_inf();
+    if (wave >= end) return;
+    float bias[VPL], next[VPL];
+    load_bias<VPL>(a, bias);
+    load_logits<F32, VPL>(a, first + wave, next);
+    for (int u0 = wave; u0 < end; u0 += WAVES * (64 / wide)) {
+        int id = -1;
+        float logit = 0.0f;
+        double most = NEG, total = 0.0;                   // of the softmax over all experts, where it is needed
+        for (int at = 0; at < 64; at += wide) {
+            const int u = u0 + WAVES * (at / wide);
+            if (u >= end) break;
+            float x[VPL];
+#pragma unroll
+            for (int i = 0; i < VPL; i++) x[i] = lane * VPL + i < a.experts ? next[i] : -__builtin_inff();
+            load_logits<F32, VPL>(a, first + min(u + WAVES, end - 1), next);
+            if (!choose<float, VPL>(a, x, bias, at, id)) choose<double, VPL>(a, x, bias, at, id);
+            const bool here = lane >= at && lane < at + wide;
+#pragma unroll
+            for (int i = 0; i < VPL; i++) {
+                const float v = __shfl(x[i], id >= 0 ? id / VPL : 0, 64);
+                logit = here && id >= 0 && id % VPL == i ? v : logit;
+            }
+            if (!a.sigmoid && !a.renormalize) {
+                double m = NEG, sum = 0.0;
+#pragma unroll
+                for (int i = 0; i < VPL; i++) m = larger(m, x[i] > -__builtin_inff() ? (double)x[i] : NEG);
+                m = wave_most(m);
+#pragma unroll
+                for (int i = 0; i < VPL; i++)
+                    if (x[i] > -__builtin_inff()) sum += (double)x[i] == m ? 1.0 : exp((double)x[i] - m);
+                sum = wave_total(sum);
+                most = here ? m : most, total = here ? sum : total;
+            }
+        }
+        const double own = id >= 0 ? (double)logit : NEG;
+        double share;
+        if (a.sigmoid) {
+            share = id >= 0 ? 1.0 / (1.0 + exp(-own)) : 0.0;
+        } else {
+            if (a.renormalize) most = group_most(own, wide);
+            // the largest itself without a difference, which is NaN between infinities
+            share = id < 0 ? 0.0 : own == most ? 1.0 : exp(own - most);
+        }
+        if (a.renormalize) total = group_total(share, wide);
+        if (a.renormalize || !a.sigmoid) share = total > 0.0 ? share / total : 0.0;
+        const int u = u0 + WAVES * (lane / wide), j = lane & (wide - 1);
+        if (u < end && j < a.top_k) {
+            const int64_t i = (first + u) * a.top_k + j;
+            a.ids[i] = id;
+            a.weights[i] = (float)(share * (double)a.scale);
+            if (id >= 0) atomicOr(&mask[id], 1ull << u);
+        }
     }
 }
 
@@ -317,20 +411,16 @@ __device__ __forceinline__ void place(const RouteArgs& a, int64_t first, int i, 
 
 // Experts and weights of a run of tokens, and how many rows each expert gets of it.
 template <bool F32, int VPL>
-__global__ __launch_bounds__(RT_THREADS) void route_tokens(RouteArgs a, int run) {
+__global__ __launch_bounds__(64 * rt_waves(VPL)) void route_tokens(RouteArgs a, int run, int wide) {
+    constexpr int THREADS = 64 * rt_waves(VPL);
     __shared__ unsigned long long mask[RT_MAX_EXPERTS];
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    for (int e = tid; e < a.experts; e += RT_THREADS) mask[e] = 0;
+    const int tid = threadIdx.x;
+    for (int e = tid; e < a.experts; e += THREADS) mask[e] = 0;
     __syncthreads();
     const int64_t first = (int64_t)blockIdx.x * run;
-    for (int u = wave; u < run && first + u < a.tokens; u += RT_WAVES) {
-        int id;
-        float w;
-        route_token<F32, VPL>(a, first + u, id, w);
-        note(a, first + u, u, id, w, mask);
-    }
+    route_run<F32, VPL>(a, first, (int)min((int64_t)run, a.tokens - first), wide, mask);
     __syncthreads();
-    for (int e = tid; e < a.experts; e += RT_THREADS) a.workspace[(int64_t)blockIdx.x * a.experts + e] = __popcll(mask[e]);
+    for (int e = tid; e < a.experts; e += THREADS) a.workspace[(int64_t)blockIdx.x * a.experts + e] = __popcll(mask[e]);
 }
 
 // Counts of each run -> rows of the runs before it, expert by expert, and the totals.
@@ -393,29 +483,35 @@ __global__ __launch_bounds__(RT_PLACE) void route_place(RouteArgs a, int run, in
 
 // Up to 64 tokens: everything in one workgroup.
 template <bool F32, int VPL>
-__global__ __launch_bounds__(RT_THREADS) void route_small(RouteArgs a) {
+__global__ __launch_bounds__(64 * rt_waves(VPL)) void route_small(RouteArgs a, int wide) {
+    constexpr int THREADS = 64 * rt_waves(VPL), PER = RT_MAX_EXPERTS / THREADS;
     __shared__ int base[RT_MAX_EXPERTS];
-    __shared__ int part[RT_WAVES];
+    __shared__ int part[rt_waves(VPL)];
     __shared__ unsigned long long mask[RT_MAX_EXPERTS];
-    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), E = a.experts;
-    for (int e = tid; e < E; e += RT_THREADS) mask[e] = 0;
+    const int tid = threadIdx.x, E = a.experts;
+    for (int e = tid; e < E; e += THREADS) mask[e] = 0;
     __syncthreads();
-    for (int u = wave; u < a.tokens; u += RT_WAVES) {
-        int id;
-        float w;
-        route_token<F32, VPL>(a, u, id, w);
-        note(a, u, u, id, w, mask);
+    route_run<F32, VPL>(a, 0, a.tokens, wide, mask);
+    __syncthreads();
+    int own[PER], sum = 0, total;
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        const int e = tid * PER + i;
+        own[i] = e < E ? __popcll(mask[e]) : 0;
+        sum += own[i];
     }
-    __syncthreads();
-    static_assert(RT_MAX_EXPERTS <= RT_THREADS, "a thread an expert");
-    int total;
-    const int at = before_threads<RT_THREADS>(tid < E ? __popcll(mask[tid]) : 0, part, total);
-    if (tid < E) base[tid] = a.expert_start[tid] = at;
+    int at = before_threads<THREADS>(sum, part, total);
+#pragma unroll
+    for (int i = 0; i < PER; i++) {
+        const int e = tid * PER + i;
+        if (e < E) base[e] = a.expert_start[e] = at;
+        at += own[i];
+    }
     if (tid == 0) a.expert_start[E] = total;
     __syncthreads();
     const int entries = a.tokens * a.top_k;
     // ids from this workgroup's own stores (ordered by the barriers)
-    for (int i = tid; i < entries; i += RT_THREADS) place(a, 0, i, a.ids[i], base, mask, total);
+    for (int i = tid; i < entries; i += THREADS) place(a, 0, i, a.ids[i], base, mask, total);
 }
 
 struct RoutePlan {
@@ -423,7 +519,7 @@ struct RoutePlan {
 };
 static RoutePlan route_plan(const RouteArgs& a) {
     if (a.tokens <= RT_SMALL) return {RT_RUN, 0};
-    int run = RT_WAVES;                  // a token a wave, until the card is full of runs
+    int run = 16;                        // a token a wave, until the card is full of runs
     while (run < RT_RUN && (int64_t)run * 256 < a.tokens) run *= 2;
     return {run, (a.tokens + run - 1) / run};
 }
@@ -436,11 +532,13 @@ int64_t moe_route_bytes(const RouteArgs& a) {
 template <bool F32, int VPL>
 static hipError_t queue_route(const RouteArgs& a, hipStream_t stream) {
     const RoutePlan p = route_plan(a);
+    int wide = 1;
+    while (wide < a.top_k) wide *= 2;
     if (p.runs == 0) {
-        route_small<F32, VPL><<<dim3(1), dim3(RT_THREADS), 0, stream>>>(a);
+        route_small<F32, VPL><<<dim3(1), dim3(64 * rt_waves(VPL)), 0, stream>>>(a, wide);
         return hipGetLastError();
     }
-    route_tokens<F32, VPL><<<dim3((unsigned)p.runs), dim3(RT_THREADS), 0, stream>>>(a, p.run);
+    route_tokens<F32, VPL><<<dim3((unsigned)p.runs), dim3(64 * rt_waves(VPL)), 0, stream>>>(a, p.run, wide);
     route_counts<<<dim3((unsigned)((a.experts + RT_PLACE / 64 - 1) / (RT_PLACE / 64))), dim3(RT_PLACE), 0, stream>>>(a, p.runs);
     route_place<<<dim3((unsigned)p.runs), dim3(RT_PLACE), 0, stream>>>(a, p.run, p.runs);
     return hipGetLastError();
