@@ -117,7 +117,7 @@ int add_rms_norm_quantize(const void* x, int64_t x_stride, const void* residual,
         for (int j = 0; j < i; j++)
             if (overlaps(out[i], out[j])) return FP8G_ERR_OVERLAP;
     }
-    const NormArgs a = {x, residual, weight, sum, norm, q, scale, x_stride, residual_stride, (int32_t)rows, (int32_t)cols, eps};
+    const NormArgs a = {x, residual, weight, sum, norm, q, scale, x_stride, residual_stride, (int32_t)rows, (int32_t)cols, eps, 1.0 / (double)cols};
     return hip_status(launch_add_rms_norm(a, in_dtype == FP8G_IN_F32, mx, out_fmt == FP8G_FMT_E5M2, stream));
 }
 

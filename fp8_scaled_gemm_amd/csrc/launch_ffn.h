@@ -16,6 +16,7 @@ struct NormArgs {
     int64_t x_stride, residual_stride;   // elements
     int32_t rows, cols;
     float eps;
+    double inv_cols;
 };
 hipError_t launch_add_rms_norm(const NormArgs& a, int f32, int mx, int e5m2, hipStream_t stream);
 

@@ -57,18 +57,16 @@ typedef enum {
  * product that reads it.
  *
  *   s = round_in_dtype(x + residual)        (s = x where residual is NULL)
- *   y = s / sqrt(mean_c s_c^2 + eps) * weight_c                (fp32)
- *   per row (FP8G_SCALE_PER_ROW): scale[r] = fp32(max_c |y| / MAX), q = RNE_SAT(y / scale[r]),
+ *   y = s / sqrt(mean_c s_c^2 + eps) * weight_c
+ *   per row (FP8G_SCALE_PER_ROW): scale[r] = fp32(max_c |y| / MAX), q = RNE_SAT(y * MAX / max_c |y|),
  *       MAX and RNE_SAT as in fp8_quantize_ex for out_fmt
  *   MX (FP8G_SCALE_MX): q and scale codes of y as in mxfp8_quantize (E4M3 only)
- * The codes are those that fp8_quantize_ex / mxfp8_quantize give for the
- * fp32 y.  y differs from its exact value by at most (10 + cols / 512) * 2^-24
- * of it: the two products, the mean, the root and its reciprocal, and half the
- * error of a sum that no square passes through more than cols / 256 + 8
- * additions of.
+ * with everything behind s in fp64 (within 2^-48) and one rounding each to
+ * scale, norm and codes.  A scale of 0 gives
+ * signed zeros.
  * A row whose sum of squares is no finite number (it holds a NaN or an
- * infinity, or values past 2^64) has codes 0 with the scale NaN (MX: codes 255),
- * and NaN in norm; the others are not touched by it.
+ * infinity) has codes 0 with the scale NaN (MX: codes 255), and NaN in norm;
+ * the others are not touched by it.
  *
  * x        device, [rows, cols] of in_dtype (fp8g_in_t), rows x_stride elements apart
  * residual device, the same type, rows residual_stride elements apart, or NULL

@@ -18,13 +18,6 @@ def rms_norm(s, weight, eps):
     return y if weight is None else y * np.asarray(weight, np.float64)
 
 
-def rms_norm_error(cols):
-    """Relative error of the fp32 y: the two products, the mean, the root and its
-    reciprocal (about two half steps each where the hardware's form is a step off), and half
-    the error of a sum that no square passes through more than cols / 256 + 8 additions of."""
-    return (10 + cols / 512) * EPS32
-
-
 def activate(z, act):
     if act == "silu":
         p = z
