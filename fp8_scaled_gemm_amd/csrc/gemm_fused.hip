@@ -35,7 +35,7 @@ __global__ __launch_bounds__(NTHREADS, 1) void gemm_fused_kernel(int M, int N, i
 template <bool MX, bool OUT_F32, bool KTAIL, int TILE, int EPI, bool MOE>
 static hipError_t launch_tile(const FusedArgs& a, const TileLaunch& t, hipStream_t stream) {
     auto kern = gemm_fused_kernel<MX, OUT_F32, KTAIL, TILE, EPI, MOE>;
-    constexpr int LDS_BYTES = Ring<MX, KTAIL, TILE>::LDS_TOTAL;
+    constexpr int LDS_BYTES = Ring<MX, false, TILE>::LDS_TOTAL;
     // above the default launch limit: raised once per device; setting it twice
     // from racing threads is harmless
     static std::atomic<uint64_t> configured{0};
@@ -108,6 +108,40 @@ static hipError_t launch_fused(const FusedArgs& a, const TileLaunch& t, hipStrea
 
 constexpr int PLAN_THREADS = 256, PLAN_EXPERTS = 1024;
 
+// ---- scale rows of whole dwords, for K not a multiple of 128: 4 bytes for each
+// 128 of K, those behind the row 2^0 (the codes there are read as zeros).  A few
+// percent of the operands' bytes, where fetching the odd bytes one by one in the
+// product halved its rate.
+struct PadArgs {
+    const uint8_t* from[2];
+    uint8_t* to[2];
+    int64_t rows[2];
+    int nblk, words;             // bytes of a row, dwords of a padded one
+};
+__device__ __forceinline__ uint32_t padded_word(const uint8_t* row, int c, int nblk) {
+    const uint32_t w = scale_word(row, c, nblk), left = (uint32_t)max(nblk - 4 * c, 0);
+    return left >= 4 ? w : (w & ((1u << (8 * left)) - 1u)) | (0x7F7F7F7Fu << (8 * left));
+}
+__global__ __launch_bounds__(PLAN_THREADS) void pad_scales(PadArgs p) {
+    const int side = blockIdx.y;
+    const int64_t total = p.rows[side] * p.words, step = (int64_t)gridDim.x * PLAN_THREADS;
+    for (int64_t i = (int64_t)blockIdx.x * PLAN_THREADS + threadIdx.x; i < total; i += step) {
+        const int64_t r = i / p.words;
+        const int c = (int)(i - r * p.words);
+        reinterpret_cast<uint32_t*>(p.to[side])[i] = padded_word(p.from[side] + r * p.nblk, c, p.nblk);
+    }
+}
+static hipError_t launch_pad(const PadArgs& p, hipStream_t stream) {
+    const int64_t most = (p.rows[0] > p.rows[1] ? p.rows[0] : p.rows[1]) * p.words;
+    int64_t blocks = (most + PLAN_THREADS - 1) / PLAN_THREADS;
+    if (blocks > 4096) blocks = 4096;
+    pad_scales<<<dim3((unsigned)blocks, 2), dim3(PLAN_THREADS), 0, stream>>>(p);
+    return hipGetLastError();
+}
+// bytes of a padded scale row; 0: the rows are whole dwords already
+static int64_t pad_pitch(const FusedArgs& a) { return a.mx && a.k % BK ? (a.k + BK - 1) / BK * 4 : 0; }
+static int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
+
 // One workgroup per possible tile row t: every one counts the experts' tile
 // rows (an expert of c slots has ceil(c / bm)); the expert that holds t writes it down.
 __global__ __launch_bounds__(PLAN_THREADS) void moe_plan(const int32_t* __restrict__ start, const int32_t* __restrict__ rows,
@@ -170,20 +204,11 @@ __global__ __launch_bounds__(PLAN_THREADS) void moe_plan(const int32_t* __restri
         row_at[(int64_t)t * bm + r] = off;
     }
     if (!mx) return;
-    const int nblk = k / 32;
-    if (nblk % 4 == 0) {
-        const int nw = nblk / 4;
-        for (int i = tid; i < here * nw; i += PLAN_THREADS) {
-            const int r = i / nw, a = min(max(rows[m0 + r], 0), a_rows - 1);
-            static_cast<uint32_t*>(scale)[(int64_t)(m0 + r) * nw + i % nw] =
-                static_cast<const uint32_t*>(sa)[(int64_t)a * nw + i % nw];
-        }
-    } else {
-        for (int i = tid; i < here * nblk; i += PLAN_THREADS) {
-            const int r = i / nblk, a = min(max(rows[m0 + r], 0), a_rows - 1);
-            static_cast<uint8_t*>(scale)[(int64_t)(m0 + r) * nblk + i % nblk] =
-                static_cast<const uint8_t*>(sa)[(int64_t)a * nblk + i % nblk];
-        }
+    const int nblk = k / 32, nw = (k + BK - 1) / BK;      // whole dwords a row
+    for (int i = tid; i < here * nw; i += PLAN_THREADS) {
+        const int r = i / nw, a = min(max(rows[m0 + r], 0), a_rows - 1);
+        static_cast<uint32_t*>(scale)[(int64_t)(m0 + r) * nw + i % nw] =
+            padded_word(static_cast<const uint8_t*>(sa) + (int64_t)a * nblk, i % nw, nblk);
     }
 }
 
@@ -234,7 +259,7 @@ static FusedPlan fused_plan(const FusedArgs& a, int cus) {
     const double hbm = 6.0 + work / 5.3e6;
     auto consider = [&](const TileCost& c) {
         // 256x256 tiles only where they hold their registers (fp32 output: 256x128 then)
-        if (c.tile == 256 && (a.mx || a.k % BK)) return;
+        if (c.tile == 256 && (a.mx || a.k % BK || a.n % 8)) return;
         const int64_t tiles = ((a.m + tile_bm(c.tile) - 1) / tile_bm(c.tile)) * ((b_rows + tile_bn(c.tile) - 1) / tile_bn(c.tile));
         const int64_t rounds = (tiles + cus - 1) / cus;
         const double stage = 2 * tiles <= cus ? c.idle_stage : c.stage;
@@ -261,16 +286,19 @@ static FusedPlan fused_plan(const FusedArgs& a, int cus) {
 
 constexpr int PLAN_CUS = 256;    // the workspace's size may not hang on a device
 
+// Partial sums; behind them the padded scale rows of A and B.
 struct PartSpace {
-    int64_t rows, pitch, bytes;
+    int64_t rows, pitch, scale_a, scale_b, bytes;
 };
 static PartSpace part_space(const FusedArgs& a, const FusedPlan& p) {
     PartSpace s = {};
-    if (p.ranges < 2) return s;
+    if (!p.tile) return s;
     const int bm = tile_bm(p.tile), bn = tile_bn(p.tile);
     s.rows = (a.m + bm - 1) / bm * bm;
     s.pitch = ((a.gated ? 2 * a.n : a.n) + bn - 1) / bn * bn;
-    s.bytes = p.ranges * s.rows * s.pitch * 4;
+    s.scale_a = p.ranges > 1 ? p.ranges * s.rows * s.pitch * 4 : 0;
+    s.scale_b = s.scale_a + up16(a.m * pad_pitch(a));
+    s.bytes = s.scale_b + up16((a.gated ? 2 * a.n : a.n) * pad_pitch(a));
     return s;
 }
 int64_t gemm_fused_bytes(const FusedArgs& a) { return part_space(a, fused_plan(a, PLAN_CUS)).bytes; }
@@ -352,7 +380,7 @@ static int moe_tile(const FusedArgs& a) {
     int best = 0;
     double best_us = 0.0;
     auto consider = [&](const TileCost& c) {
-        if (c.tile == 256 && a.k % BK) return;
+        if (c.tile == 256 && (a.k % BK || a.n % 8)) return;
         double rows = (double)a.m / (double)a.experts / tile_bm(c.tile) + 0.5;      // of an expert
         if (rows < 1.0) rows = 1.0;
         const double tiles = rows * (double)a.experts * (double)((b_rows + tile_bn(c.tile) - 1) / tile_bn(c.tile));
@@ -369,7 +397,7 @@ static int moe_tile(const FusedArgs& a) {
 }
 
 struct MoeSpace {
-    int64_t tile_rows, row_at, scale, bytes;      // byte offsets behind the plan, which comes first
+    int64_t tile_rows, row_at, scale, scale_b, bytes;      // byte offsets; the plan comes first
 };
 static MoeSpace moe_space(const FusedArgs& a) {
     const int bm = tile_bm(moe_tile(a));
@@ -377,7 +405,9 @@ static MoeSpace moe_space(const FusedArgs& a) {
     s.tile_rows = a.m / bm + a.experts;           // at most: sum of ceil(c / bm)
     s.row_at = (16 * (1 + s.tile_rows) + 255) / 256 * 256;
     s.scale = s.row_at + (a.rows ? 4 * bm * s.tile_rows : 0);
-    s.bytes = s.scale + (a.rows ? (a.m * (a.mx ? a.k / 32 : 4) + 15) / 16 * 16 : 0);
+    const int64_t pad = pad_pitch(a);
+    s.scale_b = s.scale + (a.rows || pad ? up16(a.m * (!a.mx ? 4 : pad ? pad : a.k / 32)) : 0);
+    s.bytes = s.scale_b + a.experts * (a.gated ? 2 * a.n : a.n) * pad;
     return s;
 }
 
@@ -393,13 +423,22 @@ static hipError_t launch_product(const FusedArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     t.tile = p.tile == 256 && a.f32 ? TILE_256x128 : p.tile;
     t.scale_a = a.scale_a;
-    const int64_t tiles = ((a.m + tile_bm(p.tile) - 1) / tile_bm(p.tile)) *
-                          (((a.gated ? 2 * a.n : a.n) + tile_bn(p.tile) - 1) / tile_bn(p.tile));
-    if (p.ranges * tiles > t.cus) p.ranges = 1;      // a device of fewer CUs: an item a workgroup would not fit
-    if (p.ranges == 1) return a.mx ? launch_fused<true, false>(a, t, stream) : launch_fused<false, false>(a, t, stream);
+    const int64_t b_rows = a.gated ? 2 * a.n : a.n;
+    const int64_t tiles = ((a.m + tile_bm(p.tile) - 1) / tile_bm(p.tile)) * ((b_rows + tile_bn(p.tile) - 1) / tile_bn(p.tile));
     const PartSpace s = part_space(a, p);
-    FusedArgs g = a;             // the plain product of all of B's rows
-    g.n = a.gated ? 2 * a.n : a.n, g.gated = 0, g.f32 = 1;
+    if (p.ranges * tiles > t.cus) p.ranges = 1;      // a device of fewer CUs: an item a workgroup would not fit
+    FusedArgs g = a;
+    if (pad_pitch(a)) {
+        uint8_t *ws = static_cast<uint8_t*>(a.workspace), *pa = ws + s.scale_a, *pb = ws + s.scale_b;
+        const PadArgs pad = {{static_cast<const uint8_t*>(a.scale_a), static_cast<const uint8_t*>(a.scale_b)}, {pa, pb},
+                             {a.m, b_rows}, (int)(a.k / 32), (int)(pad_pitch(a) / 4)};
+        e = launch_pad(pad, stream);
+        if (e != hipSuccess) return e;
+        t.scale_a = pa, g.scale_b = pb;
+    }
+    if (p.ranges == 1) return a.mx ? launch_fused<true, false>(g, t, stream) : launch_fused<false, false>(g, t, stream);
+    // the plain product of all of B's rows
+    g.n = b_rows, g.gated = 0, g.f32 = 1;
     g.bias = nullptr, g.residual = nullptr, g.D = a.workspace;
     t.ranges = p.ranges, t.pitch = (int32_t)s.pitch, t.part_rows = (int32_t)s.rows;
     e = a.mx ? launch_fused_part<true, false, EPI_PARTIAL>(g, t, stream) : launch_fused_part<false, false, EPI_PARTIAL>(g, t, stream);
@@ -433,7 +472,17 @@ hipError_t launch_gemm_fused(const FusedArgs& a, hipStream_t stream) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (t.tile == 256 && a.f32) t.tile = TILE_256x128;      // the same rows a tile
-    return a.mx ? launch_fused<true, true>(a, t, stream) : launch_fused<false, true>(a, t, stream);
+    FusedArgs g = a;
+    if (pad_pitch(a)) {
+        // A's rows, too, unless the plan has put them in order already
+        PadArgs pad = {{static_cast<const uint8_t*>(a.scale_a), static_cast<const uint8_t*>(a.scale_b)},
+                       {ws + s.scale, ws + s.scale_b}, {a.rows ? 0 : a.m, a.experts * (a.gated ? 2 * a.n : a.n)},
+                       (int)(a.k / 32), (int)(pad_pitch(a) / 4)};
+        e = launch_pad(pad, stream);
+        if (e != hipSuccess) return e;
+        t.scale_a = ws + s.scale, g.scale_b = ws + s.scale_b;
+    }
+    return a.mx ? launch_fused<true, true>(g, t, stream) : launch_fused<false, true>(g, t, stream);
 }
 #endif  // FP8G_FUSED_PART == 0
 

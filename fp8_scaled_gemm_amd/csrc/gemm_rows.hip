@@ -112,18 +112,21 @@ __global__ __launch_bounds__(RW_THREADS, WPE) void gemm_rows_kernel(RowsArgs arg
     // r's, or nullptr
     const int pitch = scale_pitch(nblk);
     auto fetch_scales = [&](int at, int rows, auto from) __attribute__((always_inline)) {
-        auto copy = [&](auto unit) __attribute__((always_inline)) {
-            using U = decltype(unit);
-            const int per = nblk / (int)sizeof(U);
+        if (nblk % 16 == 0) {
+            const int per = nblk / 16;
             for (int i = threadIdx.x; i < rows * per; i += RW_THREADS) {
                 const int r = i / per, c = i - r * per;
                 const uint8_t* p = from(r);
-                if (p) reinterpret_cast<U*>(scales + (at + r) * pitch)[c] = reinterpret_cast<const U*>(p)[c];
+                if (p) reinterpret_cast<v4u*>(scales + (at + r) * pitch)[c] = reinterpret_cast<const v4u*>(p)[c];
             }
-        };
-        if (nblk % 16 == 0) copy(v4u{});
-        else if (nblk % 4 == 0) copy(uint32_t{});
-        else copy(uint8_t{});
+            return;
+        }
+        const int per = (nblk + 3) / 4;
+        for (int i = threadIdx.x; i < rows * per; i += RW_THREADS) {
+            const int r = i / per, c = i - r * per;
+            const uint8_t* p = from(r);
+            if (p) reinterpret_cast<uint32_t*>(scales + (at + r) * pitch)[c] = scale_word(p, c, nblk);
+        }
     };
     if constexpr (SC_LDS) {
         fetch_scales(0, 16 * NB, [&](int r) {

@@ -293,13 +293,18 @@ __device__ __forceinline__ void gemm_tiles(
     static_assert(!SPLIT || (!MX && !KTAIL && TILE == 128), "K splits: mode (a), whole stages, 128x128 tiles");
     static_assert(!SPLIT || EPI == EPI_NONE, "no K splits of fused products");
     constexpr bool GATED = EPI == EPI_GATED, PARTIAL = EPI == EPI_PARTIAL;
-    static_assert(!PARTIAL || (OUT_F32 && Ring<MX, KTAIL, TILE>::OWN_STAGE), "partial sums: fp32, staging of their own");
+    // fused products get scale rows of whole dwords (padded where K has a tail)
+    constexpr bool PADDED = MX && KTAIL && EPI != EPI_NONE;
+    using R = Ring<MX, KTAIL && !PADDED, TILE>;
+    static_assert(!PARTIAL || (OUT_F32 && R::OWN_STAGE), "partial sums: fp32, staging of their own");
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     using GEO = Geo<TILE>;
     constexpr int BM = GEO::BM, BN = GEO::BN, WTM = GEO::WTM, WTN = GEO::WTN, NBM = GEO::NBM, NBN = GEO::NBN;
     constexpr int NBX = NBM > NBN ? NBM : NBN;
     constexpr int BNO = GATED ? BN / 2 : BN;              // output columns of a tile
     constexpr int NBO = GATED ? NBN / 2 : NBN;            // blocks of them in a wave tile
+
+    constexpr bool RES = !MOE;                            // experts' products have no residual
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -310,7 +315,7 @@ __device__ __forceinline__ void gemm_tiles(
     const int tiles_m = MOE ? const_at(ex.plan)[0] : (M + BM - 1) / BM, tiles_n = (N + BNO - 1) / BNO;
     const int tiles = tiles_m * tiles_n, total = PARTIAL ? tiles * ex.ranges : tiles;
     const int nk = (K + BK - 1) / BK;            // stages per tile
-    const int nblk = K / 32;                     // MX scale bytes per row
+    const int nblk = PADDED ? 4 * nk : K / 32;   // MX scale bytes per row
 
     // ---- this workgroup's work items: XCD x = b % 8 owns a contiguous run of
     // tiles; its W_x workgroups take every W_x-th tile of the run.  SPLIT: only
@@ -394,7 +399,6 @@ __device__ __forceinline__ void gemm_tiles(
     // walks the items; descriptors change once per tile.  Past the end of the
     // stream the last stage is loaded again (never read), so every K step
     // issues the same number of loads.
-    using R = Ring<MX, KTAIL, TILE>;
     constexpr int NSLOT = R::NSLOT, SLOT = R::SLOT, LA = R::LA, LB = R::LB;
     static_assert(!R::PAIRED || LA == LB, "paired ring: square tiles");
     // loads of n consecutive items that start with an A item
@@ -426,20 +430,17 @@ __device__ __forceinline__ void gemm_tiles(
         rsB = panel(Be + (int64_t)p.n0 * K, rows_b * (uint32_t)K);
         if constexpr (GATED) rsU = panel(Be + (int64_t)(N + p.n0) * K, rows_b * (uint32_t)K);
         if constexpr (MOE) {
-            // load q of wave w takes the rows 32 q + 8 w + lane / 8: eight offsets of a
-            // wave are 32 bytes that the scalar cache gives at once, and a lane picks its
-            // own; a vector load would have to wait for the operand loads in flight
+            // load q of wave w takes the rows 32 q + 8 w + lane / 8.  One load for all of
+            // them, handed to their lanes by permutations, waits once for the operand loads
+            // in flight; scalar loads waited longer, for each q's (65536 rows of 128 experts
+            // x 2048 x 4096: 588 us, with scalar loads 636 us).
             if (gather) {
                 rsA = panel(A, ex.a_bytes);
-                const const_words at = const_at(ex.row_at) + (int64_t)tc.tm * BM + 8 * wave;
-                const int sub = lane >> 3;
+                const int at = 32 * min(lane >> 3, LA - 1) + 8 * wave + (lane & 7);
+                const int rows = (int)ex.row_at[(int64_t)tc.tm * BM + at];
 #pragma unroll
-                for (int q = 0; q < LA; ++q) {
-                    uint32_t v = (uint32_t)at[32 * q];
-#pragma unroll
-                    for (int s = 1; s < 8; ++s) v = sub == s ? (uint32_t)at[32 * q + s] : v;
-                    a_voff[q] = v + dma_chunk * 16u;
-                }
+                for (int q = 0; q < LA; ++q)
+                    a_voff[q] = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (8 * q + (lane >> 3)), rows) + dma_chunk * 16u;
             } else {
 #pragma unroll
                 for (int q = 0; q < LA; ++q) a_voff[q] = dma_voff + (uint32_t)(32 * q) * (uint32_t)K;
@@ -593,14 +594,10 @@ __device__ __forceinline__ void gemm_tiles(
                 }
             } else {
                 const Place p = place_of(tile_of(j));
-                const uint8_t* eb_e = MOE ? eb + (int64_t)p.expert * b_rows * nblk : eb;
-                const uint32_t cols = (uint32_t)min(BNO, N - p.n0);
+                static_assert(EPI == EPI_NONE, "fused products have scale groups");
                 const __amdgpu_buffer_rsrc_t pa = panel(ea + (int64_t)p.m0 * nblk, (uint32_t)p.rows * (uint32_t)nblk);
-                const __amdgpu_buffer_rsrc_t pb = panel(eb_e + (int64_t)p.n0 * nblk, cols * (uint32_t)nblk);
-                __amdgpu_buffer_rsrc_t pu = pb;
-                if constexpr (GATED) pu = panel(eb_e + (int64_t)(N + p.n0) * nblk, cols * (uint32_t)nblk);
-                // this lane half's block
-                const int kb = 4 * s + 2 * h + lhi + (PARTIAL ? 4 * item_of(0).kb : 0);
+                const __amdgpu_buffer_rsrc_t pb = panel(eb + (int64_t)p.n0 * nblk, (uint32_t)min(BN, N - p.n0) * (uint32_t)nblk);
+                const int kb = 4 * s + 2 * h + lhi;   // this lane half's block
                 const bool in = kb < nblk;
                 const uint32_t kc = (uint32_t)min(kb, nblk - 1);
 #pragma unroll
@@ -611,11 +608,8 @@ __device__ __forceinline__ void gemm_tiles(
                         xa[i] = in ? va : 127u;
                     }
                     if (i < NBN) {
-                        const uint32_t vb = GATED
-                            ? __builtin_amdgcn_raw_buffer_load_b8(
-                                  i < NBO ? pb : pu, (uint32_t)(32 * (wn * NBO + i % NBO) + l32) * (uint32_t)nblk + kc, 0, 0)
-                            : __builtin_amdgcn_raw_buffer_load_b8(
-                                  pb, (uint32_t)(wn * WTN + i * 32 + l32) * (uint32_t)nblk + kc, 0, 0);
+                        const uint32_t vb = __builtin_amdgcn_raw_buffer_load_b8(
+                            pb, (uint32_t)(wn * WTN + i * 32 + l32) * (uint32_t)nblk + kc, 0, 0);
                         xb[i] = in ? vb : 127u;
                     }
                 }
@@ -915,7 +909,14 @@ __device__ __forceinline__ void gemm_tiles(
 #pragma unroll
             for (int gq = 0; gq < 4; ++gq) {
                 const uint32_t n = (uint32_t)(p.n0 + 32 * (wn * NBO + i) + 8 * gq + 4 * lhie);
-                b[h][gq] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, 4u * n, 0, 0));
+                if (TILE == 256 || N % 4 == 0) {
+                    b[h][gq] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, 4u * n, 0, 0));
+                } else {
+                    // the last four may end inside
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        b[h][gq][t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, 4u * (n + t), 0, 0));
+                }
             }
         }
     };
@@ -954,73 +955,18 @@ __device__ __forceinline__ void gemm_tiles(
             else f(No{}, No{});
         }
     };
-    // from registers, any N
-    auto fused_direct = [&](int j, v16f (&acc)[NBN][NBM], uint32_t stage_off) __attribute__((always_inline)) {
+    // bf16 through LDS, as epilogue_staged: bands of 32 rows x CB blocks of 32
+    // columns (CB = 2, or 1 where the wave has one block of output columns), stored
+    // row-contiguously.  The residual takes the same way back: read
+    // row-contiguously, put into the band, and added by the lane that overwrites it
+    // there.  ANY: rows of any length, by units of 8 that start at any element and
+    // end at N.
+    auto fused_staged = [&](int j, v16f (&acc)[NBN][NBM], uint32_t stage_off, auto any_tag) __attribute__((always_inline)) {
         const Place p = place_of(tile_of(j));
-        const int lane_e = fresh_lane();
-        const int l32e = lane_e & 31, lhie = lane_e >> 5;
-        const float* lsa = reinterpret_cast<const float*>(smem + ts_off(stage_off));
-        const float* lsb = reinterpret_cast<const float*>(smem + ts_off(stage_off) + 1024);
-        const uint32_t bytes = (uint32_t)p.rows * (uint32_t)N * ESZ;
-        const __amdgpu_buffer_rsrc_t rsD = panel(reinterpret_cast<uint8_t*>(Dv) + (int64_t)p.m0 * N * ESZ, bytes);
-        const __amdgpu_buffer_rsrc_t rsR = panel(reinterpret_cast<const uint8_t*>(ex.residual) + (int64_t)p.m0 * N * ESZ, bytes);
-#pragma unroll
-        for (int i = 0; i < NBO; ++i) {
-            v4f b[GATED ? 2 : 1][4] = {};
-            if (ex.bias) {
-                // element by element: a row of the last tile may end inside four
-#pragma unroll
-                for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-                    const __amdgpu_buffer_rsrc_t rs =
-                        panel(ex.bias + (MOE ? (int64_t)p.expert * b_rows : 0) + (int64_t)h * N, (uint32_t)N * 4u);
-#pragma unroll
-                    for (int gq = 0; gq < 4; ++gq)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t)
-                            b[h][gq][t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                rs, 4u * (uint32_t)(p.n0 + 32 * (wn * NBO + i) + 8 * gq + 4 * lhie + t), 0, 0));
-                }
-            }
-#pragma unroll
-            for (int jb = 0; jb < NBM; ++jb) {
-                const int mr = wm * WTM + jb * 32 + l32e;
-                float smv = 1.0f;
-                if constexpr (!MX) smv = lsa[mr];
-#pragma unroll
-                for (int gq = 0; gq < 4; ++gq) {
-                    const int n = p.n0 + 32 * (wn * NBO + i) + 8 * gq + 4 * lhie;
-                    float v[4];
-                    if (ex.act.on) fused_values(acc, i, jb, gq, smv, lsb, lhie, b, true, true, v);
-                    else fused_values(acc, i, jb, gq, smv, lsb, lhie, b, true, false, v);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t off = (mr < p.rows && n + t < N) ? ((uint32_t)mr * (uint32_t)N + (uint32_t)(n + t)) * ESZ
-                                                                        : OOB_OFF;
-                        if constexpr (OUT_F32) {
-                            if (ex.residual)
-                                v[t] += __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsR, off, 0, 0));
-                            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v[t]), rsD, off, 0, 0);
-                        } else {
-                            if (ex.residual) {
-                                const uint32_t r = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsR, off, 0, 0);
-                                v[t] += __builtin_bit_cast(float, r << 16);
-                            }
-                            __builtin_amdgcn_raw_buffer_store_b16((unsigned short)bf16x2_bits(v[t], 0.0f), rsD, off, 0, 0);
-                        }
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
-        }
-    };
-    // bf16 through LDS (N % 8 == 0), as epilogue_staged: bands of 32 rows x CB
-    // blocks of 32 columns (CB = 2, or 1 where the wave has one block of output
-    // columns).  The residual takes the same way back: read row-contiguously,
-    // put into the band, and added by the lane that overwrites it there.
-    auto fused_staged = [&](int j, v16f (&acc)[NBN][NBM], uint32_t stage_off) __attribute__((always_inline)) {
-        const Place p = place_of(tile_of(j));
-        constexpr int CB = NBO >= 2 ? 2 : 1;               // blocks of a band
-        constexpr int CPR = 4 * CB, RPI = 64 / CPR;         // 16-byte chunks of a band row; rows of a store
+        constexpr int CB = NBO >= 2 ? 2 : 1;                 // blocks of a band
+        constexpr bool ANY = decltype(any_tag)::value;
+        constexpr int UPR = 4 * CB, RPI = 64 / UPR;   // units of a band row; rows of a store
+        constexpr int STEPS = 32 / RPI;
         const uint32_t bytes = (uint32_t)p.rows * (uint32_t)N * 2u;
         const __amdgpu_buffer_rsrc_t rsD = panel(reinterpret_cast<uint8_t*>(Dv) + (int64_t)p.m0 * N * 2, bytes);
         const __amdgpu_buffer_rsrc_t rsR = panel(reinterpret_cast<const uint8_t*>(ex.residual) + (int64_t)p.m0 * N * 2, bytes);
@@ -1033,31 +979,39 @@ __device__ __forceinline__ void gemm_tiles(
         // chunk c of row r in slot c ^ key(r); 8-byte halves swapped when r >= 16
         auto key = [](int r) { return CB == 2 ? (r >> 1) & 7 : (r >> 2) & 3; };
         const uint32_t wkey = (uint32_t)key(l32e), whalf = (uint32_t)(lhie ^ (l32e >> 4));
-        const int rc = lane_e & (CPR - 1), rr = lane_e / CPR;      // read-back: chunk, row within RPI
+        const int rc = lane_e & (UPR - 1), rr = lane_e / UPR;      // read-back: unit, row within RPI
         auto band = [&](int ih, int jb, const v4f (&b)[CB][GATED ? 2 : 1][4], auto bias_tag, auto act_tag)
                         __attribute__((always_inline)) {
             const int n = p.n0 + 32 * (wn * NBO + CB * ih) + 8 * rc;
             // branch-free select (a compare-and-select here becomes a branch)
             uint32_t keep = n < N ? 0xFFFFFFFFu : 0u;
             asm volatile("" : "+v"(keep));
-            uint32_t off[32 / RPI];
-#pragma unroll
-            for (int k = 0; k < 32 / RPI; ++k) {
-                const uint32_t mr = (uint32_t)(wm * WTM + jb * 32 + RPI * k + rr);   // row inside the tile
-                off[k] = ((mr * (uint32_t)N * 2u + (uint32_t)n * 2u) & keep) | (OOB_OFF & ~keep);
-            }
+            auto at = [&](int k) __attribute__((always_inline)) -> uint32_t {      // offset in the tile's rows
+                const uint32_t mr = (uint32_t)(wm * WTM + jb * 32 + RPI * k + rr);
+                return (((mr * (uint32_t)N + (uint32_t)n) * 2u) & keep) | (OOB_OFF & ~keep);
+            };
             auto slot = [&](int k) __attribute__((always_inline)) {
                 const int r = RPI * k + rr;
-                return st + r * (16 * CPR) + ((rc ^ key(r)) << 4);
+                return reinterpret_cast<v4u*>(st + r * (64 * CB) + ((rc ^ key(r)) << 4));
             };
-            if (ex.residual) {
-                v4u d[32 / RPI];
+            // element of D and of the residual where ANY unit k starts, how many of its 8 there are
+            auto first = [&](int k) __attribute__((always_inline)) {
+                return ((int64_t)p.m0 + wm * WTM + jb * 32 + RPI * k + rr) * N + n;
+            };
+            auto many = [&](int k) __attribute__((always_inline)) {
+                return wm * WTM + jb * 32 + RPI * k + rr < p.rows ? N - n : 0;
+            };
+            if (RES && ex.residual) {
+                v4u d[STEPS];
 #pragma unroll
-                for (int k = 0; k < 32 / RPI; ++k) d[k] = __builtin_amdgcn_raw_buffer_load_b128(rsR, off[k], 0, 0);
+                for (int k = 0; k < STEPS; ++k) {
+                    if constexpr (ANY) d[k] = load_some(reinterpret_cast<const uint16_t*>(ex.residual) + first(k), many(k));
+                    else d[k] = __builtin_amdgcn_raw_buffer_load_b128(rsR, at(k), 0, 0);
+                }
 #pragma unroll
-                for (int k = 0; k < 32 / RPI; ++k) {
+                for (int k = 0; k < STEPS; ++k) {
                     if (RPI * k >= 16) d[k] = (v4u){d[k].z, d[k].w, d[k].x, d[k].y};
-                    *reinterpret_cast<v4u*>(slot(k)) = d[k];
+                    *slot(k) = d[k];
                 }
             }
             float smv = 1.0f;
@@ -1069,21 +1023,24 @@ __device__ __forceinline__ void gemm_tiles(
                     float v[4];
                     fused_values(acc, CB * ih + ii, jb, gq, smv, lsb, lhie, b[ii], decltype(bias_tag)::value,
                                  decltype(act_tag)::value, v);
-                    v2u* at = reinterpret_cast<v2u*>(st + l32e * (16 * CPR) + (((uint32_t)(4 * ii + gq) ^ wkey) << 4) + whalf * 8);
-                    if (ex.residual) {
-                        const v2u r = *at;
+                    v2u* to = reinterpret_cast<v2u*>(st + l32e * (64 * CB) + (((uint32_t)(4 * ii + gq) ^ wkey) << 4) + whalf * 8);
+                    if (RES && ex.residual) {
+                        const v2u r = *to;
                         v[0] += __builtin_bit_cast(float, r.x << 16);
                         v[1] += __builtin_bit_cast(float, r.x & 0xFFFF0000u);
                         v[2] += __builtin_bit_cast(float, r.y << 16);
                         v[3] += __builtin_bit_cast(float, r.y & 0xFFFF0000u);
                     }
-                    *at = (v2u){bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
+                    *to = (v2u){bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])};
+                    // the 256x256 tile's waves have no registers for a second four
+                    if constexpr (TILE == 256) __builtin_amdgcn_sched_barrier(0);
                 }
 #pragma unroll
-            for (int k = 0; k < 32 / RPI; ++k) {
-                v4u d = *reinterpret_cast<const v4u*>(slot(k));
+            for (int k = 0; k < STEPS; ++k) {
+                v4u d = *slot(k);
                 if (RPI * k >= 16) d = (v4u){d.z, d.w, d.x, d.y};   // rows 16..31: halves swapped
-                __builtin_amdgcn_raw_buffer_store_b128(d, rsD, off[k], 0, ST_NT);
+                if constexpr (ANY) store_some(reinterpret_cast<uint16_t*>(Dv) + first(k), many(k), d);
+                else __builtin_amdgcn_raw_buffer_store_b128(d, rsD, at(k), 0, ST_NT);
             }
             __builtin_amdgcn_sched_barrier(0);
         };
@@ -1100,10 +1057,11 @@ __device__ __forceinline__ void gemm_tiles(
             }
         });
     };
-    // fp32 through LDS (mode (a), N % 32 == 0), as epilogue_staged_f32; the
-    // residual is added where the rows are stored.
-    auto fused_staged_f32 = [&](int j, v16f (&acc)[NBN][NBM], uint32_t stage_off) __attribute__((always_inline)) {
+    // fp32 through LDS, as epilogue_staged_f32; the residual is added where the
+    // rows are stored.  ANY: as above, by units of 4.
+    auto fused_staged_f32 = [&](int j, v16f (&acc)[NBN][NBM], uint32_t stage_off, auto any_tag) __attribute__((always_inline)) {
         const Place p = place_of(tile_of(j));
+        constexpr bool ANY = decltype(any_tag)::value;
         const uint32_t bytes = (uint32_t)p.rows * (uint32_t)N * 4u;
         const __amdgpu_buffer_rsrc_t rsD = panel(reinterpret_cast<uint8_t*>(Dv) + (int64_t)p.m0 * N * 4, bytes);
         const __amdgpu_buffer_rsrc_t rsR = panel(reinterpret_cast<const uint8_t*>(ex.residual) + (int64_t)p.m0 * N * 4, bytes);
@@ -1113,15 +1071,13 @@ __device__ __forceinline__ void gemm_tiles(
         const float* lsa = reinterpret_cast<const float*>(smem + ts_off(stage_off));
         const float* lsb = reinterpret_cast<const float*>(smem + ts_off(stage_off) + 1024);
         const uint32_t wkey = (uint32_t)((l32e >> 1) & 7);
-        const uint32_t rc = (uint32_t)(lane_e & 7);
-        const int rr = lane_e >> 3;
-        const uint32_t rd_off = (uint32_t)(rr * 128) + ((rc ^ (uint32_t)((rr >> 1) & 3)) << 4);
+        const int rc = lane_e & 7, rr = lane_e >> 3;
         fused_kind([&](auto bias_tag, auto act_tag) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < NBO; ++i) {
                 v4f b[GATED ? 2 : 1][4] = {};
                 if constexpr (decltype(bias_tag)::value) fused_bias(p, i, b, lhie);
-                const int n = p.n0 + 32 * (wn * NBO + i) + 4 * (int)rc;
+                const int n = p.n0 + 32 * (wn * NBO + i) + 4 * rc;
                 uint32_t keep = n < N ? 0xFFFFFFFFu : 0u;
                 asm volatile("" : "+v"(keep));
 #pragma unroll
@@ -1137,16 +1093,36 @@ __device__ __forceinline__ void gemm_tiles(
                     }
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        v4f d = *reinterpret_cast<const v4f*>(st + k * 1024 + (rd_off ^ (uint32_t)(64 * (k & 1))));
-                        const uint32_t mr = (uint32_t)(wm * WTM + jb * 32 + 8 * k + rr);   // row inside the tile
-                        const uint32_t off = ((mr * (uint32_t)N * 4u + (uint32_t)n * 4u) & keep) | (OOB_OFF & ~keep);
-                        if (ex.residual) d += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsR, off, 0, 0));
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, d), rsD, off, 0, ST_NT);
+                        const int r = 8 * k + rr, mr = wm * WTM + jb * 32 + r;            // row inside the tile
+                        v4f d = *reinterpret_cast<const v4f*>(st + r * 128 + ((rc ^ ((r >> 1) & 7)) << 4));
+                        if constexpr (ANY) {
+                            const int64_t first = ((int64_t)p.m0 + mr) * N + n;
+                            const int many = mr < p.rows ? N - n : 0;
+                            if (RES && ex.residual) d += __builtin_bit_cast(v4f, load_some(reinterpret_cast<const uint32_t*>(ex.residual) + first, many));
+                            store_some(reinterpret_cast<uint32_t*>(Dv) + first, many, __builtin_bit_cast(v4u, d));
+                        } else {
+                            const uint32_t off = ((((uint32_t)mr * (uint32_t)N + (uint32_t)n) * 4u) & keep) | (OOB_OFF & ~keep);
+                            if (RES && ex.residual) d += __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsR, off, 0, 0));
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4u, d), rsD, off, 0, ST_NT);
+                        }
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
         });
+    };
+    // 256x256 tiles are chosen for whole vectors only: their registers hold no more
+    auto fused_any = [&](int j, v16f (&acc)[NBN][NBM], uint32_t stage_off) __attribute__((always_inline)) {
+        auto staged = [&](auto any_tag) __attribute__((always_inline)) {
+            if constexpr (OUT_F32) fused_staged_f32(j, acc, stage_off, any_tag);
+            else fused_staged(j, acc, stage_off, any_tag);
+        };
+        if constexpr (TILE == 256) {
+            staged(std::false_type{});
+        } else {
+            if (N % (OUT_F32 ? 4 : 8) == 0) staged(std::false_type{});
+            else staged(std::true_type{});
+        }
     };
     // ---- partial sums (EPI_PARTIAL): the item's accumulators as they are, whole
     // tiles of rows of ex.pitch elements, through LDS as in epilogue_staged_f32
@@ -1188,16 +1164,10 @@ __device__ __forceinline__ void gemm_tiles(
     // rows of whole 128-byte lines (at N = 22012, rows straddling lines, staged
     // fp32 ran 4% slower than from registers; mode (b) with fp32 output staged
     // spilled in its main loop)
-    auto epilogue_any = [&](int j, v16f (&acc)[NBN][NBM], uint32_t stage_off) __attribute__((always_inline)) {
-        if constexpr (EPI != EPI_NONE) fused_direct(j, acc, stage_off);
-        else epilogue(j, acc, stage_off);
-    };
-    const bool staged = OUT_F32 ? (!MX && (N % 32) == 0) : (N % 8) == 0;
+    const bool staged = EPI != EPI_NONE || (OUT_F32 ? (!MX && (N % 32) == 0) : (N % 8) == 0);
     auto epilogue_staged_any = [&](int j, v16f (&acc)[NBN][NBM], uint32_t stage_off) __attribute__((always_inline)) {
-        if constexpr (EPI != EPI_NONE) {
-            if constexpr (OUT_F32) fused_staged_f32(j, acc, stage_off);
-            else fused_staged(j, acc, stage_off);
-        } else if constexpr (OUT_F32) epilogue_staged_f32(j, acc, stage_off);
+        if constexpr (EPI != EPI_NONE) fused_any(j, acc, stage_off);
+        else if constexpr (OUT_F32) epilogue_staged_f32(j, acc, stage_off);
         else epilogue_staged(j, acc, stage_off);
     };
 
@@ -1294,7 +1264,7 @@ __device__ __forceinline__ void gemm_tiles(
             wait_vmcnt<0>();
             __syncthreads();
             if (staged) epilogue_staged_any(j, acc, 0);
-            else epilogue_any(j, acc, 0);
+            else epilogue(j, acc, 0);
             __syncthreads();
         }
         return;
@@ -1508,7 +1478,7 @@ __device__ __forceinline__ void gemm_tiles(
                 wait_vmcnt<LI_LAST>();
                 __syncthreads();
             }
-            epilogue_any(j, acc, stage_off);
+            epilogue(j, acc, stage_off);
             if constexpr (!MX) __syncthreads();   // scale reads done before that slot is loaded again
         }
         // the next stage's step-0 fragments and scales (its items landed before

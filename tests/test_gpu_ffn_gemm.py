@@ -62,6 +62,23 @@ def test_fused_large(gpu_lib, m, n, k, mx, gated, dtype):
     case(gpu_lib, m, n, k, mx, "silu" if gated else "none", gated, bias=True, residual=True, dtype=dtype, wide=True)
 
 
+# K that ends inside a stage, rows of scales that are no whole dwords, rows of D that are no whole vectors
+@pytest.mark.parametrize("m,n,k", [(600, 1032, 672), (515, 2050, 160), (700, 1001, 992), (1400, 523, 1056), (129, 255, 4192), (80, 131, 8224)])
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_fused_tails(gpu_lib, m, n, k, mx, gated, dtype):
+    case(gpu_lib, m, n, k, mx, "silu" if gated else "none", gated, bias=n % 2 == 1, residual=True, dtype=dtype)
+
+
+# few tiles and a long K: partial sums of K ranges
+@pytest.mark.parametrize("m,n,k", [(64, 512, 8192), (200, 256, 6144), (33, 1000, 16384), (129, 130, 4160)])
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+def test_fused_long_k(gpu_lib, m, n, k, mx, gated):
+    case(gpu_lib, m, n, k, mx, "gelu_tanh" if gated else "none", gated, bias=True, residual=True, dtype=BF if n % 2 else F)
+
+
 @pytest.mark.parametrize("mx", [False, True])
 def test_fused_empty(gpu_lib, mx):
     call = call_of(gpu_lib, mx)
@@ -151,6 +168,13 @@ def test_experts(gpu_lib, S, E, n, k, mx, gated, how):
 @pytest.mark.parametrize("gather", [False, True])
 def test_experts_large(gpu_lib, S, E, n, k, mx, gather):
     experts_case(gpu_lib, S, E, n, k, mx, not gather, "even", gather, BF, True)
+
+
+@pytest.mark.parametrize("S,E,n,k", [(2000, 3, 264, 672), (1500, 2, 1001, 160), (600, 5, 130, 1056), (12, 4, 72, 1120)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+def test_experts_tails(gpu_lib, S, E, n, k, gather, gated):
+    experts_case(gpu_lib, S, E, n, k, True, gated, "gaps", gather, BF, True)
 
 
 def test_experts_wrong_indices_stay_inside(gpu_lib):
