@@ -181,14 +181,20 @@ TRAFFIC_FILES = {"ffn_up": "profiles/gemm_fp8_ffn_up_8192x22016x8192_hbm_traffic
                  "quantize": "profiles/quantize_rows_f32_e4m3_8192x8192_hbm_traffic.txt"}
 
 
+KERNEL_HEADERS = {"gemm.hip": ["gemm_tile.h"], "quantize.hip": ["row_div.h"]}    # that hold a part of the kernel's code
+
+
 def code_digest(name="gemm.hip"):
-    """sha256 of a kernel source file's code, without its comments and
-    whitespace: counters taken on another version of the code do not describe
-    the kernel being timed, while an edit of a comment changes nothing."""
+    """sha256 of a kernel's code (its source file and KERNEL_HEADERS), without
+    comments and whitespace: counters taken on another version of the code do
+    not describe the kernel being timed, while an edit of a comment changes
+    nothing."""
     import hashlib
     import re
-    with open(os.path.join(ROOT, "fp8_scaled_gemm_amd", "csrc", name)) as f:
-        text = f.read()
+    text = ""
+    for part in [name] + KERNEL_HEADERS.get(name, []):
+        with open(os.path.join(ROOT, "fp8_scaled_gemm_amd", "csrc", part)) as f:
+            text += f.read()
     text = re.sub(r"/\*.*?\*/", " ", text, flags=re.S)   # block comments
     text = re.sub(r"//[^\n]*", " ", text)                 # line comments
     return hashlib.sha256("".join(text.split()).encode()).hexdigest()

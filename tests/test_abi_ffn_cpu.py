@@ -138,7 +138,7 @@ def test_route_refusals(lib):
                 assert route(lib, **{name: P(j)}) == OVERLAP, (name, j)
     need = lib.moe_route_workspace(70, 64, 4)
     assert need > 0 and route(lib, size=need - 1) == UNSUPPORTED
-    assert lib.moe_route_workspace(64, 64, 4) == 0                  # one workgroup does it all
+    assert lib.moe_route_workspace(24, 64, 4) == 0                  # one workgroup does it all
     assert lib.moe_route_workspace(7, 64, 65) == -1 and lib.moe_route_workspace(7, 1025, 2) == -1
 
 
