@@ -70,7 +70,7 @@ typedef enum {
  *
  * x        device, [rows, cols] of in_dtype (fp8g_in_t), rows x_stride elements apart
  * residual device, the same type, rows residual_stride elements apart, or NULL
- * weight   device, fp32 [cols], or NULL: all ones
+ * weight   device, fp32 [cols], finite, or NULL: all ones
  * sum      device, [rows, cols] of in_dtype, dense, written with s, or NULL;
  *          may be x or residual itself, where that is dense
  * norm     device, [rows, cols] of in_dtype, dense, written with round(y), or NULL

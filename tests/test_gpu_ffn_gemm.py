@@ -94,6 +94,15 @@ def test_fused_empty(gpu_lib, mx):
     close(host(got), exact, rounded(exact, tol, F), "k = 0")
 
 
+@pytest.mark.parametrize("m,n", [(300, 200), (700, 1031)])
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("gated", [False, True])
+def test_no_k_of_many_rows(gpu_lib, m, n, mx, gated):
+    case(gpu_lib, m, n, 0, mx, "silu", gated, bias=True, residual=True, dtype=BF)
+    if not gated:
+        experts_case(gpu_lib, m, 3, n, 0, mx, False, "even", True, F, True)
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 def test_activations_over_their_range(gpu_lib, act):
     """k = 0 and a bias: the activation alone, from far negative to far positive."""
