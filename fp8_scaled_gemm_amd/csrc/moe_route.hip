@@ -277,8 +277,11 @@ __device__ __forceinline__ void route_run(const RouteArgs& a, int64_t first, int
 #pragma unroll
             for (int i = 0; i < VPL; i++) x[i] = lane * VPL + i < a.experts ? next[i] : -__builtin_inff();
             load_logits<F32, VPL>(a, first + min(u + WAVES, end - 1), next);
-            if (!choose<float, VPL>(a, x, bias, at, id)) choose<double, VPL>(a, x, bias, at, id);
             const bool here = lane >= at && lane < at + wide;
+            if (!choose<float, VPL>(a, x, bias, at, id)) {
+                id = here ? -1 : id;                      // fp64 may find fewer experts than fp32 did
+                choose<double, VPL>(a, x, bias, at, id);
+            }
 #pragma unroll
             for (int i = 0; i < VPL; i++) {
                 const float v = __shfl(x[i], id >= 0 ? id / VPL : 0, 64);

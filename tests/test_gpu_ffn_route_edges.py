@@ -1,0 +1,40 @@
+"""moe_route where the fp32 look at the choices and the fp64 one part, and where
+groups have few available experts: the definition, token by token."""
+
+import numpy as np
+import pytest
+
+from block_util import f32, rng
+from gpu_util import say
+from test_gpu_ffn_route import check
+
+pytestmark = pytest.mark.gpu
+
+
+# experts a lane: 1, 4, 8 and 16; groups of 8 (several lanes, or a lane), of 5 (lanes shared by two) and of 64
+SIZES = [(16, 2), (15, 3), (256, 32), (250, 50), (512, 64), (1024, 16)]
+
+
+@pytest.mark.parametrize("E,groups", SIZES)
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_groups_that_only_fp64_tells_apart(gpu_lib, E, groups, renormalize):
+    """All sigmoids are 1 in fp32, where the first group wins; in fp64 the second one does, which has two experts."""
+    width = E // groups
+    x = np.full((9, E), 20.0)
+    x[:, width:2 * width] = -np.inf
+    x[:, width:width + 2] = 21.0
+    x[1::3, 2 * width - 1] = np.nan
+    say("close groups", E, groups)
+    check(gpu_lib, *f32(x), 4, None, score="sigmoid", groups=groups, top_groups=1, renormalize=renormalize)
+
+
+@pytest.mark.parametrize("E,groups", SIZES)
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_close_groups_of_masked_experts(gpu_lib, E, groups, group_top):
+    """Whole logits of 20 to 32, whose sigmoids are 1 in fp32 and far apart in fp64, most of them masked."""
+    r = rng(E, groups, group_top)
+    x = r.integers(20, 33, (120, E)).astype(np.float64)
+    x[r.random(x.shape) < np.linspace(0.2, 1.0, 120)[:, None]] = -np.inf
+    say("masked groups", E, groups, group_top)
+    for top_groups in {1, 2, groups - 1}:
+        check(gpu_lib, *f32(x), 6, None, score="sigmoid", groups=groups, top_groups=top_groups, group_top=group_top)
