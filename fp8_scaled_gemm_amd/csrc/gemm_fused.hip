@@ -149,6 +149,11 @@ static int64_t up16(int64_t v) { return (v + 15) / 16 * 16; }
 
 // One workgroup per possible tile row t: every one counts the experts' tile
 // rows (an expert of c slots has ceil(c / bm)); the expert that holds t writes it down.
+// Ascending starts have disjoint experts, sum c <= slots, so that there are at most
+// slots / bm + experts tile rows, which is the grid (moe_space).  Starts that fall
+// again count slots twice and could have more: the plan ends with the grid, and the
+// tile kernel never walks past what is written here.  A planned row lies in [0,
+// slots) whatever the starts, as each end is clamped to its own start and to slots.
 __global__ __launch_bounds__(PLAN_THREADS) void moe_plan(const int32_t* __restrict__ start, const int32_t* __restrict__ rows,
                                                          const void* __restrict__ sa, int experts, int slots, int a_rows,
                                                          int k, int mx, int bm, int32_t* __restrict__ plan,
@@ -168,6 +173,8 @@ __global__ __launch_bounds__(PLAN_THREADS) void moe_plan(const int32_t* __restri
         }
         tiles += (count[i] + bm - 1) / bm;
     }
+    // at most all of the grid each: a thread's 4 x 2^22 tile rows, 256 times, would pass 2^31
+    tiles = min(tiles, (int)gridDim.x);
     int upto = tiles;                                     // with this thread's
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -182,7 +189,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void moe_plan(const int32_t* __restri
         if (w < wave) upto += sum[w];
         total += sum[w];
     }
-    if (t == 0 && tid == 0) plan[0] = total;
+    if (t == 0 && tid == 0) plan[0] = min(total, (int)gridDim.x);
     if (t >= total) return;
     int at = upto - tiles;
 #pragma unroll

@@ -183,7 +183,9 @@ int64_t moe_route_workspace(int64_t tokens, int64_t experts, int64_t top_k);
  * A        device, E4M3 codes [a_rows, k] (a_rows == slots where rows is NULL)
  * rows     device, int32 [slots], or NULL; a row outside [0, a_rows) stands
  *          for some row inside
- * expert_start  device, int32 [experts + 1], ascending; values are clamped to [0, slots]
+ * expert_start  device, int32 [experts + 1], ascending; values are clamped to [0,
+ *          slots], and an expert's end to its start.  Where they are not ascending,
+ *          slots that several experts claim hold the row of any of them, or none
  * B        device, E4M3 codes [experts, n or 2 n, k]
  * scale_a  fp32 [a_rows] or UE8M0 codes [a_rows, k / 32];  scale_b  [experts, n or 2 n] or [.., k / 32]
  * bias     device, fp32 [experts, n or 2 n], or NULL
