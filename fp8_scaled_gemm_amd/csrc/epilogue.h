@@ -9,7 +9,8 @@ namespace fp8g {
 // v / (1 + exp(-p(v))), p(v) = v (c1 + c3 v^2): SILU has c1 = 1, c3 = 0, and
 // the tanh form of GELU, v (1 + tanh u) / 2 = v / (1 + exp(-2 u)), has
 // c1 = 2 sqrt(2 / pi), c3 = 0.044715 c1.  Held times -log2(e), so that the
-// exponential is one instruction.
+// exponential is one instruction.  Of +inf both are +inf, of -inf and NaN they are NaN,
+// as the formulas are.
 struct Act {
     float c1, c3;
     int32_t on;
@@ -23,7 +24,9 @@ inline Act act_of(int act) {
 }
 
 __device__ __forceinline__ float activate(float v, float c1, float c3) {
-    const float t = v * __builtin_fmaf(c3 * v, v, c1);
+    // finite inside the polynomial: SILU's c3 = 0 times +inf would be NaN
+    const float w = __builtin_fminf(v, 3.40282347e+38f);
+    const float t = v * __builtin_fmaf(c3 * w, w, c1);
     return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t));
 }
 

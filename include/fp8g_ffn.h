@@ -99,7 +99,9 @@ int add_rms_norm_quantize(const void* x, int64_t x_stride, const void* residual,
  * All of it in fp32, one rounding at the end.  Accuracy of z as there; the
  * activation adds (4 + |p|) 2^-22 of |v|, p = z (SILU) or 2 u (GELU_TANH): its
  * exponential and reciprocal are the hardware's, one ulp each, and p's own
- * rounding passes through the exponential.
+ * rounding passes through the exponential.  Where 1 + exp(-p) passes 2^126, the
+ * activation (below 2^-126 |z| in size) may be 0.  Of +inf it is +inf, of -inf and
+ * NaN it is NaN.
  *
  * A        device, E4M3 codes [m, k]      B  device, E4M3 codes [n or 2 n, k]
  * scale_a, scale_b   fp32 [m], [n or 2 n];  mxfp8: UE8M0 codes [.., k / 32]

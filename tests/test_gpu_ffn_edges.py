@@ -12,6 +12,38 @@ from test_gpu_ffn_limits import guarded
 pytestmark = pytest.mark.gpu
 
 
+INF = float("inf")
+
+
+# the row kernel, small and large tiles, and K ranges
+@pytest.mark.parametrize("m,k", [(1, 0), (1, 64), (100, 64), (100, 4096), (600, 128), (3000, 128), (3000, 160)])
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("mx", [False, True])
+def test_activations_of_infinities(gpu_lib, m, k, act, mx):
+    """z = bias alone (codes of zero): act(+inf) = +inf, NaN stays, and the largest finite values are themselves."""
+    z = torch.tensor([INF, -INF, float("nan"), 3.4028234e38, -3.4028234e38, 2.0 ** 64, 0.0, -INF], device="cuda")
+    n = 2200 if k == 128 else 264
+    bias = z.repeat(n // 8)
+    call = gpu_lib.mxfp8_gemm_fused if mx else gpu_lib.fp8_gemm_fused
+    A, B = (torch.zeros(i, k, dtype=torch.uint8, device="cuda") for i in (m, 2 * n))
+    sa, sb = (torch.full((i, k // 32), 127, dtype=torch.uint8, device="cuda") if mx else torch.ones(i, device="cuda") for i in (m, 2 * n))
+    say("infinities", m, k, act, mx)
+    want = torch.tensor([INF, float("nan"), float("nan"), 3.4028234e38, -0.0, 2.0 ** 64, 0.0, float("nan")], device="cuda")
+    for dtype in (torch.float32, torch.bfloat16):
+        got = call(m, n, k, A, B[:n], sa, sb[:n], bias=bias, act=act, out_dtype=dtype)
+        torch.testing.assert_close(got, want.to(dtype).repeat(m, n // 8), rtol=0, atol=0, equal_nan=True)
+        # gated: act(z) times an up projection of 0.5
+        got = call(m, n, k, A, B, sa, sb, bias=torch.cat([bias, torch.full((n,), 0.5, device="cuda")]), act=act, gated=True,
+                   out_dtype=dtype)
+        torch.testing.assert_close(got, (0.5 * want).to(dtype).repeat(m, n // 8), rtol=0, atol=0, equal_nan=True)
+    if m > 1 and k < 4096:
+        start = torch.tensor([0, m // 2, m], dtype=torch.int32, device="cuda")
+        many = (lambda t: torch.stack([t[:n], t[:n]]))                     # noqa: E731
+        moe = gpu_lib.mxfp8_moe_gemm if mx else gpu_lib.fp8_moe_gemm
+        got = moe(A, many(B), sa, many(sb), start, bias=torch.stack([bias, bias]), act=act)
+        torch.testing.assert_close(got, want.to(torch.bfloat16).repeat(m, n // 8), rtol=0, atol=0, equal_nan=True)
+
+
 @pytest.mark.parametrize("starts", ["0 S 0 S", "one step back", "falling"])
 @pytest.mark.parametrize("S,E,n,k", [(3000, 64, 136, 256), (500, 40, 72, 160), (2000, 1024, 40, 32)])
 @pytest.mark.parametrize("mx", [False, True])
