@@ -131,7 +131,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
                 second = larger(larger(second, u), t < top ? t : top);
                 top = larger(top, t);
             }
-            const R value = a.group_top == 2 ? top + second : top;
+            // behind all others without a second one, whatever the first (+inf - inf is NaN)
+            const R value = a.group_top == 1 ? top : second > NEG ? top + second : NEG;
             mine = __shfl(value, lane * lanes & 63, 64);
             if (lane >= a.groups) mine = NEG;
         } else {
@@ -156,7 +157,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
                         second = larger(second, out ? NEG : v[i]);
                         gone = gone || out;
                     }
-                    value = best + wave_most(second);
+                    second = wave_most(second);
+                    value = second > NEG ? best + second : NEG;
                 }
                 if (lane == q) mine = value;
             }

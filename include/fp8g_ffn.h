@@ -141,7 +141,7 @@ int64_t gemm_fused_workspace(int64_t m, int64_t n, int64_t k, int gated, int mx)
  *       ties go to the lowest index, of experts and of groups
  *   weights: p of those experts; renormalize: divided by their sum (0 where
  *       that is 0); times scale
- * An expert whose logit is -inf or NaN is not available; a token with fewer
+ * An expert whose logit or bias is -inf or NaN is not available; a token with fewer
  * than top_k available experts has -1 and weight 0 in the last places (a token
  * whose logits are all -inf, a padded one, goes nowhere).  A group that lacks
  * group_top available experts is behind all that have them.  Logits of +inf share the

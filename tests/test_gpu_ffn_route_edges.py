@@ -38,3 +38,20 @@ def test_close_groups_of_masked_experts(gpu_lib, E, groups, group_top):
     say("masked groups", E, groups, group_top)
     for top_groups in {1, 2, groups - 1}:
         check(gpu_lib, *f32(x), 6, None, score="sigmoid", groups=groups, top_groups=top_groups, group_top=group_top)
+
+
+@pytest.mark.parametrize("E,groups", SIZES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_of_infinity(gpu_lib, E, groups, score):
+    """A bias of +inf puts an expert first, but not its group before those with enough experts."""
+    r = rng(E, groups)
+    width = E // groups
+    x = 2 * r.standard_normal((12, E))
+    bias = 0.1 * r.standard_normal(E)
+    bias[1] = np.inf
+    bias[width + 1:width + 3] = np.inf
+    x[::2, :width] = np.where(np.arange(width) == 1, 0.5, -np.inf)          # group 0: its only expert
+    x[1::4, width:2 * width] = -np.inf
+    say("infinite bias", E, groups, score)
+    for top_groups in {1, groups - 1}:
+        check(gpu_lib, *f32(x), 5, f32(bias)[1], score=score, groups=groups, top_groups=top_groups)
