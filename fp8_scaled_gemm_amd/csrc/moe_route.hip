@@ -42,7 +42,8 @@ constexpr int RT_SUM_RUNS = 64;          // runs whose counts the placing workgr
 // fp32 choices: p from the hardware's exponential and reciprocal (one ulp each, the
 // argument's rounding times an exponent of at most 88 p) and a sum of 1024
 // terms is within 2^-20 of p's range [0, 1]; the bias adds half an ulp of the
-// choice, a group's sum twice all of that.
+// choice, a group's sum twice all of that, by the size of its terms: biases of both
+// signs may leave a small sum of large ones.
 constexpr float RT_MARGIN = 1.0f / (1 << 18);
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
@@ -117,6 +118,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
     if (a.groups > 1) {
         const int width = E / a.groups, lanes = width / VPL;
         R mine = NEG;                                     // lane q: group q's value
+        R size = (R)1;                                    // of the values' largest term (p is at most 1)
+        const auto term = [&](R v) __attribute__((always_inline)) { return v > NEG ? larger(v, -v) : (R)0; };
         if (width % VPL == 0 && (lanes & (lanes - 1)) == 0) {
             // a group is `lanes` neighbouring lanes: all groups at once
             R top = NEG, second = NEG;
@@ -133,6 +136,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
             }
             // behind all others without a second one, whatever the first (+inf - inf is NaN)
             const R value = a.group_top == 1 ? top : second > NEG ? top + second : NEG;
+            if (!exact && a.bias) size = wave_most(larger(term(top), a.group_top == 2 ? term(second) : (R)0));
             mine = __shfl(value, lane * lanes & 63, 64);
             if (lane >= a.groups) mine = NEG;
         } else {
@@ -159,7 +163,9 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
                     }
                     second = wave_most(second);
                     value = second > NEG ? best + second : NEG;
+                    size = larger(size, term(second));
                 }
+                size = larger(size, term(best));
                 if (lane == q) mine = value;
             }
         }
@@ -173,7 +179,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&x)[VPL]
         if (!exact && a.top_groups < a.groups) {
             const R last = -wave_most(in ? -mine : NEG), next = wave_most(lane < a.groups && !in ? mine : NEG);
             // groups without enough experts (NEG) are behind all others for sure
-            clear = next == NEG || last - next > (R)RT_MARGIN * ((R)1 + larger(last, -last));
+            clear = next == NEG || last - next > (R)RT_MARGIN * ((R)1 + size);
         }
 #pragma unroll
         for (int i = 0; i < VPL; i++) {

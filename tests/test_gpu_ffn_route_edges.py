@@ -55,3 +55,18 @@ def test_biases_of_infinity(gpu_lib, E, groups, score):
     say("infinite bias", E, groups, score)
     for top_groups in {1, groups - 1}:
         check(gpu_lib, *f32(x), 5, f32(bias)[1], score=score, groups=groups, top_groups=top_groups)
+
+
+@pytest.mark.parametrize("E,groups", [(16, 8), (60, 20), (256, 32), (1024, 64)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [3.0, 1000.0, 3e5])
+def test_biases_that_cancel(gpu_lib, E, groups, score, size):
+    """Groups whose two best choices are size + p and p - size: their sums are as close as p's fp32 rounding at that size."""
+    r = rng(E, groups, score == "softmax")
+    width = E // groups
+    x = 0.01 * r.standard_normal((200, E))
+    bias = np.full(E, -4.0 * size)
+    bias[::width], bias[1::width] = size, -size
+    say("cancelling biases", E, groups, score, size)
+    for top_groups in (1, groups // 2):
+        check(gpu_lib, *f32(x), 2, f32(bias)[1], score=score, groups=groups, top_groups=top_groups)
