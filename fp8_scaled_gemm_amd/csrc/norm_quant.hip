@@ -60,10 +60,10 @@ __device__ __forceinline__ uint32_t pack_odd(OutE5M2, float a, float b, float c,
     return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(c, d, r, true);
 }
 
-// 1 / sqrt(v): the hardware's root to 2^-26 or so, and one Newton step.  v = 0: infinity.
+// 1 / sqrt(v), v > 0: the hardware's root to 2^-26 or so, and one Newton step.
 __device__ __forceinline__ double inverse_root(double v) {
     const double r = __builtin_amdgcn_rsq(v);
-    return v > 0.0 ? r * (1.5 - 0.5 * v * r * r) : r;
+    return r * (1.5 - 0.5 * v * r * r);
 }
 
 // Waves of a SIMD that the registers of a row are to allow.
@@ -162,9 +162,11 @@ __global__ __launch_bounds__(NORM_THREADS, norm_waves(VPL, Row16<F32>::VEC)) voi
     if ((tid & 63) == 0) red[0][tid >> 6] = ss, red[1][tid >> 6] = most;
     __syncthreads();
     ss = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
-    // a sum that is no finite number: the row's scale says so
-    const bool bad = !(ss <= 1.7976931348623157e308);
-    const double rstd = bad ? __builtin_nan("") : inverse_root(ss * a.inv_cols + (double)a.eps);
+    // a sum that is no finite number, or a mean + eps with no root (a row of zeros and
+    // eps = 0): the row's scale says so
+    const double mean = ss * a.inv_cols + (double)a.eps;
+    const bool bad = !(ss <= 1.7976931348623157e308) || !(mean > 0.0);
+    const double rstd = bad ? __builtin_nan("") : inverse_root(mean);
 
     auto store = [&](int idx, const float* y) __attribute__((always_inline)) {
         if constexpr (VEC == 8)

@@ -65,8 +65,9 @@ typedef enum {
  * scale, norm and codes.  A scale of 0 gives
  * signed zeros.
  * A row whose sum of squares is no finite number (it holds a NaN or an
- * infinity) has codes 0 with the scale NaN (MX: codes 255), and NaN in norm;
- * the others are not touched by it.
+ * infinity), or whose mean square + eps is not above 0 (zeros with eps = 0), has
+ * codes 0 with the scale NaN (MX: codes 255), and NaN in norm; the others are not
+ * touched by it.
  *
  * x        device, [rows, cols] of in_dtype (fp8g_in_t), rows x_stride elements apart
  * residual device, the same type, rows residual_stride elements apart, or NULL

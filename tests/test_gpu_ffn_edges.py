@@ -82,3 +82,24 @@ def test_starts_that_are_not_ascending_stay_inside(gpu_lib, starts, S, E, n, k, 
     assert not written[claims == 0].any()
     if starts == "falling":
         assert not written.any()
+
+
+@pytest.mark.parametrize("mode", ["row", "row_e5m2", "mx"])
+@pytest.mark.parametrize("cols", [64, 4096, 20000])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_without_a_norm(gpu_lib, mode, cols, dtype):
+    """0 / sqrt(0 + 0), and roots of negative numbers and NaN: codes 0, a scale of NaN; other rows keep their own."""
+    x = torch.randn(5, cols, generator=torch.Generator(device="cuda").manual_seed(cols), device="cuda").to(dtype)
+    x[0], x[3, ::2], x[3, 1::2] = 0.0, -0.0, 0.0
+    how = {"mx": mode == "mx", "fmt": 1 if mode == "row_e5m2" else 0}
+    for eps, bad in ((0.0, (0, 3)), (-1e-3, (0, 3)), (float("nan"), range(5)), (-1e9, range(5))):
+        say("no norm", mode, cols, dtype, eps)
+        got = gpu_lib.add_rms_norm_quantize(x, eps=eps, return_norm=True, **how)
+        for t in range(5):
+            if t in bad:
+                assert (got.q[t].view(torch.uint8) == 0).all() and torch.isnan(got.norm[t]).all()
+                assert (got.scale[t] == 255).all() if mode == "mx" else torch.isnan(got.scale[t])
+            else:
+                same = gpu_lib.add_rms_norm_quantize(x[t:t + 1], eps=eps, return_norm=True, **how)
+                assert torch.equal(got.q[t].view(torch.uint8), same.q[0].view(torch.uint8)) and torch.equal(got.scale[t], same.scale[0])
+                assert torch.isfinite(got.norm[t]).all()
