@@ -52,7 +52,7 @@ int fused(int64_t m, int64_t n, int64_t k, int64_t experts, const uint8_t* A, in
     FusedArgs a = {A, B, sa, sb, bias, residual, D, rows, moe ? start : nullptr, ws, m, n, k, a_rows, products, act,
                    gated != 0, mx, out_dtype == FP8G_OUT_F32};
     const int64_t need = moe ? moe_gemm_bytes(a) : gemm_fused_bytes(a);
-    if (ws_bytes < need) return FP8G_ERR_UNSUPPORTED;
+    if (ws_bytes < need || (moe && !moe_gemm_fits(a))) return FP8G_ERR_UNSUPPORTED;
     if ((ab > 0 && !A) || (bb > 0 && !B) || (sab > 0 && !sa) || (sbb > 0 && !sb) || !D || (moe && !start) ||
         (need > 0 && !ws))
         return FP8G_ERR_NULL;
@@ -151,7 +151,8 @@ int64_t moe_gemm_workspace(int64_t slots, int64_t n, int64_t k, int64_t experts,
     a.m = slots, a.n = n, a.k = k, a.experts = experts, a.gated = gated != 0, a.mx = mx != 0;
     a.rows = gathered ? &some : nullptr;
     a.expert_start = &some;
-    return slots && n && experts ? moe_gemm_bytes(a) : 0;
+    if (!slots || !n || !experts) return 0;
+    return moe_gemm_fits(a) ? moe_gemm_bytes(a) : -1;
 }
 
 int fp8_moe_gemm(int64_t slots, int64_t n, int64_t k, int64_t experts, const uint8_t* A, int64_t a_rows,

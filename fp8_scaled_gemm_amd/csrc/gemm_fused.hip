@@ -408,6 +408,8 @@ static int moe_tile(const FusedArgs& a) {
     return best;
 }
 
+bool moe_gemm_fits(const FusedArgs& a) { return !few_rows(a) || gemm_rows_fits(a); }
+
 struct MoeSpace {
     int64_t tile_rows, row_at, scale, scale_b, bytes;      // byte offsets; the plan comes first
 };

@@ -289,16 +289,28 @@ __global__ __launch_bounds__(RW_THREADS, WPE) void gemm_rows_kernel(RowsArgs arg
     }
 }
 
+constexpr int64_t RW_GROUPS = ((int64_t)1 << 32) / RW_THREADS;      // of a launch, fewer than this
+
+// two workgroups share an expert's blocks of rows, should it have several: 200 rows
+// of 128 experts, 2 x 1024 x 2048, in four of them 36 -> 25 us; spread evenly 89 both
+static unsigned row_shares(const FusedArgs& f, int mb) { return f.expert_start && f.m > 16 * mb ? 2 : 1; }
+
+// Experts have a workgroup for every 16 (gated) or 32 columns of each.
+bool gemm_rows_fits(const FusedArgs& f) {
+    const int64_t cols = f.gated ? 16 : 32;
+    return !f.expert_start || (f.n + cols - 1) / cols * f.experts * row_shares(f, 1) < RW_GROUPS;
+}
+
 template <bool MX, bool GATED, int NB, int MB, int AHEAD, int WPE>
 static hipError_t launch_one_rows(const FusedArgs& f, hipStream_t stream) {
     constexpr int COLS = GATED ? 8 * NB : 16 * NB;
     const int64_t gx = (f.n + COLS - 1) / COLS;
     int64_t gy = f.expert_start ? f.experts : (f.m + 16 * MB - 1) / (16 * MB);
     if (gy > 65535) gy = 65535;
+    // a workgroup of one product goes round as many blocks of rows as are left
+    if (!f.expert_start && gx * gy >= RW_GROUPS) gy = (RW_GROUPS - 1) / gx;
     RowsArgs args{f, act_of(f.act)};
-    // two workgroups share an expert's blocks of rows, should it have several: 200 rows
-    // of 128 experts, 2 x 1024 x 2048, in four of them 36 -> 25 us; spread evenly 89 both
-    const unsigned gz = f.expert_start && f.m > 16 * MB ? 2 : 1;
+    const unsigned gz = row_shares(f, MB);
     const dim3 grid((unsigned)gx, (unsigned)gy, gz), threads(RW_THREADS);
     if constexpr (MX) {
         const int64_t lds = (int64_t)scale_pitch((int)(f.k / 32)) * 16 * (NB + MB);

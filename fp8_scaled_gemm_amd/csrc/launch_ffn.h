@@ -34,8 +34,10 @@ struct FusedArgs {
 };
 int64_t gemm_fused_bytes(const FusedArgs& a);
 int64_t moe_gemm_bytes(const FusedArgs& a);
+bool moe_gemm_fits(const FusedArgs& a);
 hipError_t launch_gemm_fused(const FusedArgs& a, hipStream_t stream);
 hipError_t launch_gemm_rows(const FusedArgs& a, hipStream_t stream);      // few rows, no workspace
+bool gemm_rows_fits(const FusedArgs& a);
 
 // A launch of the tile kernel; for the experts' products with its plan (gemm_tile.h).
 struct TileLaunch {

@@ -7,7 +7,7 @@ import torch
 from block_util import rng
 from ffn_util import dev, operand
 from gpu_util import say
-from test_gpu_ffn_limits import guarded
+from test_gpu_ffn_limits import guarded, same_but_for_a_step
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +103,21 @@ def test_rows_without_a_norm(gpu_lib, mode, cols, dtype):
                 same = gpu_lib.add_rms_norm_quantize(x[t:t + 1], eps=eps, return_norm=True, **how)
                 assert torch.equal(got.q[t].view(torch.uint8), same.q[0].view(torch.uint8)) and torch.equal(got.scale[t], same.scale[0])
                 assert torch.isfinite(got.norm[t]).all()
+
+
+def test_more_blocks_of_rows_than_a_launch_holds(gpu_lib):
+    """2^35 outputs of one K step on the row kernel, 32 columns x 64 rows a workgroup: 2^24 workgroups of 256
+    threads would be 2^32 threads, so that some go round twice."""
+    m, n, k = 1 << 15, 1 << 20, 16
+    r = rng(35)
+    A, sa = operand(r, 64, k, False)
+    B, sb = operand(r, n, k, False)
+    A, sa, B, sb = dev(A), dev(sa), dev(B), dev(sb)
+    say("row kernel", m, n, k)
+    D = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device="cuda")               # 69 GB
+    gpu_lib.fp8_gemm_fused(m, n, k, A.repeat(m // 64, 1), B, sa.repeat(m // 64), sb, D=D)
+    for at in range(64, m, 64):
+        assert torch.equal(D[at:at + 64], D[:64]), at
+    for at in (0, n - 5000):
+        want = gpu_lib.fp8_gemm_fused(64, 5000, k, A, B[at:at + 5000], sa, sb[at:at + 5000])
+        same_but_for_a_step(D[:64, at:at + 5000], want)
