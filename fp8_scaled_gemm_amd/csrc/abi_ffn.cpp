@@ -79,6 +79,7 @@ RouteArgs route_sizes(int64_t tokens, int64_t experts, int64_t top_k) {
 int check_route_sizes(int64_t tokens, int64_t experts, int64_t top_k) {
     if (tokens < 0 || experts < 1 || top_k < 1 || top_k > experts) return FP8G_ERR_SHAPE;
     if (experts > MAX_EXPERTS || top_k > 32 || tokens >= LIM28 || tokens * top_k >= LIM28) return FP8G_ERR_UNSUPPORTED;
+    if (!moe_route_fits(route_sizes(tokens, experts, top_k))) return FP8G_ERR_UNSUPPORTED;
     return FP8G_OK;
 }
 

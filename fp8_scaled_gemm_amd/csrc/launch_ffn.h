@@ -56,6 +56,7 @@ struct RouteArgs {
     int32_t tokens, experts, top_k, groups, top_groups, group_top, sigmoid, renormalize;
     float scale;
 };
+bool moe_route_fits(const RouteArgs& a);
 int64_t moe_route_bytes(const RouteArgs& a);
 hipError_t launch_moe_route(const RouteArgs& a, int f32, hipStream_t stream);
 

@@ -499,6 +499,9 @@ static RoutePlan route_plan(const RouteArgs& a) {
     return {run, (a.tokens + run - 1) / run};
 }
 
+// A run's workgroup has up to 1024 threads; the other launches have fewer.
+bool moe_route_fits(const RouteArgs& a) { return route_plan(a).runs < ((int64_t)1 << 32) / 1024; }
+
 int64_t moe_route_bytes(const RouteArgs& a) {
     const RoutePlan p = route_plan(a);
     return p.runs ? ((int64_t)p.runs + 1) * a.experts * 4 : 0;
