@@ -24,6 +24,7 @@
 // (SC_LDS): fetched by the step they are a load each for a byte a lane, half as
 // many again as the operands' (64 experts of 2 x 1408 x 4096, 6 rows: 168 us so).
 
+#include <atomic>
 #include <type_traits>
 
 #include "epilogue.h"
@@ -53,7 +54,7 @@ struct RowsArgs {
 // Bytes between the scale rows in LDS: whole 16 bytes, an odd number of them, so
 // that the 16 rows of a read lie in different banks.
 __host__ __device__ constexpr int scale_pitch(int nblk) { return ((nblk + 15) / 16 | 1) * 16; }
-constexpr int SC_LIMIT = 40 * 1024;       // of a workgroup: four on a CU beside their sums
+constexpr int SC_LIMIT = 40 * 1024;       // of a workgroup, beside 4 to 32 KB of sums: two or three on a CU at least
 
 // B's rows of a workgroup: NB blocks of 16; gated: the first half of them the
 // gate's, the others the up projection's.  MB: blocks of 16 rows of A.  AHEAD:
@@ -315,7 +316,22 @@ static hipError_t launch_one_rows(const FusedArgs& f, hipStream_t stream) {
     if constexpr (MX) {
         const int64_t lds = (int64_t)scale_pitch((int)(f.k / 32)) * 16 * (NB + MB);
         if (lds <= SC_LIMIT && f.k > 0) {
-            gemm_rows_kernel<true, true, GATED, NB, MB, AHEAD, WPE><<<grid, threads, (unsigned)lds, stream>>>(args);
+            auto kern = gemm_rows_kernel<true, true, GATED, NB, MB, AHEAD, WPE>;
+            // with the sums above the default launch limit: raised once per device; setting
+            // it twice from racing threads is harmless
+            if constexpr (RW_WAVES * NB * MB * 64 * (int)sizeof(v4f) + SC_LIMIT > 64 * 1024) {
+                static std::atomic<uint64_t> configured{0};
+                int dev = 0;
+                hipError_t e = hipGetDevice(&dev);
+                if (e != hipSuccess) return e;
+                const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+                if (!bit || !(configured.load(std::memory_order_acquire) & bit)) {
+                    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, SC_LIMIT);
+                    if (e != hipSuccess) return e;
+                    configured.fetch_or(bit, std::memory_order_release);
+                }
+            }
+            kern<<<grid, threads, (unsigned)lds, stream>>>(args);
             return hipGetLastError();
         }
     }
