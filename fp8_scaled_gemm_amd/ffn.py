@@ -98,19 +98,20 @@ def moe_route_workspace(tokens, experts, top_k):
     return _bytes(load().moe_route_workspace(tokens, experts, top_k), "moe_route_workspace")
 
 
-def moe_route(logits, top_k, bias=None, score="softmax", groups=1, top_groups=1, group_top=2, renormalize=True, scale=1.0,
+def moe_route(logits, top_k, bias=None, score="softmax", groups=1, top_groups=1, group_top=None, renormalize=True, scale=1.0,
               workspace=None):
     """The top_k experts of every token of logits [T, E] (bfloat16 or float32),
     by score "softmax" or "sigmoid" plus bias [E] float32 (for the choice only),
     among the top_groups of `groups` groups of experts with the largest sum of
-    their group_top best.  Weights are the scores, divided by their sum with
-    renormalize, times scale.  Experts with a logit of -inf are not available.
+    their group_top best (1 or 2; None: 2, or 1 where groups is 1).  Weights are
+    the scores, divided by their sum with renormalize, times scale.  Experts with a
+    logit or bias of -inf are not available.
 
     Returns MoeRoute(ids, weights, expert_start, rows, slots).  workspace: a
     device tensor to use instead of a fresh one (moe_route_workspace bytes).
     """
-    if groups == 1:
-        top_groups = group_top = 1
+    if group_top is None:
+        group_top = 1 if groups == 1 else 2
     return MoeRoute(*_done(_block().moe_route(logits, top_k, bias, _choice(_SCORES, score, "score"), groups, top_groups, group_top,
                                               renormalize, scale, workspace), "moe_route"))
 

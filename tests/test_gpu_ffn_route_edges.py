@@ -3,6 +3,7 @@ groups have few available experts: the definition, token by token."""
 
 import numpy as np
 import pytest
+import torch
 
 from block_util import f32, rng
 from gpu_util import say
@@ -70,3 +71,16 @@ def test_biases_that_cancel(gpu_lib, E, groups, score, size):
     say("cancelling biases", E, groups, score, size)
     for top_groups in (1, groups // 2):
         check(gpu_lib, *f32(x), 2, f32(bias)[1], score=score, groups=groups, top_groups=top_groups)
+
+
+def test_groups_that_are_refused(gpu_lib):
+    """One group has no other to choose from; None stands for a group_top that fits."""
+    x = torch.randn(3, 8, device="cuda")
+    want = gpu_lib.moe_route(x, 2)
+    for how in ({"groups": 1, "top_groups": 1}, {"group_top": 1}, {"group_top": 2}):
+        assert all(torch.equal(a, b) for a, b in zip(gpu_lib.moe_route(x, 2, **how), want)), how
+    gpu_lib.moe_route(x[:, :1].contiguous(), 1)
+    for how in ({"top_groups": 2}, {"top_groups": 0}, {"group_top": 3}, {"group_top": 0}, {"groups": 4, "top_groups": 5},
+                {"groups": 8, "group_top": 2}, {"groups": 3}):
+        with pytest.raises(gpu_lib.Fp8gError):
+            gpu_lib.moe_route(x, 2, **how)
