@@ -44,26 +44,9 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, v);
 }
 
-// The MXFP8 exponent of a block: the smallest e with amax <= 448 * 2^e, in
-// [-127, 127] (-127 for a block of zeros).
-__device__ __forceinline__ int mx_exponent(float amax) {
-    const uint32_t u0 = __builtin_bit_cast(uint32_t, amax);
-    const bool sub = (u0 >> 23) == 0;                          // zero or subnormal
-    const uint32_t u = sub ? __builtin_bit_cast(uint32_t, amax * 16777216.0f) : u0;
-    const int E = (int)(u >> 23) - 127 - (sub ? 24 : 0);
-    const int e = E - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return u0 == 0 ? -127 : min(max(e, -127), 127);
-}
-
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, off, 64));
-    return v;
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
     return v;
 }
 

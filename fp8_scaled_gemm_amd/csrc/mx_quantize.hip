@@ -28,6 +28,15 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 constexpr int MX_UNROLL = 4;         // float4 loads in flight per lane and iteration
 constexpr int MX_THREADS = 256;
 
+__device__ __forceinline__ int mx_exponent(float amax) {
+    const uint32_t u0 = __builtin_bit_cast(uint32_t, amax);
+    const bool sub = (u0 >> 23) == 0;                          // zero or subnormal
+    const uint32_t u = sub ? __builtin_bit_cast(uint32_t, amax * 16777216.0f) : u0;
+    const int E = (int)(u >> 23) - 127 - (sub ? 24 : 0);
+    const int e = E - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return u0 == 0 ? -127 : min(max(e, -127), 127);
+}
+
 __global__ __launch_bounds__(MX_THREADS) void quantize_mx_kernel(const v4f* __restrict__ x, int64_t nvec,
                                                                   uint32_t* __restrict__ q, uint8_t* __restrict__ sc) {
     const int tid = threadIdx.x;
