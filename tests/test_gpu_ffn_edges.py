@@ -4,9 +4,10 @@ import numpy as np
 import pytest
 import torch
 
-from block_util import rng
+from block_util import close, host, rng
 from ffn_util import dev, operand
 from gpu_util import say
+from oracle import ffn
 from test_gpu_ffn_gemm import case
 from test_gpu_ffn_limits import guarded, same_but_for_a_step
 
@@ -43,6 +44,22 @@ def test_activations_of_infinities(gpu_lib, m, k, act, mx):
         moe = gpu_lib.mxfp8_moe_gemm if mx else gpu_lib.fp8_moe_gemm
         got = moe(A, many(B), sa, many(sb), start, bias=torch.stack([bias, bias]), act=act)
         torch.testing.assert_close(got, want.to(torch.bfloat16).repeat(m, n // 8), rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_activations_of_every_size(gpu_lib, act):
+    """Powers of two and their neighbours of both signs, over fp32's range."""
+    z = 2.0 ** np.arange(-126, 128)
+    z = np.concatenate([z, 1.5 * z, z * (1 + 2.0 ** -23), z * (2 - 2.0 ** -23)]).astype(np.float32)
+    z = np.concatenate([z, -z])
+    n = len(z)
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    got = gpu_lib.fp8_gemm_fused(1, n, 0, none.view(1, 0), none.view(n, 0), dev(np.ones(1, np.float32)), dev(np.ones(n, np.float32)),
+                                 bias=dev(z), act=act, out_dtype=torch.float32)
+    z = z.astype(np.float64)
+    v, own = ffn.activate(z, act)
+    # where 1 + exp(-p) passes 2^126 the result may be 0, and below the smallest normal the rounding is absolute
+    close(host(got)[0], v, own + 2.0 ** -24 * np.abs(v) + 2.0 ** -126 * np.maximum(1, np.where(z < -8, -z, 0)), act)
 
 
 @pytest.mark.parametrize("starts", ["0 S 0 S", "one step back", "falling"])
