@@ -374,9 +374,22 @@ __global__ __launch_bounds__(FIN_THREADS) void fused_finish(FinishArgs x) {
 }
 
 // ---- the experts' products.  Up to this many rows an expert on average the
-// row kernel reads the weights faster (64 experts of 2 x 1408 x 4096, 6 rows:
-// 131 us against 144 on 64x128 tiles); above, the experts of many rows make it
-// read them again for every 16, and tiles win whatever the spread.
+// row kernel reads the weights faster; above, experts of many rows make it read
+// theirs again for every 16.  Row kernel / tiles in us, rows spread evenly, and in
+// brackets unevenly (the fullest expert has 4 to 14 times the average):
+//                                     4 rows            6                 8                 12                16
+//   (a) 64 x 2 x 1408 x 4096    136 / 151         139 / 152         142 / 152         145 / 155         153 / 155
+//                              (117 / 132)       (119 / 132)       (143 / 137)       (175 / 156)       (211 / 155)
+//       60 x 2048 x 1408         36 / 43           37 / 43           38 / 43           42 / 43           45 / 43
+//                               (33 / 34)         (37 / 42)         (48 / 42)         (53 / 42)         (67 / 42)
+//       128 x 2 x 1024 x 2048    96 / 105          97 / 106         101 / 105         109 / 107         118 / 107
+//                               (81 / 91)         (93 / 93)        (111 / 105)       (152 / 105)       (154 / 105)
+//   (b) 64 x 2 x 1408 x 4096    137 / 195         139 / 195         141 / 196         148 / 197         160 / 197
+//                              (119 / 162)       (143 / 197)       (155 / 197)       (183 / 202)       (227 / 205)
+//       60 x 2048 x 1408         40 / 53           40 / 53           42 / 53           44 / 53           47 / 53
+//                               (36 / 51)         (39 / 52)         (53 / 53)         (53 / 53)         (79 / 55)
+// The bound is mode (a)'s with uneven experts; mode (b), which has no 64x128 tiles,
+// would still gain up to about 10 rows.
 constexpr int64_t FEW_ROWS_EXPERT = 6;
 static bool few_rows(const FusedArgs& a) { return a.m <= FEW_ROWS_EXPERT * a.experts; }
 

@@ -343,7 +343,8 @@ static hipError_t launch_one_rows(const FusedArgs& f, hipStream_t stream) {
 // TB/s); the same with one column block less in flight or eight waves 40 to 65 us.
 // Plain products of few column blocks (below 512 workgroups of 32 columns) take 16
 // columns a workgroup and four steps in flight, wider ones 32 and one.  More rows than
-// 16 come in blocks of 32 or 64, where registers allow two waves of a SIMD.
+// 16 come in blocks of 32 or 64, where registers allow two waves of a SIMD (one
+// product only: experts come here with few rows on average, see gemm_fused.hip).
 template <bool MX, bool GATED>
 static hipError_t launch_rows(const FusedArgs& f, hipStream_t stream) {
     const int64_t rows = f.expert_start ? (f.m + f.experts - 1) / f.experts : f.m;   // of a product, on average

@@ -12,10 +12,10 @@
 // error (RT_MARGIN); a token with a closer one (about one in a thousand) is gone
 // through again in fp64.  Weights always come from fp64.
 //
-// Bound by the vector instructions of a token (some 400, most of them in the
-// rounds), not by its bytes; a run of tokens has 16 waves, four on a SIMD.  16384
-// tokens, 8 of 256 experts in 8 groups, sigmoid with bias: 33 us, and 9 us for the order;
-// one token 4.4 us.
+// Bound by the vector instructions of a token (680 of them, most in the rounds, each
+// of which waits for the one before), not by its bytes; a run of tokens has 16
+// waves, four on a SIMD.  16384 tokens, 8 of 256 experts in 8 groups, sigmoid with
+// bias: 34 us, and 10 us for the order; without groups 27 us in all; one token 4.3 us.
 //
 // The rows are sorted by counting, stably and with no result that hangs on an
 // order: a run of at most 64 tokens sets bit t of its experts' 64-bit masks in

@@ -88,7 +88,10 @@ class MoeRoute(collections.namedtuple("MoeRoute", "ids weights expert_start rows
     """Experts ids [T, k] of every token (-1: none) and their weights [T, k]; the
     routed rows sorted by expert: expert e has the slots expert_start[e] ..
     expert_start[e + 1] - 1, rows[slot] is a slot's token and slots[t, j] the
-    slot of token t's j-th expert (-1: none)."""
+    slot of token t's j-th expert (-1: none).
+
+    The five are parts of one allocation, which stays as long as one of them is
+    kept, and which torch.save writes whole: clone() what outlives the step."""
 
     __slots__ = ()
 

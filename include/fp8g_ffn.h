@@ -110,8 +110,10 @@ int add_rms_norm_quantize(const void* x, int64_t x_stride, const void* residual,
  * act      fp8g_act_t
  * residual device, [m, n] of out_dtype, or NULL; may be D itself
  * D        device, [m, n] of out_dtype (fp8g_out_t), written
- * workspace  device, for the partial sums of products whose K is split (few
- *          tiles and a long K); at most 64 MB
+ * workspace  device, gemm_fused_workspace bytes: the partial sums of products
+ *          whose K is split (few tiles and a long K; at most 16 MB), and with
+ *          block scales and k % 128 != 0 also copies of both operands' scale rows
+ *          in whole dwords, (m + rows of B) * 4 * ceil(k / 128) bytes
  * m == 0 or n == 0: no-op.  k == 0: the product is 0.
  * Limits and contract as fp8_gemm_scaled / mxfp8_gemm, with n or 2 n rows of B
  * below 2^22 (bf16 output) / 2^21 (fp32); a workspace smaller than
