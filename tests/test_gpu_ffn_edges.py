@@ -141,9 +141,9 @@ def test_more_blocks_of_rows_than_a_launch_holds(gpu_lib):
         same_but_for_a_step(D[:64, at:at + 5000], want)
 
 
-@pytest.mark.parametrize("m,k", [(33, 11264), (48, 11008), (64, 10784), (48, 12288), (17, 16384), (5, 24576)])
+@pytest.mark.parametrize("m,k", [(33, 11264), (48, 12288), (64, 10784), (17, 16384)])
 def test_block_scales_and_sums_past_64_kb(gpu_lib, m, k):
-    """The row kernel's largest LDS: 32 KB of sums beside up to 40 KB of block scales (the last two: less of one)."""
+    """The row kernel's largest LDS: 32 KB of sums beside up to 40 KB of block scales (the last: less of one)."""
     n = 2624 if k == 12288 else 2112
     assert gpu_lib.gemm_fused_workspace(m, n, k, True, True) == 0                           # K is not split
     case(gpu_lib, m, n, k, True, "silu", True, bias=True, residual=True, dtype=torch.bfloat16)
